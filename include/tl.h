@@ -52,9 +52,11 @@ typedef enum tl_status {
 typedef enum tl_kv_dtype {
   TL_KV_FP16 = 0,  /* K and V as fp16 */
   TL_KV_INT8 = 1,  /* int8 codes + one fp16 scale per (token, head) */
-  TL_KV_H = 2      /* store-h: the fp16 input rows x of each block application;
+  TL_KV_H = 2,     /* store-h: the fp16 input rows x of each block application;
                     * K and V are rebuilt from them at every decode step (see
                     * tl_kv_create) */
+  TL_KV_INT4 = 3   /* 4-bit codes + an fp16 scale and zero point per group of 32
+                    * values (see tl_kv_int4) */
 } tl_kv_dtype;
 
 /* Description of the last failure on this thread ("" if none). */
@@ -140,6 +142,84 @@ tl_status tl_unpack_codes(const uint32_t* packed, int N, int K, int bits,
  * Requirements: rows >= 0, 1 <= hd <= 256. */
 tl_status tl_kv_quant_int8(const uint16_t* x, int rows, int hd, int8_t* codes,
                            uint16_t* scales, tl_stream stream);
+
+/* ------------------------------------------------------------------------
+ * 4-bit KV cache.  A K or V row of one (token, head) is held in groups of 32
+ * consecutive values, each with an fp16 scale and an fp16 zero point (the
+ * pages' caches stop at 8 bits: "Performance and Memory", "KV cache INT8"; their
+ * 4-bit mode stores hidden states, "Current Status", KV cache mode table,
+ * Store-h (INT4)).  For a group of fp16 values x with least value lo and
+ * largest hi, all steps in IEEE fp32:
+ *   scale = fp16, rounded towards zero, of (hi - lo) / 15;   zero = lo
+ *   code  = clamp(rint((x - lo) * (1 / scale)), 0, 15), scale == 0 gives 0
+ * (difference, reciprocal and product each rounded; rint ties to even).  The
+ * value held is zero + code * scale, within [lo, hi].  A group with a NaN or an
+ * infinity gets NaN scale and zero and codes 0.
+ * Layout of one lane: codes uint32 [n_heads][max_ctx][head_dim / 8] (word j of a
+ * row holds elements 8j .. 8j + 7, element 8j + i in bits 4i .. 4i + 3) and
+ * parameters fp16 [n_heads][max_ctx][head_dim / 32][2] (scale, zero), for K and
+ * for V: head_dim * 5 / 8 bytes per row, 31 % of fp16.  A TL_KV_INT4 layer of a
+ * tl_kv holds one lane in this layout (tl_kv_layer_ptrs).
+ *
+ * The calls below take caller's memory: any number of lanes, head counts that
+ * need not be a model's.  They allocate nothing, keep nothing and may be
+ * captured into CUDA graphs; calls on the same lanes must be ordered by
+ * streams, as for any memory.
+ * ------------------------------------------------------------------------ */
+typedef struct tl_kv_int4 {
+  uint32_t* k_codes;    /* device, 16-byte aligned, lane b at k_codes + b * code_stride */
+  uint32_t* v_codes;
+  uint32_t* k_params;   /* device, (scale, zero) pairs, scale in the low half; */
+  uint32_t* v_params;   /*   lane b at k_params + b * param_stride */
+  size_t code_stride;   /* uint32 words between lanes, a multiple of 4 */
+  size_t param_stride;  /* pairs between lanes */
+  int n_lanes;          /* 0 .. 65535 */
+  int n_heads;          /* 1 .. 256 */
+  int head_dim;         /* 64 or 128 */
+  int max_ctx;          /* 1 .. 2^24 */
+} tl_kv_int4;
+
+/* Quantise a batch of K and V rows into the lanes' caches.  Packed rows
+ * cu[b] .. cu[b + 1] - 1 go to lane b at positions pos[b], pos[b] + 1, ...; a
+ * lane may have none.  Rows behind cu[n_lanes] (or before cu[0]) and rows whose
+ * position lies outside [0, max_ctx) are not written, nor is any other entry.
+ *   k, v        device fp16 [n_rows][row_stride], head h in columns
+ *               [h * head_dim, (h + 1) * head_dim): contiguous rows or column
+ *               slices of a fused projection; K as it is to be attended (after
+ *               RoPE)
+ *   cu          device int32 [n_lanes + 1], ascending, or NULL: the lanes share
+ *               the rows equally (n_rows a multiple of n_lanes)
+ *   pos         device int32 [n_lanes]
+ * Requirements: k and v 16-byte aligned, row_stride >= n_heads * head_dim and a
+ * multiple of 8. */
+tl_status tl_kv_write_int4(const tl_kv_int4* cache, const uint16_t* k, const uint16_t* v,
+                           long row_stride, const int32_t* cu, const int32_t* pos, int n_rows,
+                           tl_stream stream);
+
+/* The reverse: the values of those positions as fp16 rows (each value rounded
+ * once).  Rows that tl_kv_write_int4 would not write are left as they were. */
+tl_status tl_kv_read_int4(const tl_kv_int4* cache, uint16_t* k, uint16_t* v, long row_stride,
+                          const int32_t* cu, const int32_t* pos, int n_rows, tl_stream stream);
+
+/* Attention of the last n_q tokens of every lane over its cache: query i of lane
+ * b sits at position P = lens[b] - n_q + i (its own entry included in the
+ * cache) and sees positions max(0, P - window + 1) .. P (window 0: all of them):
+ *   out = sum_j softmax_j(q . k_j / sqrt(head_dim)) v_j
+ * Query head h reads cache head h / (q_heads / n_heads).  A query with P < 0
+ * sees nothing and gets zeros.  What a query does not see has no effect on it,
+ * NaN included.  Scores, maxima, exponentials and sums in fp32; softmax weights
+ * and values enter the products as fp16; out is rounded to fp16.  A query's
+ * result does not depend on the contents of other lanes.
+ *   q      device fp16 [n_lanes * n_q][q_stride], row b * n_q + i, head h at
+ *          column h * head_dim
+ *   lens   device int32 [n_lanes]: positions that hold entries, the queries' own
+ *          included; values above max_ctx count as max_ctx
+ *   out    device fp16 [n_lanes * n_q][out_stride] (must not overlap q)
+ * Requirements: 0 <= n_q <= 8, q_heads a multiple of n_heads (at most 1024), q and
+ * out 16-byte aligned, strides multiples of 8 and at least q_heads * head_dim. */
+tl_status tl_attention_int4(const tl_kv_int4* cache, const uint16_t* q, long q_stride, int n_q,
+                            int q_heads, const int32_t* lens, int window, uint16_t* out,
+                            long out_stride, tl_stream stream);
 
 /* Causal self-attention of a prefill (test hook): the block's attention step
  * on its own, with the kernel the block's prefill uses (a tiled kernel with an
@@ -313,7 +393,8 @@ tl_status tl_loops_used(tl_model* model, int* loops, int n, tl_stream stream);
  * each lane b, for each layer l < n_pre + L_b: K [H][max_ctx][hd], V
  * [H][max_ctx][hd] (fp16, or int8 codes), then for INT8 the scales K
  * [H][max_ctx], V [H][max_ctx] (fp16); every region starts on 256 bytes.
- * K is stored after RoPE.
+ * K is stored after RoPE.  TL_KV_INT4: K codes, V codes, K parameters, V
+ * parameters, each one lane of the layout tl_kv_int4 describes.
  *
  * TL_KV_H (store-h: "Current Status", KV cache mode table, Store-h (FP16) and
  * tensor-core reconstruction rows; "Claims & Data Sources", h-mode KV
@@ -333,7 +414,8 @@ typedef struct tl_kv tl_kv;
 
 /* Bytes of one (lane, layer) slot: 2 * align256(H * max_ctx * hd * elem)
  * plus, for INT8, 2 * align256(H * max_ctx * 2) of fp16 scales; for TL_KV_H
- * align256(max_ctx * H * hd * 2).  Host-only. */
+ * align256(max_ctx * H * hd * 2); for TL_KV_INT4 2 * align256(H * max_ctx * hd /
+ * 2) + 2 * align256(H * max_ctx * hd / 8) (hd a multiple of 32).  Host-only. */
 tl_status tl_kv_layer_bytes(int n_heads, int head_dim, int max_ctx, tl_kv_dtype dtype,
                             size_t* bytes);
 
@@ -366,7 +448,8 @@ tl_status tl_kv_position(const tl_kv* kv, int lane, int* pos);
  * cache filled by the caller through tl_kv_layer_ptrs). */
 tl_status tl_kv_set_position(tl_kv* kv, int lane, int pos, tl_stream stream);
 /* Device pointers of one (lane, layer) slot: K, V ([H][max_ctx][hd]) and, for
- * INT8, the scales ([H][max_ctx]; NULL for FP16).  TL_KV_H: *k receives the
+ * INT8, the scales ([H][max_ctx]; NULL for FP16), for TL_KV_INT4 the codes and
+ * the parameter pairs.  TL_KV_H: *k receives the
  * fp16 rows x [max_ctx][d]; *v and the scales are NULL. */
 tl_status tl_kv_layer_ptrs(const tl_kv* kv, int lane, int layer, void** k,
                            void** v, uint16_t** k_scale, uint16_t** v_scale);
@@ -433,6 +516,35 @@ tl_status tl_extend(tl_model* model, tl_kv* kv, int lane, const int32_t* ids,
  * Requirements: an embedding in the model, 1 <= n <= 8. */
 tl_status tl_greedy_head(tl_model* model, const float* y, int n, int32_t* ids,
                          tl_stream stream);
+
+/* Scoring head over an embedding used as output head (the model's tied
+ * embedding, or any [vocab, d] fp16 matrix): for each row r with logits
+ * z[v] = y[r] . E[v] and lse = log sum_v exp(z[v])
+ *   logp[r]       = z[targets[r]] - lse;  0 for a negative target (no token),
+ *                   NaN for a target >= vocab
+ *   entropy[r]    = lse - sum_v exp(z[v] - lse) z[v]   (nats)
+ *   top_ids[r][i], top_logp[r][i] = the k most probable tokens, most probable
+ *                   first, the lowest id first among equal logits, and their log
+ *                   probabilities
+ * The logits are not stored.  y enters the products as two fp16 parts (22 bits);
+ * sums are fp32; the given token's logit and the order of the best are decided
+ * by fp64 dot products of the inputs.  A row with a logit that is not finite gets
+ * NaN and ids of -1.
+ *   embed      device fp16 [vocab, d]
+ *   y          device fp32 [n][y_stride]
+ *   targets    device int32 [n], with logp; or both NULL
+ *   logp, entropy  device fp32 [n] (entropy may be NULL)
+ *   top_ids    device int32 [n, k], top_logp device fp32 [n, k] (k = 0: NULL)
+ *   workspace  device scratch of tl_score_head_workspace_bytes bytes, 256-byte
+ *              aligned, for this call's use until it completes on the stream
+ * Requirements: 0 <= n <= 65536, 1 <= vocab <= 2^24, d a multiple of 64 in
+ * [64, 8192], 0 <= k <= min(16, vocab), embed and y 16-byte aligned, y_stride a
+ * multiple of 4. */
+tl_status tl_score_head_workspace_bytes(int n, int vocab, int d, int k, size_t* bytes);
+tl_status tl_score_head(const uint16_t* embed, int vocab, int d, const float* y, long y_stride,
+                        int n, const int32_t* targets, float* logp, float* entropy, int k,
+                        int32_t* top_ids, float* top_logp, void* workspace,
+                        size_t workspace_bytes, tl_stream stream);
 
 /* One greedy self-speculative step of one lane with one weight set and one
  * cache ("Current Status", self-speculative row; "TinyLoop Framework", "What

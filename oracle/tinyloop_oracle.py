@@ -205,6 +205,42 @@ def kv_dequant_int8(codes: np.ndarray, scale16: np.ndarray) -> np.ndarray:
 
 
 # --------------------------------------------------------------------------
+# 4-bit KV quantisation: groups of 32 with an fp16 scale and zero point
+# --------------------------------------------------------------------------
+
+INT4_GROUP = 32
+
+
+def kv_quant_int4(x16: np.ndarray):
+    """fp16 rows [..., hd] -> codes uint8 [..., hd] (0..15), scale and zero fp16
+    [..., hd / 32].  Per group: scale = (hi - lo) / 15 rounded towards zero to
+    fp16, zero = lo, code = clamp(rint((x - lo) * (1 / scale)), 0, 15), every
+    step an IEEE fp32 operation; a group holding a non-finite value gets NaN
+    parameters and codes 0."""
+    x = np.asarray(x16, dtype=np.float16)
+    g = x.reshape(x.shape[:-1] + (x.shape[-1] // INT4_GROUP, INT4_GROUP)).astype(np.float32)
+    bad = ~np.isfinite(g).all(-1)
+    g = np.where(bad[..., None], np.float32(0), g)
+    lo, hi = g.min(-1), g.max(-1)
+    step = ((hi - lo).astype(np.float32) / np.float32(15)).astype(np.float32)
+    near = step.astype(np.float16)
+    scale = np.where(near.astype(np.float32) > step, np.nextafter(near, np.float16(0)), near)
+    s32 = scale.astype(np.float32)
+    with np.errstate(divide="ignore"):
+        inv = np.where(s32 > 0, np.float32(1) / s32, np.float32(0)).astype(np.float32)
+    off = (g - lo[..., None]).astype(np.float32)
+    codes = np.clip(np.rint((off * inv[..., None]).astype(np.float32)), 0, 15).astype(np.uint8)
+    scale = np.where(bad, np.float16(np.nan), scale)
+    zero = np.where(bad, np.float16(np.nan), (lo + np.float32(0)).astype(np.float16))
+    return codes.reshape(x.shape), scale, zero
+
+
+def kv_dequant_int4(codes: np.ndarray, scale16: np.ndarray, zero16: np.ndarray) -> np.ndarray:
+    c = codes.reshape(codes.shape[:-1] + (codes.shape[-1] // INT4_GROUP, INT4_GROUP)).astype(F64)
+    return (zero16.astype(F64)[..., None] + c * scale16.astype(F64)[..., None]).reshape(codes.shape)
+
+
+# --------------------------------------------------------------------------
 # Byte sizes (closed forms the pages' memory numbers pin)
 # --------------------------------------------------------------------------
 
@@ -216,6 +252,8 @@ def kv_cache_bytes(n_layers: int, max_seq: int, n_heads: int, head_dim: int, kv_
         return 2 * elems
     if kv_dtype == "int8":
         return elems + 2 * (2 * n_layers * max_seq * n_heads)
+    if kv_dtype == "int4":   # half a byte a value, four bytes per group of 32
+        return elems // 2 + elems // INT4_GROUP * 4
     raise ValueError(kv_dtype)
 
 
@@ -369,7 +407,7 @@ def pack_block(weights: Dict[str, np.ndarray], bits: int, group: int,
 
 class KVSlot:
     """K/V of one layer (one pre-block or one loop iteration) for one lane, in
-    the cache's storage dtype: "fp16", "int8", "exact" (fp64, used only to
+    the cache's storage dtype: "fp16", "int8", "int4", "exact" (fp64, used only to
     check the cached path against the uncached one without storage rounding)
     or "h".  Stored values are kept dequantised, positions 0..len-1.
 
@@ -399,6 +437,8 @@ class KVSlot:
         if self.dtype == "int8":
             codes, scale = kv_quant_int8(x16)
             return kv_dequant_int8(codes, scale)
+        if self.dtype == "int4":
+            return kv_dequant_int4(*kv_quant_int4(x16))
         raise ValueError(self.dtype)
 
     def _reserve(self, n: int, shape) -> None:

@@ -1,0 +1,232 @@
+"""Attention over a 4-bit KV cache against fp64 attention over the values the
+cache holds; the bound of each element is derived from the kernel's roundings
+(int4_util.attend)."""
+import numpy as np
+import pytest
+import torch
+
+import synthetic as syn
+import weight_shared_looped_b200 as tl
+
+from int4_util import Cache, attend
+
+pytestmark = pytest.mark.gpu
+
+
+def _kv(lanes, H, ctx, hd, seed):
+    k = syn.normal((lanes, H, ctx, hd), 1.0, seed, "a4.k")
+    k += np.where(np.abs(syn.normal((H, 1, hd), 1.0, seed, "a4.off")) > 1.8, 3.0, 0.0)
+    return k.astype(np.float16), syn.normal((lanes, H, ctx, hd), 1.0, seed, "a4.v").astype(np.float16)
+
+
+def _q(rows, heads, hd, seed, std=1.0):
+    return syn.normal((rows, heads, hd), std, seed, "a4.q").astype(np.float16)
+
+
+def _run(q, cache, lens, n_q, window, out=None):
+    rows, heads, hd = q.shape
+    tq = torch.from_numpy(q.reshape(rows, heads * hd)).cuda()
+    if out is None:
+        out = torch.full((rows, heads * hd), float("nan"), dtype=torch.float16, device="cuda")
+    tl.tl_attention_int4(tq, *cache.t, torch.tensor(lens, dtype=torch.int32, device="cuda"), out,
+                         n_q=n_q, window=window)
+    torch.cuda.synchronize()
+    return out.cpu().numpy().reshape(rows, heads, hd)
+
+
+def _check(got, q, cache, lens, n_q, window):
+    for b, length in enumerate(lens):
+        rows = slice(b * n_q, (b + 1) * n_q)
+        ref, tol = attend(q[rows].astype(np.float64), cache.K(b), cache.V(b), length, n_q, window)
+        y = got[rows].astype(np.float64)
+        assert np.isfinite(y).all(), (b, length)
+        over = np.abs(y - ref) - tol
+        assert over.max() <= 0, (b, length, over.max(), np.unravel_index(over.argmax(), over.shape))
+
+
+CASES = [
+    # H, group, hd, ctx, n_q, window, lens, q_std
+    (1, 1, 64, 1, 1, 0, [1], 1.0),
+    (1, 1, 128, 16, 1, 0, [1, 2, 15, 16], 1.0),
+    (2, 1, 128, 17, 1, 0, [17, 16, 0, 1], 1.0),
+    (4, 1, 64, 63, 1, 0, [63, 62, 33], 4.0),
+    (16, 1, 128, 384, 1, 0, [384, 257], 1.0),
+    (2, 4, 128, 130, 1, 0, [130, 128, 65], 1.0),
+    (1, 8, 64, 200, 1, 0, [200, 111], 2.0),
+    (2, 3, 64, 90, 5, 0, [90, 7, 5, 4, 1, 0], 1.0),       # 15 queries a head; rows that see nothing
+    (1, 16, 128, 70, 8, 0, [70, 33, 8, 3], 1.0),          # 128 queries a head
+    (3, 1, 128, 100, 2, 1, [100, 50, 2, 1], 1.0),         # window 1: only itself
+    (2, 2, 64, 300, 3, 40, [300, 41, 40, 39, 3], 1.0),
+    (2, 1, 128, 300, 8, 17, [300, 16, 160], 8.0),
+    (2, 1, 64, 1000, 4, 1000, [1000, 999], 1.0),
+    (1, 2, 128, 2112, 1, 0, [2112, 2049], 8.0),
+    (2, 1, 128, 9000, 1, 0, [9000], 4.0),
+    (1, 4, 64, 33000, 2, 20000, [33000], 2.0),
+]
+
+
+@pytest.mark.parametrize("H,group,hd,ctx,n_q,window,lens,q_std", CASES)
+def test_matches_fp64(H, group, hd, ctx, n_q, window, lens, q_std):
+    lanes = len(lens)
+    cache = Cache(*_kv(lanes, H, ctx, hd, ctx))
+    q = _q(lanes * n_q, H * group, hd, ctx + 1, q_std)
+    got = _run(q, cache, lens, n_q, window)
+    _check(got, q, cache, lens, n_q, window)
+    for b, length in enumerate(lens):
+        for i in range(n_q):
+            if length - n_q + i < 0:
+                assert (got[b * n_q + i] == 0).all()
+
+
+def test_length_above_the_cache_counts_as_the_cache():
+    cache = Cache(*_kv(1, 2, 20, 64, 7))
+    q = _q(1, 2, 64, 8)
+    assert np.array_equal(_run(q, cache, [1 << 30], 1, 0), _run(q, cache, [20], 1, 0))
+    assert (_run(q, cache, [-5], 1, 0) == 0).all()
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+def test_equal_keys_give_the_mean(hd):
+    """Constant groups have scale 0: the value is the zero point, and equal keys
+    weigh equally whatever the query."""
+    ctx, n = 100, 77
+    k = np.full((1, 1, ctx, hd), 1.5, np.float16)
+    _, v = _kv(1, 1, ctx, hd, 9)
+    cache = Cache(k, v)
+    assert (cache.kp[..., 0] == 0).all()
+    q = _q(1, 1, hd, 10)
+    _check(_run(q, cache, [n], 1, 0), q, cache, [n], 1, 0)
+
+
+def _spoil(cache, lane, head, p, value):
+    cache.kp[lane, head, p] = value
+    cache.vp[lane, head, p] = value
+
+
+@pytest.mark.parametrize("value", [np.nan, np.inf, -np.inf, 65504.0])
+def test_unseen_entries_have_no_effect(value):
+    """Entries behind a lane's length, before its window, after a query's own
+    position, or of another lane may hold anything."""
+    H, hd, ctx, n_q, window = 2, 128, 90, 3, 30
+    lens = [70, 35, 2]
+    clean = Cache(*_kv(3, H, ctx, hd, 11))
+    q = _q(9, 2 * H, hd, 12)
+    want = _run(q, clean, lens, n_q, window)
+    _check(want, q, clean, lens, n_q, window)
+    dirty = Cache(*_kv(3, H, ctx, hd, 11))
+    for b, length in enumerate(lens):
+        for p in list(range(length, ctx)) + list(range(max(0, length - n_q + 1 - window))):
+            _spoil(dirty, b, slice(None), p, value)
+    dirty.upload()
+    assert np.array_equal(_run(q, dirty, lens, n_q, window), want)
+    # the last token's own entry and the oldest: seen by some of the lane's queries, not by others
+    _spoil(dirty, 0, slice(None), 69, value)
+    _spoil(dirty, 0, slice(None), 70 - n_q + 1 - window, value)
+    dirty.upload()
+    got = _run(q, dirty, lens, n_q, window)
+    assert np.array_equal(got[3:], want[3:])                        # the other lanes
+    assert np.array_equal(got[1], want[1])                          # query 1 sees neither
+    if np.isnan(value):
+        assert np.isnan(got[0]).all() and np.isnan(got[2]).all()    # query 0 the oldest, query 2 its own
+
+
+def test_a_seen_nan_reaches_only_its_lane_and_head():
+    H, hd, ctx = 3, 64, 50
+    cache = Cache(*_kv(2, H, ctx, hd, 13))
+    q = _q(2, H, hd, 14)
+    want = _run(q, cache, [50, 50], 1, 0)
+    _spoil(cache, 0, 1, 20, np.nan)
+    cache.upload()
+    got = _run(q, cache, [50, 50], 1, 0)
+    assert np.isnan(got[0, 1]).all()
+    got[0, 1] = want[0, 1]
+    assert np.array_equal(got, want)
+
+
+def test_a_query_alone_and_among_others_gives_the_same_bits():
+    """A query's arithmetic does not depend on the lane's other queries, its
+    neighbours' contents, or the run."""
+    H, hd, ctx, n_q = 2, 128, 400, 8
+    cache = Cache(*_kv(1, H, ctx, hd, 15))
+    q = _q(n_q, H, hd, 16, 3.0)
+    many = _run(q, cache, [333], n_q, 0)
+    assert np.array_equal(many, _run(q, cache, [333], n_q, 0))
+    for i in range(n_q):
+        assert np.array_equal(_run(q[i:i + 1], cache, [333 - n_q + 1 + i], 1, 0)[0], many[i]), i
+
+
+def test_strides():
+    """Queries and outputs as column slices of wider rows, lanes further apart
+    than their size."""
+    H, hd, ctx, lens = 2, 64, 40, [40, 13]
+    k, v = _kv(2, H, ctx, hd, 17)
+    cache, padded = Cache(k, v), Cache(k, v, lane_pad=3)
+    q = _q(2, 2 * H, hd, 18)
+    want = _run(q, cache, lens, 1, 0)
+    assert padded.t[0].stride(0) == H * (ctx + 3) * hd // 8
+    assert np.array_equal(_run(q, padded, lens, 1, 0), want)
+    w = 2 * H * hd
+    wide = torch.zeros(2, 3 * w, dtype=torch.float16, device="cuda")
+    wide[:, w:2 * w] = torch.from_numpy(q.reshape(2, w)).cuda()
+    out = torch.full((2, 2 * w), 5.0, dtype=torch.float16, device="cuda")
+    tl.tl_attention_int4(wide[:, w:2 * w], *cache.t, torch.tensor(lens, dtype=torch.int32, device="cuda"), out[:, w:])
+    got = out.cpu().numpy()
+    assert (got[:, :w] == 5).all() and np.array_equal(got[:, w:].reshape(want.shape), want)
+
+
+def test_streams_graphs_and_growing_lengths():
+    """Two calls at once on two streams; a captured write and attention replayed
+    while the lane grows."""
+    H, hd, ctx = 2, 128, 64
+    k, v = _kv(1, H, ctx, hd, 19)
+    ref = Cache(k, v)
+    q = _q(1, H, hd, 20)
+    others = [Cache(*_kv(1, H, ctx, hd, 30 + i)) for i in range(2)]
+    wants = [_run(q, c, [ctx], 1, 0) for c in others]
+    streams = [torch.cuda.Stream() for _ in others]
+    tq = torch.from_numpy(q.reshape(1, -1)).cuda()
+    full = torch.tensor([ctx], dtype=torch.int32, device="cuda")
+    outs = [torch.zeros_like(tq) for _ in others]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for s, c, out in zip(streams, others, outs):
+            tl.tl_attention_int4(tq, *c.t, full, out, stream=s)
+    torch.cuda.synchronize()
+    for out, want in zip(outs, wants):
+        assert np.array_equal(out.cpu().numpy().reshape(want.shape), want)
+
+    cache = [torch.full_like(t, 0) for t in ref.t]
+    row = [torch.zeros(1, H * hd, dtype=torch.float16, device="cuda") for _ in range(2)]
+    pos, lens = torch.zeros(1, dtype=torch.int32, device="cuda"), torch.ones(1, dtype=torch.int32, device="cuda")
+    out = torch.zeros_like(tq)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        tl.tl_kv_write_int4(row[0], row[1], *cache, pos)
+        tl.tl_attention_int4(tq, *cache, lens, out)
+    for p in range(40):
+        row[0].copy_(torch.from_numpy(k[0, :, p].reshape(1, -1)))
+        row[1].copy_(torch.from_numpy(v[0, :, p].reshape(1, -1)))
+        pos.fill_(p)
+        lens.fill_(p + 1)
+        graph.replay()
+        if p in (0, 15, 16, 39):
+            torch.cuda.synchronize()
+            assert np.array_equal(out.cpu().numpy().reshape(1, H, hd), _run(q, ref, [p + 1], 1, 0)), p
+
+
+def test_far_offsets():
+    """A cache whose last lane lies past 2^31 code words: one head of lane 2 over
+    a lane stride of 2^30 words, most of it never touched."""
+    hd, ctx = 128, 48
+    k, v = _kv(3, 1, ctx, hd, 21)
+    cache = Cache(k, v)
+    stride = 1 << 30
+    big = torch.empty(2 * stride + ctx * hd // 8, dtype=torch.int32, device="cuda")
+    codes = [torch.as_strided(big, (3, 1, ctx, hd // 8), (stride, ctx * hd // 8, hd // 8, 1))] * 2
+    # K and V share the far array here: both hold K's codes
+    codes[0].copy_(cache.t[0])
+    cache.vw = cache.kw
+    cache.t = [codes[0], cache.t[1], codes[1], cache.t[3]]
+    q = _q(3, 1, hd, 22)
+    lens = [48, 47, 33]
+    _check(_run(q, cache, lens, 1, 0), q, cache, lens, 1, 0)

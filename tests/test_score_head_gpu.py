@@ -1,0 +1,224 @@
+"""The scoring head against fp64 softmax statistics of y . E.
+
+Bounds.  A logit of the streaming pass is a sum of d products with activations
+of at least 22 bits and fp32 accumulation: with A = sum |y_i E_i| its error is at
+most A (2^-22 + (d / 16 + 24) 2^-23), the accumulation taking 16 products or
+fewer at a time.  The log of the sum of exponentials moves by no more than the
+logits do, plus the rounding of the exponentials and their sum (2^-20 covers
+2^-22 of the fast exponential, its argument's rounding 2^-24 |z - m| <= 2^-19 on
+weights e^-(m - z), and the sum of V terms held in many parts).  The given
+token's logit and the order of the best come from fp64 sums."""
+import numpy as np
+import pytest
+import torch
+
+import synthetic as syn
+import weight_shared_looped_b200 as tl
+
+from gpu_util import device_model
+
+pytestmark = pytest.mark.gpu
+
+
+def _inputs(n, V, d, seed, lean=12.0):
+    """Rows that lean towards one token by varying amounts: flat to peaked."""
+    E = syn.normal((V, d), 0.02, seed, "score.E").astype(np.float16)
+    y = syn.normal((n, d), 1.0, seed, "score.y")
+    t = syn.token_ids(n, seed, "score.t", V)
+    w = E[t].astype(np.float32)
+    amount = np.linspace(0, lean, n)[:, None].astype(np.float32)
+    return E, (y + amount * w / np.linalg.norm(w, axis=1, keepdims=True)).astype(np.float32), t
+
+
+def _run(E, y, targets, k, entropy=True, ty=None):
+    n = y.shape[0]
+    tE = torch.from_numpy(E).cuda()
+    ty = torch.from_numpy(y).cuda() if ty is None else ty
+    tt = None if targets is None else torch.from_numpy(np.asarray(targets, np.int32)).cuda()
+    f = lambda *s: torch.full(s, 777.0, dtype=torch.float32, device="cuda")  # noqa: E731
+    lp, h = None if tt is None else f(n), f(n) if entropy else None
+    ids, top = (torch.full((n, k), -7, dtype=torch.int32, device="cuda"), f(n, k)) if k else (None, None)
+    ws = torch.empty(tl.tl_score_head_workspace_bytes(n, E.shape[0], E.shape[1], k), dtype=torch.uint8, device="cuda")
+    tl.tl_score_head(tE, ty, tt, lp, h, ids, top, ws)
+    torch.cuda.synchronize()
+    return [None if t is None else t.cpu().numpy() for t in (lp, h, ids, top)]
+
+
+def _reference(E, y, targets, k):
+    """logp, entropy, ids, top in fp64, and the bound of each row."""
+    V, d = E.shape
+    e, yy = torch.from_numpy(E).cuda().double(), torch.from_numpy(y).cuda().double()
+    out = []
+    for r0 in range(0, len(y), 256):
+        z = yy[r0:r0 + 256] @ e.t()
+        A = (yy[r0:r0 + 256].abs() @ e.t().abs()).amax(1)
+        lp = z - torch.logsumexp(z, 1, keepdim=True)
+        h = -(lp.exp() * lp).sum(1)
+        spread = (lp.exp() * (lp + h[:, None]).abs()).sum(1)   # how entropy moves with a logit
+        ids = torch.sort(z, dim=1, descending=True, stable=True).indices[:, :k]
+        out.append([t.cpu().numpy() for t in (lp, h, ids, lp.gather(1, ids), A, spread)])
+    lp, h, ids, top, A, spread = (np.concatenate(t) for t in zip(*out))
+    eps = A * (2.0 ** -22 + (d / 16 + 24) * 2.0 ** -23) + 2.0 ** -20
+    got = None if targets is None else np.where(np.asarray(targets) < 0, 0.0, lp[np.arange(len(y)), np.maximum(targets, 0)])
+    return got, h, ids, top, eps, eps * (1 + 2 * spread) + np.abs(h) * 2.0 ** -20
+
+
+def _check(E, y, targets, k):
+    lp, h, ids, top = _run(E, y, targets, k)
+    rlp, rh, rids, rtop, eps, heps = _reference(E, y, targets, k)
+    f32 = 2.0 ** -24
+    if targets is not None:
+        assert (np.abs(lp - rlp) <= eps + f32 * np.abs(rlp)).all(), np.abs(lp - rlp).max()
+        assert (lp[np.asarray(targets) < 0] == 0).all()
+    assert (np.abs(h - rh) <= heps).all(), (np.abs(h - rh) - heps).max()
+    if k:
+        assert np.array_equal(ids, rids)
+        assert (np.abs(top - rtop) <= eps[:, None] + f32 * np.abs(rtop)).all()
+
+
+CASES = [
+    # n, V, d, k
+    (1, 1, 64, 1), (1, 2, 64, 0), (3, 17, 64, 16), (2, 16, 128, 16),
+    (1, 1000, 256, 5), (4, 1021, 256, 3), (8, 4099, 512, 8), (9, 777, 320, 1),
+    (16, 5003, 2048, 5), (17, 255, 192, 16), (31, 256, 256, 4), (32, 257, 256, 5), (33, 258, 64, 2),
+    (63, 3001, 256, 9), (64, 2000, 512, 16), (65, 1999, 1024, 6), (127, 300, 256, 2),
+    (128, 4000, 256, 8), (129, 129, 256, 4), (200, 6001, 768, 12), (257, 50257, 256, 5),
+    (300, 1500, 8192, 3), (1, 50257, 2048, 5), (8, 50257, 2048, 0),
+]
+
+
+@pytest.mark.parametrize("n,V,d,k", CASES)
+def test_matches_fp64(n, V, d, k):
+    E, y, t = _inputs(n, V, d, n + V + d)
+    t = np.where(np.arange(n) % 5 == 3, -1, t)
+    _check(E, y, t, k)
+
+
+def test_ties_go_to_the_lowest_id():
+    """Equal rows of the embedding give equal logits."""
+    E, y, t = _inputs(40, 3000, 256, 50)
+    E[2999] = E[1234] = E[7] = E[int(t[-1])]
+    E[1000:1100] = E[999]
+    y[0] = 0                                  # every logit 0: ids 0 .. k - 1
+    y[1] = 60 * E[999].astype(np.float32)     # 101 equal best
+    _, _, ids, top = _run(E, y, t, 10)
+    assert np.array_equal(ids[0], np.arange(10)) and (np.abs(top[0] + np.log(3000)) <= 2.0 ** -18).all()
+    assert np.array_equal(ids[1], 999 + np.arange(10))
+    same = [7, 1234, 2999] + ([int(t[-1])] if int(t[-1]) not in (7, 1234, 2999) else [])
+    assert np.array_equal(ids[-1][:len(same)], np.sort(same))
+
+
+@pytest.mark.parametrize("scale", [1e-30, 1e-4, 300.0, 1e6])
+def test_activations_of_any_size(scale):
+    """Activations beyond the fp16 range on both sides; logits up to 1e6."""
+    E, y, t = _inputs(20, 1500, 256, 60)
+    _check(E, (y * np.float32(scale)).astype(np.float32), t, 4)
+
+
+def test_one_large_channel():
+    """A channel 10^4 times the others must not cost the others their bits."""
+    E, y, t = _inputs(20, 1500, 256, 61)
+    y[:, 17] = 1e4
+    _check(E, y, t, 4)
+
+
+def test_targets_outside_and_missing_outputs():
+    E, y, t = _inputs(12, 400, 128, 70)
+    t = t.copy()
+    t[3], t[4], t[5] = -100, 400, 2 ** 31 - 1
+    lp, h, ids, top = _run(E, y, t, 2)
+    assert lp[3] == 0 and np.isnan(lp[4]) and np.isnan(lp[5])
+    ok = [i for i in range(12) if i not in (4, 5)]
+    rlp = _reference(E, y, np.where(t >= 400, -1, t), 2)[0]
+    assert np.abs(lp[ok] - rlp[ok]).max() < 1e-4
+    a = _run(E, y, None, 2)
+    assert a[0] is None and np.array_equal(a[1], h) and np.array_equal(a[2], ids) and np.array_equal(a[3], top)
+    b = _run(E, y, t, 0, entropy=False)
+    assert b[1] is None and np.array_equal(b[0], lp, equal_nan=True)
+
+
+@pytest.mark.parametrize("bad", [np.nan, np.inf, -np.inf])
+def test_rows_that_are_not_finite(bad):
+    """They get NaN and ids of -1; the rows beside them keep their results."""
+    for n in (5, 40, 140):
+        E, y, t = _inputs(n, 600, 256, 80)
+        want = _run(E, y, t, 3)
+        y[2, 100] = bad
+        got = _run(E, y, t, 3)
+        assert np.isnan(got[0][2]) and np.isnan(got[1][2]) and np.isnan(got[3][2]).all() and (got[2][2] == -1).all()
+        keep = np.arange(n) != 2
+        for g, w in zip(got, want):
+            assert np.array_equal(g[keep], w[keep])
+
+
+def test_an_embedding_row_that_is_not_finite():
+    E, y, t = _inputs(6, 600, 256, 81)
+    E[77, 5] = np.nan
+    lp, h, ids, top = _run(E, y, t, 3)
+    assert np.isnan(lp).all() and np.isnan(h).all() and np.isnan(top).all() and (ids == -1).all()
+
+
+@pytest.mark.parametrize("n", [3, 20, 130])
+def test_row_strides_and_unaligned_tails(n):
+    E, y, t = _inputs(n, 900, 192, 90)
+    want = _run(E, y, t, 4)
+    wide = torch.full((n, 192 + 60), 9.0, dtype=torch.float32, device="cuda")
+    wide[:, 12:204] = torch.from_numpy(y).cuda()
+    got = _run(E, y, t, 4, ty=wide[:, 12:204])
+    for g, w in zip(got, want):
+        assert np.array_equal(g, w)
+
+
+@pytest.mark.parametrize("n", [1, 24, 150])
+def test_streams_and_graphs(n):
+    """Captured and replayed with new rows; two graphs with their own workspaces
+    in flight together; equal bits at every run."""
+    V, d, k = 2003, 256, 5
+    E, y, t = _inputs(n, V, d, 91)
+    tE, tt = torch.from_numpy(E).cuda(), torch.from_numpy(t).cuda()
+    runs = []
+    for i in range(2):
+        r = dict(y=torch.from_numpy(y).cuda(), lp=torch.zeros(n, device="cuda"), h=torch.zeros(n, device="cuda"),
+                 ids=torch.zeros(n, k, dtype=torch.int32, device="cuda"), top=torch.zeros(n, k, device="cuda"),
+                 ws=torch.empty(tl.tl_score_head_workspace_bytes(n, V, d, k), dtype=torch.uint8, device="cuda"))
+        call = lambda r=r: tl.tl_score_head(tE, r["y"], tt, r["lp"], r["h"], r["ids"], r["top"], r["ws"])  # noqa: E731
+        call()
+        torch.cuda.synchronize()
+        r["g"] = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(r["g"]):
+            call()
+        runs.append(r)
+    streams = [torch.cuda.Stream() for _ in runs]
+    for seed in (1, 2):
+        ys = [_inputs(n, V, d, 100 + 10 * seed + i)[1] for i in range(2)]
+        for r, yy in zip(runs, ys):
+            r["y"].copy_(torch.from_numpy(yy))
+        torch.cuda.synchronize()
+        for _ in range(5):
+            for r, s in zip(runs, streams):
+                with torch.cuda.stream(s):
+                    r["g"].replay()
+        torch.cuda.synchronize()
+        for r, yy in zip(runs, ys):
+            want = _run(E, yy, t, k)
+            for g, w in zip((r["lp"], r["h"], r["ids"], r["top"]), want):
+                assert np.array_equal(g.cpu().numpy(), w)
+
+
+def test_model_scores_a_prompt():
+    """Through the model: prefill, then the scores of the following tokens; the
+    best alternative is the greedy head's token."""
+    w = syn.WORKLOADS["prefill407m"]
+    m = device_model("prefill407m", max_tokens=128)
+    ids = syn.token_ids(24, 0, "score.prompt")
+    y = m.prefill(torch.from_numpy(ids).cuda(), L=2)
+    nxt = torch.from_numpy(np.append(ids[1:], -1).astype(np.int32)).cuda()
+    got = m.score(y, nxt, k=3)
+    E = syn.embedding(w.shape, w.seed)
+    rlp, rh, rids, rtop, eps, heps = _reference(E, y.cpu().numpy(), np.append(ids[1:], -1), 3)
+    assert (np.abs(got["logp"].cpu().numpy() - rlp) <= eps + 2.0 ** -20).all()
+    assert (np.abs(got["entropy"].cpu().numpy() - rh) <= heps).all()
+    assert np.array_equal(got["ids"].cpu().numpy(), rids)
+    greedy = m.greedy_head(y[:8].contiguous())
+    assert torch.equal(greedy, got["ids"][:8, 0])
+    m.close()

@@ -17,7 +17,7 @@ LIB_PATH = os.path.join(HERE, "libtinyloop_b200.so")
 
 TL_OK, TL_ERR_INVALID_ARG, TL_ERR_CUDA, TL_ERR_OOM, TL_ERR_TIMEOUT, TL_ERR_UNSUPPORTED, \
     TL_ERR_NUMERIC = range(7)
-TL_KV_FP16, TL_KV_INT8, TL_KV_H = 0, 1, 2
+TL_KV_FP16, TL_KV_INT8, TL_KV_H, TL_KV_INT4 = 0, 1, 2, 3
 STATUS_NAMES = {0: "TL_OK", 1: "TL_ERR_INVALID_ARG", 2: "TL_ERR_CUDA", 3: "TL_ERR_OOM",
                 4: "TL_ERR_TIMEOUT", 5: "TL_ERR_UNSUPPORTED", 6: "TL_ERR_NUMERIC"}
 
@@ -37,6 +37,7 @@ P = ctypes.c_void_p
 I = ctypes.c_int
 SZ = ctypes.c_size_t
 F = ctypes.c_float
+LG = ctypes.c_long
 
 
 class BlockDesc(ctypes.Structure):
@@ -54,6 +55,12 @@ class ModelDesc(ctypes.Structure):
                 ("max_L", I)]
 
 
+class KvInt4Desc(ctypes.Structure):
+    _fields_ = [("k_codes", P), ("v_codes", P), ("k_params", P), ("v_params", P),
+                ("code_stride", SZ), ("param_stride", SZ),
+                ("n_lanes", I), ("n_heads", I), ("head_dim", I), ("max_ctx", I)]
+
+
 _SIGS = {
     "tl_last_error": ([], ctypes.c_char_p),
     "tl_abi_version": ([], I),
@@ -64,6 +71,11 @@ _SIGS = {
     "tl_sign_bits_bytes": ([I, I, ctypes.POINTER(SZ)], I),
     "tl_pack_sign_bits": ([P, I, I, I, I, P, P, P], I),
     "tl_kv_quant_int8": ([P, I, I, P, P, P], I),
+    "tl_kv_write_int4": ([ctypes.POINTER(KvInt4Desc), P, P, LG, P, P, I, P], I),
+    "tl_kv_read_int4": ([ctypes.POINTER(KvInt4Desc), P, P, LG, P, P, I, P], I),
+    "tl_attention_int4": ([ctypes.POINTER(KvInt4Desc), P, LG, I, I, P, I, P, LG, P], I),
+    "tl_score_head_workspace_bytes": ([I, I, I, I, ctypes.POINTER(SZ)], I),
+    "tl_score_head": ([P, I, I, P, LG, I, P, P, P, I, P, P, P, SZ, P], I),
     "tl_attention_prefill": ([P, P, P, I, I, I, P, P], I),
     "tl_block_create": ([ctypes.POINTER(BlockDesc), ctypes.POINTER(P)], I),
     "tl_block_destroy": ([P], I),
@@ -180,6 +192,170 @@ def tl_attention_prefill(q, k, v, H: int, hd: int, out, stream=None) -> None:
     T = q.shape[0]
     _check(lib.tl_attention_prefill(_ptr(q), _ptr(k), _ptr(v), T, H, hd, _ptr(out),
                                     _stream(stream)))
+
+
+# --------------------------------------------------------------------- 4-bit KV cache
+
+def _fail(message: str) -> None:
+    raise TLError(TL_ERR_INVALID_ARG, message)
+
+
+def _tensors(what: str, **named):
+    """Checks that the C side cannot make: every tensor (None entries aside) is a CUDA
+    tensor of the given type and number of dimensions, all on one device.  named: name ->
+    (tensor, torch dtypes, dims).  Returns the device."""
+    device = None
+    named = {name: v for name, v in named.items() if v[0] is not None}
+    for name, (t, dtypes, dims) in named.items():
+        if t.dtype not in dtypes:
+            _fail(f"{what}: {name} has dtype {t.dtype}, not {' or '.join(str(d) for d in dtypes)}")
+        if t.dim() != dims:
+            _fail(f"{what}: {name} has {t.dim()} dimensions, not {dims}")
+    for name, (t, _, _) in named.items():
+        if not t.is_cuda:
+            _fail(f"{what}: {name} is not on a CUDA device")
+        if device is None:
+            device = t.device
+        elif t.device != device:
+            _fail(f"{what}: {name} is on {t.device}, not {device}")
+    return device
+
+
+def _dtypes():
+    """fp16 values (also as raw int16 bits), int32, fp32, 4-byte parameter pairs."""
+    import torch
+    return (torch.float16, torch.int16), (torch.int32,), (torch.float32,)
+
+
+def _on(device, call, *args, stream=None) -> None:
+    """The C call on `device`'s current stream (or `stream`), with `device` current."""
+    import torch
+    if device.index == torch.cuda.current_device():
+        _check(call(*args, _stream(stream)))
+    else:
+        with torch.cuda.device(device):
+            _check(call(*args, _stream(stream)))
+
+
+def _kv_int4(what: str, k_codes, k_params, v_codes, v_params, f16, i32):
+    """The cache description of codes int32 [lanes, heads, ctx, hd / 8] and parameters fp16
+    [lanes, heads, ctx, hd / 32, 2]; only the lane stride is free."""
+    lanes, heads, ctx, words = k_codes.shape
+    strides = []
+    for name, t, want in (("k_codes", k_codes, (lanes, heads, ctx, words)),
+                          ("v_codes", v_codes, (lanes, heads, ctx, words)),
+                          ("k_params", k_params, (lanes, heads, ctx, words // 4, 2)),
+                          ("v_params", v_params, (lanes, heads, ctx, words // 4, 2))):
+        if tuple(t.shape) != want:
+            _fail(f"{what}: {name} has shape {tuple(t.shape)}, not {want}")
+        if not t.is_contiguous() and not (lanes > 0 and t[0].is_contiguous()):
+            _fail(f"{what}: {name} is not contiguous within a lane")
+        inner = want[1] * want[2] * want[3] * (2 if len(want) == 5 else 1)
+        strides.append(t.stride(0) if lanes > 1 else inner)
+    if strides[0] != strides[1] or strides[2] != strides[3] or strides[2] % 2:
+        _fail(f"{what}: K and V have different lane strides")
+    return KvInt4Desc(_ptr(k_codes), _ptr(v_codes), _ptr(k_params), _ptr(v_params), strides[0],
+                      strides[2] // 2, lanes, heads, words * 8, ctx)
+
+
+def _kv_int4_rows(what, fn, k, v, k_codes, k_params, v_codes, v_params, pos, cu, stream):
+    f16, i32, _ = _dtypes()
+    device = _tensors(what, k=(k, f16, 2), v=(v, f16, 2), k_codes=(k_codes, i32, 4),
+                      k_params=(k_params, f16, 5), v_codes=(v_codes, i32, 4),
+                      v_params=(v_params, f16, 5), pos=(pos, i32, 1), cu=(cu, i32, 1))
+    d = _kv_int4(what, k_codes, k_params, v_codes, v_params, f16, i32)
+    n, width = k.shape
+    if tuple(v.shape) != (n, width) or width != d.n_heads * d.head_dim:
+        _fail(f"{what}: k {tuple(k.shape)} and v {tuple(v.shape)} are not rows of "
+              f"{d.n_heads} x {d.head_dim} values")
+    if n and (k.stride(1) != 1 or v.stride(1) != 1 or (n > 1 and k.stride(0) != v.stride(0))):
+        _fail(f"{what}: k and v need unit column stride and the same row stride")
+    if pos.shape[0] != d.n_lanes or not pos.is_contiguous():
+        _fail(f"{what}: pos is not a contiguous [{d.n_lanes}]")
+    if cu is not None and (cu.shape[0] != d.n_lanes + 1 or not cu.is_contiguous()):
+        _fail(f"{what}: cu is not a contiguous [{d.n_lanes + 1}]")
+    stride = k.stride(0) if n > 1 else width
+    _on(device, fn, ctypes.byref(d), _ptr(k), _ptr(v), stride, _ptr(cu), _ptr(pos), n, stream=stream)
+
+
+def tl_kv_write_int4(k, v, k_codes, k_params, v_codes, v_params, pos, cu=None, stream=None) -> None:
+    """Quantise packed fp16 rows k, v [n, heads * hd] (column slices allowed) into the 4-bit
+    caches codes int32 [lanes, heads, ctx, hd / 8] and params fp16 [lanes, heads, ctx, hd / 32,
+    2]: lane b takes rows cu[b] .. cu[b + 1] - 1 (or an equal share) at positions pos[b], ..."""
+    _kv_int4_rows("tl_kv_write_int4", lib.tl_kv_write_int4, k, v, k_codes, k_params, v_codes,
+                  v_params, pos, cu, stream)
+
+
+def tl_kv_read_int4(k_codes, k_params, v_codes, v_params, pos, k, v, cu=None, stream=None) -> None:
+    """Read those positions back into fp16 rows k, v [n, heads * hd]."""
+    _kv_int4_rows("tl_kv_read_int4", lib.tl_kv_read_int4, k, v, k_codes, k_params, v_codes,
+                  v_params, pos, cu, stream)
+
+
+def tl_attention_int4(q, k_codes, k_params, v_codes, v_params, lens, out, n_q: int = 1,
+                      window: int = 0, stream=None) -> None:
+    """q, out: fp16 [lanes * n_q, q_heads * hd]; lens int32 [lanes], the queries' own
+    positions included."""
+    f16, i32, _ = _dtypes()
+    what = "tl_attention_int4"
+    device = _tensors(what, q=(q, f16, 2), k_codes=(k_codes, i32, 4), k_params=(k_params, f16, 5),
+                      v_codes=(v_codes, i32, 4), v_params=(v_params, f16, 5), lens=(lens, i32, 1),
+                      out=(out, f16, 2))
+    d = _kv_int4(what, k_codes, k_params, v_codes, v_params, f16, i32)
+    n, width = q.shape
+    if n != d.n_lanes * n_q or width % d.head_dim or tuple(out.shape) != (n, width):
+        _fail(f"{what}: q {tuple(q.shape)} and out {tuple(out.shape)} are not {d.n_lanes} x {n_q} "
+              f"rows of heads of {d.head_dim}")
+    if n and (q.stride(1) != 1 or out.stride(1) != 1):
+        _fail(f"{what}: q and out need unit column stride")
+    if lens.shape[0] != d.n_lanes or not lens.is_contiguous():
+        _fail(f"{what}: lens is not a contiguous [{d.n_lanes}]")
+    _on(device, lib.tl_attention_int4, ctypes.byref(d), _ptr(q), q.stride(0) if n > 1 else width,
+        n_q, width // d.head_dim, _ptr(lens), window, _ptr(out),
+        out.stride(0) if n > 1 else width, stream=stream)
+
+
+# --------------------------------------------------------------------- scoring head
+
+def tl_score_head_workspace_bytes(n: int, vocab: int, d: int, k: int) -> int:
+    b = SZ()
+    _check(lib.tl_score_head_workspace_bytes(n, vocab, d, k, ctypes.byref(b)))
+    return b.value
+
+
+def tl_score_head(embed, y, targets, logp, entropy, top_ids, top_logp, workspace,
+                  stream=None) -> None:
+    """Log probabilities of `targets` int32 [n] under logits y . embed^T (y fp32 [n, d], embed
+    fp16 [vocab, d]) into logp fp32 [n]; entropy fp32 [n]; the k most probable tokens into
+    top_ids int32 [n, k] and top_logp fp32 [n, k].  targets with logp, entropy, and top_ids
+    with top_logp may be None."""
+    f16, i32, f32 = _dtypes()
+    what = "tl_score_head"
+    device = _tensors(what, embed=(embed, f16, 2), y=(y, f32, 2), targets=(targets, i32, 1),
+                      logp=(logp, f32, 1), entropy=(entropy, f32, 1), top_ids=(top_ids, i32, 2),
+                      top_logp=(top_logp, f32, 2), workspace=(workspace, (_uint8(),), 1))
+    n, d = y.shape
+    vocab = embed.shape[0]
+    if embed.shape[1] != d or not embed.is_contiguous():
+        _fail(f"{what}: embed {tuple(embed.shape)} is not a contiguous [vocab, {d}]")
+    if n and y.stride(1) != 1:
+        _fail(f"{what}: y needs unit column stride")
+    if (top_ids is None) != (top_logp is None):
+        _fail(f"{what}: top_ids and top_logp go together")
+    k = 0 if top_ids is None else top_ids.shape[1]
+    for name, t, want in (("targets", targets, (n,)), ("logp", logp, (n,)),
+                          ("entropy", entropy, (n,)), ("top_ids", top_ids, (n, k)),
+                          ("top_logp", top_logp, (n, k))):
+        if t is not None and (tuple(t.shape) != want or not t.is_contiguous()):
+            _fail(f"{what}: {name} is not a contiguous {want}")
+    _on(device, lib.tl_score_head, _ptr(embed), vocab, d, _ptr(y), y.stride(0) if n > 1 else d, n,
+        _ptr(targets), _ptr(logp), _ptr(entropy), k, _ptr(top_ids) if k else None,
+        _ptr(top_logp) if k else None, _ptr(workspace), workspace.numel(), stream=stream)
+
+
+def _uint8():
+    import torch
+    return torch.uint8
 
 
 # --------------------------------------------------------------------- blocks / model

@@ -202,6 +202,171 @@ TL_API tl_status tl_kv_quant_int8(const uint16_t* x, int rows, int hd, int8_t* c
                               reinterpret_cast<__half*>(scales), (cudaStream_t)stream);
 }
 
+namespace {
+
+// Checks shared by the calls on a caller's 4-bit cache.
+tl_status check_kv4(const tl_kv_int4* c, int* head_words) {
+  TL_CHECK_ARG(c, "NULL cache description");
+  TL_CHECK_ARG(c->n_lanes >= 0 && c->n_lanes <= 65535, "n_lanes = %d out of [0, 65535]", c->n_lanes);
+  TL_CHECK_ARG(c->n_heads >= 1 && c->n_heads <= 256, "n_heads = %d out of [1, 256]", c->n_heads);
+  if (c->head_dim != 64 && c->head_dim != 128)
+    return set_error(TL_ERR_UNSUPPORTED, "head_dim = %d: only 64 and 128 are supported", c->head_dim);
+  TL_CHECK_ARG(c->max_ctx >= 1 && c->max_ctx <= (1 << 24), "max_ctx = %d out of [1, 2^24]", c->max_ctx);
+  const size_t words = (size_t)c->n_heads * c->max_ctx * (c->head_dim / 8), params = words / 4;
+  TL_CHECK_ARG(c->n_lanes <= 1 || (c->code_stride >= words && c->param_stride >= params),
+               "lanes overlap: strides %zu and %zu words, %zu and %zu needed", c->code_stride,
+               c->param_stride, words, params);
+  TL_CHECK_ARG(c->n_lanes <= 1 || c->code_stride % 4 == 0, "code_stride = %zu must be a multiple of 4 words",
+               c->code_stride);
+  if (c->n_lanes > 0) {
+    TL_CHECK_ARG(c->k_codes && c->v_codes && c->k_params && c->v_params, "NULL device pointer");
+    TL_CHECK_ARG((((uintptr_t)c->k_codes | (uintptr_t)c->v_codes) & 15) == 0, "codes must be 16-byte aligned");
+    TL_CHECK_ARG((((uintptr_t)c->k_params | (uintptr_t)c->v_params) & 3) == 0, "parameters must be 4-byte aligned");
+  }
+  *head_words = c->n_heads * c->head_dim;
+  return ok();
+}
+
+tl_status kv4_rows(const tl_kv_int4* c, const void* k, const void* v, long row_stride, const int32_t* cu,
+                   const int32_t* pos, int n_rows, bool write, cudaStream_t s) {
+  int width;
+  TL_TRY(check_kv4(c, &width));
+  TL_CHECK_ARG(n_rows >= 0 && n_rows <= (1 << 27), "n_rows = %d out of [0, 2^27]", n_rows);
+  TL_CHECK_ARG(row_stride >= width && row_stride % 8 == 0,
+               "row_stride = %ld must be a multiple of 8, at least n_heads * head_dim = %d", row_stride, width);
+  if (n_rows == 0 || c->n_lanes == 0) return ok();
+  TL_CHECK_ARG(cu || n_rows % c->n_lanes == 0, "without cu the lanes share n_rows = %d equally: not a multiple of %d",
+               n_rows, c->n_lanes);
+  TL_CHECK_ARG(k && v && pos, "NULL device pointer");
+  TL_CHECK_ARG((((uintptr_t)k | (uintptr_t)v) & 15) == 0, "k and v must be 16-byte aligned");
+  TL_CHECK_ARG((((uintptr_t)cu | (uintptr_t)pos) & 3) == 0, "cu and pos must be 4-byte aligned");
+  Kv4RowsArgs a;
+  memset(&a, 0, sizeof(a));
+  a.k_codes = c->k_codes;
+  a.v_codes = c->v_codes;
+  a.k_params = c->k_params;
+  a.v_params = c->v_params;
+  a.code_stride = c->code_stride;
+  a.param_stride = c->param_stride;
+  a.n_lanes = c->n_lanes;
+  a.H = c->n_heads;
+  a.hd = c->head_dim;
+  a.max_ctx = c->max_ctx;
+  a.k_in = (const __half*)k;
+  a.v_in = (const __half*)v;
+  a.k_out = (__half*)k;
+  a.v_out = (__half*)v;
+  a.row_stride = row_stride;
+  a.cu = cu;
+  a.pos = pos;
+  a.n_rows = n_rows;
+  return launch_kv4_rows(a, write, s);
+}
+
+}  // namespace
+
+TL_API tl_status tl_kv_write_int4(const tl_kv_int4* cache, const uint16_t* k, const uint16_t* v, long row_stride,
+                                  const int32_t* cu, const int32_t* pos, int n_rows, tl_stream stream) {
+  return kv4_rows(cache, k, v, row_stride, cu, pos, n_rows, true, (cudaStream_t)stream);
+}
+
+TL_API tl_status tl_kv_read_int4(const tl_kv_int4* cache, uint16_t* k, uint16_t* v, long row_stride,
+                                 const int32_t* cu, const int32_t* pos, int n_rows, tl_stream stream) {
+  return kv4_rows(cache, k, v, row_stride, cu, pos, n_rows, false, (cudaStream_t)stream);
+}
+
+TL_API tl_status tl_attention_int4(const tl_kv_int4* cache, const uint16_t* q, long q_stride, int n_q, int q_heads,
+                                   const int32_t* lens, int window, uint16_t* out, long out_stride,
+                                   tl_stream stream) {
+  int width;
+  TL_TRY(check_kv4(cache, &width));
+  TL_CHECK_ARG(n_q >= 0 && n_q <= 8, "n_q = %d out of [0, 8]", n_q);
+  TL_CHECK_ARG(q_heads >= cache->n_heads && q_heads <= 1024 && q_heads % cache->n_heads == 0,
+               "q_heads = %d must be a multiple of n_heads = %d, at most 1024", q_heads, cache->n_heads);
+  TL_CHECK_ARG(window >= 0, "window = %d must be >= 0 (0: the whole context)", window);
+  const long qw = (long)q_heads * cache->head_dim;
+  TL_CHECK_ARG(q_stride >= qw && q_stride % 8 == 0 && out_stride >= qw && out_stride % 8 == 0,
+               "q_stride = %ld and out_stride = %ld must be multiples of 8, at least q_heads * head_dim = %ld",
+               q_stride, out_stride, qw);
+  if (n_q == 0 || cache->n_lanes == 0) return ok();
+  TL_CHECK_ARG(q && out && lens, "NULL device pointer");
+  TL_CHECK_ARG((((uintptr_t)q | (uintptr_t)out) & 15) == 0, "q and out must be 16-byte aligned");
+  TL_CHECK_ARG(((uintptr_t)lens & 3) == 0, "lens must be 4-byte aligned");
+  AttnInt4Args a;
+  memset(&a, 0, sizeof(a));
+  a.q = (const __half*)q;
+  a.out = (__half*)out;
+  a.q_stride = q_stride;
+  a.out_stride = out_stride;
+  a.n_rows = cache->n_lanes;
+  a.n_q = n_q;
+  a.H = cache->n_heads;
+  a.group = q_heads / cache->n_heads;
+  a.hd = cache->head_dim;
+  a.max_ctx = cache->max_ctx;
+  a.window = window;
+  a.k_codes = cache->k_codes;
+  a.v_codes = cache->v_codes;
+  a.k_params = cache->k_params;
+  a.v_params = cache->v_params;
+  a.code_stride = cache->code_stride;
+  a.param_stride = cache->param_stride;
+  a.lens = lens;
+  a.split_pairs = (int)std::min<long>((long)cache->n_lanes * cache->n_heads, 1 << 20);
+  return launch_attn_int4(a, (cudaStream_t)stream);
+}
+
+namespace {
+
+tl_status check_score(int n, int vocab, int d, int k) {
+  TL_CHECK_ARG(n >= 0 && n <= 65536, "n = %d out of [0, 65536]", n);
+  TL_CHECK_ARG(vocab >= 1 && vocab <= (1 << 24), "vocab = %d out of [1, 2^24]", vocab);
+  TL_CHECK_ARG(d >= 64 && d <= 8192 && d % 64 == 0, "d = %d must be a multiple of 64 in [64, 8192]", d);
+  TL_CHECK_ARG(k >= 0 && k <= 16 && k <= vocab, "k = %d out of [0, min(16, vocab)]", k);
+  return ok();
+}
+
+}  // namespace
+
+TL_API tl_status tl_score_head_workspace_bytes(int n, int vocab, int d, int k, size_t* bytes) {
+  TL_CHECK_ARG(bytes, "bytes is NULL");
+  TL_TRY(check_score(n, vocab, d, k));
+  *bytes = score_workspace(n, vocab, d, k);
+  return ok();
+}
+
+TL_API tl_status tl_score_head(const uint16_t* embed, int vocab, int d, const float* y, long y_stride, int n,
+                               const int32_t* targets, float* logp, float* entropy, int k, int32_t* top_ids,
+                               float* top_logp, void* workspace, size_t workspace_bytes, tl_stream stream) {
+  TL_TRY(check_score(n, vocab, d, k));
+  TL_CHECK_ARG(y_stride >= d && y_stride % 4 == 0, "y_stride = %ld must be a multiple of 4, at least d = %d", y_stride,
+               d);
+  TL_CHECK_ARG((targets == nullptr) == (logp == nullptr), "targets and logp go together");
+  if (n == 0) return ok();
+  TL_CHECK_ARG(embed && y && workspace, "NULL device pointer");
+  TL_CHECK_ARG(k == 0 || (top_ids && top_logp), "top_ids or top_logp is NULL with k = %d", k);
+  TL_CHECK_ARG((((uintptr_t)embed | (uintptr_t)y) & 15) == 0, "embed and y must be 16-byte aligned");
+  TL_CHECK_ARG(((uintptr_t)workspace & 255) == 0, "workspace must be 256-byte aligned");
+  TL_CHECK_ARG(workspace_bytes >= score_workspace(n, vocab, d, k), "workspace has %zu bytes, %zu needed",
+               workspace_bytes, score_workspace(n, vocab, d, k));
+  ScoreArgs a;
+  memset(&a, 0, sizeof(a));
+  a.E = (const __half*)embed;
+  a.V = vocab;
+  a.d = d;
+  a.y = y;
+  a.y_stride = y_stride;
+  a.n = n;
+  a.targets = targets;
+  a.logp = logp;
+  a.entropy = entropy;
+  a.k = k;
+  a.top_ids = top_ids;
+  a.top_logp = top_logp;
+  a.ws = (char*)workspace;
+  return launch_score_head(a, (cudaStream_t)stream);
+}
+
 TL_API tl_status tl_attention_prefill(const uint16_t* q, const uint16_t* k, const uint16_t* v,
                                       int T, int H, int hd, uint16_t* out, tl_stream stream) {
   TL_CHECK_ARG(T >= 0 && T <= 8192, "T = %d out of [0, 8192]", T);
@@ -529,6 +694,11 @@ void kv_geometry_hd(int H, int hd, int max_ctx, int dtype, size_t* layer, size_t
     *layer = *region;
     return;
   }
+  if (dtype == TL_KV_INT4) {   // codes [H][max_ctx][hd / 2 bytes], parameters [H][max_ctx][hd / 32][2]
+    *region = align256((size_t)H * max_ctx * hd / 2);
+    *layer = 2 * *region + 2 * align256((size_t)H * max_ctx * (hd / 32) * 4);
+    return;
+  }
   size_t esz = dtype == TL_KV_INT8 ? 1 : 2;
   size_t r = align256((size_t)H * max_ctx * hd * esz);
   size_t l = 2 * r;
@@ -558,6 +728,10 @@ size_t h_workspace_bytes(const tl_model* m, int n_lanes, int max_ctx, size_t* la
   return *part_off + align256(part * 2 * m->d * sizeof(float));
 }
 
+bool known_kv_dtype(int dtype) {
+  return dtype == TL_KV_FP16 || dtype == TL_KV_INT8 || dtype == TL_KV_H || dtype == TL_KV_INT4;
+}
+
 tl_status check_kv_args(const tl_model* m, int n_lanes, int max_ctx, const int* L, int dtype) {
   TL_CHECK_ARG(m, "NULL model");
   TL_CHECK_ARG(n_lanes >= 1 && n_lanes <= kMaxLanes, "n_lanes = %d out of [1, %d]", n_lanes,
@@ -568,8 +742,7 @@ tl_status check_kv_args(const tl_model* m, int n_lanes, int max_ctx, const int* 
   for (int b = 0; b < n_lanes; ++b)
     TL_CHECK_ARG(L[b] >= 1 && L[b] <= m->desc.max_L, "L_per_lane[%d] = %d out of [1, %d]", b,
                  L[b], m->desc.max_L);
-  TL_CHECK_ARG(dtype == TL_KV_FP16 || dtype == TL_KV_INT8 || dtype == TL_KV_H,
-               "unknown KV dtype %d", dtype);
+  TL_CHECK_ARG(known_kv_dtype(dtype), "unknown KV dtype %d", dtype);
   return ok();
 }
 
@@ -579,8 +752,9 @@ TL_API tl_status tl_kv_layer_bytes(int n_heads, int head_dim, int max_ctx, tl_kv
                                    size_t* bytes) {
   TL_CHECK_ARG(bytes, "bytes is NULL");
   TL_CHECK_ARG(n_heads >= 1 && head_dim >= 1 && max_ctx >= 1, "sizes must be positive");
-  TL_CHECK_ARG(dtype == TL_KV_FP16 || dtype == TL_KV_INT8 || dtype == TL_KV_H,
-               "unknown KV dtype %d", dtype);
+  TL_CHECK_ARG(known_kv_dtype(dtype), "unknown KV dtype %d", dtype);
+  TL_CHECK_ARG(dtype != TL_KV_INT4 || head_dim % 32 == 0,
+               "head_dim = %d: a 4-bit cache has groups of 32", head_dim);
   size_t region;
   kv_geometry_hd(n_heads, head_dim, max_ctx, dtype, bytes, &region);
   return ok();
@@ -690,7 +864,7 @@ TL_API tl_status tl_kv_layer_ptrs(const tl_kv* kv, int lane, int layer, void** k
   char* base = kv->buffer + kKvHeaderBytes + (size_t)(cum + layer) * kv->layer_bytes;
   *k = base;
   *v = kv->dtype == TL_KV_H ? nullptr : base + kv->region_bytes;
-  if (kv->dtype == TL_KV_INT8) {
+  if (kv->dtype == TL_KV_INT8 || kv->dtype == TL_KV_INT4) {
     size_t sreg = (kv->layer_bytes - 2 * kv->region_bytes) / 2;
     *k_scale = (uint16_t*)(base + 2 * kv->region_bytes);
     *v_scale = (uint16_t*)(base + 2 * kv->region_bytes + sreg);
@@ -835,6 +1009,7 @@ tl_status enqueue_block_body(tl_model* m, const tl_block* b, int layer, int rows
     r.layer = layer;
     r.max_ctx = kv->max_ctx;
     r.kv_int8 = kv->dtype == TL_KV_INT8;
+    r.kv_int4 = kv->dtype == TL_KV_INT4;
   }
   r.lane = lane;
   TL_TRY(launch_rope_kv(r, s));
@@ -934,6 +1109,57 @@ tl_status rebuild_kv(tl_model* m, const tl_block_desc& bd, int layer, int rows, 
   return ok();
 }
 
+// Decode attention of a 4-bit cache: RoPE and the append of every row's entry,
+// then the attention over the stored entries.  split_attn: the rows are
+// consecutive tokens of one lane, which its cache is read once for.
+tl_status enqueue_int4_attention(tl_model* m, int layer, int rows, tl_kv* kv, const RowMap* rm,
+                                 const int32_t* lane_of_row, bool split_attn, cudaStream_t s) {
+  RopeKvArgs r;
+  memset(&r, 0, sizeof(r));
+  r.part = m->part;
+  r.S = 1;
+  r.rows = rows;
+  r.d = m->d;
+  r.H = m->H;
+  r.hd = m->hd;
+  r.rope_cs = m->rope;
+  r.q = m->q;
+  r.kv_base = kv->buffer + kKvHeaderBytes;
+  r.hdr = (const KvHeader*)kv->buffer;
+  r.layer_bytes = kv->layer_bytes;
+  r.kv_region_bytes = kv->region_bytes;
+  r.layer = layer;
+  r.max_ctx = kv->max_ctx;
+  r.kv_int4 = 1;
+  r.lane_of_row = lane_of_row;
+  r.lane = rm->lane[0];
+  r.decode = split_attn ? 2 : 1;
+  TL_TRY(launch_rope_kv(r, s));
+  AttnInt4Args a;
+  memset(&a, 0, sizeof(a));
+  a.q = m->q;
+  a.out = m->attn;
+  a.q_stride = a.out_stride = m->d;
+  a.n_rows = split_attn ? 1 : rows;
+  a.n_q = split_attn ? rows : 1;
+  a.H = m->H;
+  a.group = 1;
+  a.hd = m->hd;
+  a.max_ctx = kv->max_ctx;
+  a.hdr = r.hdr;
+  a.kv_base = r.kv_base;
+  a.layer_bytes = kv->layer_bytes;
+  a.region_bytes = kv->region_bytes;
+  a.layer = layer;
+  for (int i = 0; i < kMaxLanes; ++i) {
+    a.row_lane[i] = rm->lane[i];
+    a.row_cum[i] = rm->cum[i];
+  }
+  // a lane's split must not depend on how many lanes run
+  a.split_pairs = 4 * m->H;
+  return launch_attn_int4(a, s);
+}
+
 // One decode block application for `rows` active rows: four decode
 // projections (the QKV and gate/up ones form their own pre-norm from the
 // residual stream; the O and down ones add into it) around the fused decode
@@ -973,6 +1199,7 @@ tl_status enqueue_decode_layer(tl_model* m, const tl_block* b, int layer, int ro
   p.ex = exit_args(m, layer, 0);
   p.x_out = nullptr;
   if (store_h) TL_TRY(rebuild_kv(m, bd, layer, rows, kv, rm, odd, s));
+  if (kv->dtype == TL_KV_INT4) TL_TRY(enqueue_int4_attention(m, layer, rows, kv, rm, lane_of_row, split_attn, s));
   // RoPE, KV append, split attention and merge in one launch
   DecodeAttnArgs da;
   memset(&da, 0, sizeof(da));
@@ -1008,7 +1235,9 @@ tl_status enqueue_decode_layer(tl_model* m, const tl_block* b, int layer, int ro
     for (int i = 0; i < kMaxLanes; ++i) da.row_cum[i] = rm->lane[i];
     da.late_prefetch = 1;
   }
-  if (!split_attn) {
+  if (kv->dtype == TL_KV_INT4) {
+    // done above
+  } else if (!split_attn) {
     da.mode = 0;
     TL_TRY(launch_attn_decode_fused(da, s));
   } else {

@@ -6,6 +6,7 @@
 //
 // Every reduction runs in a fixed order that depends only on the row length,
 // so a row's result never depends on how many rows share the launch.
+#include "kv_int4.cuh"
 #include "kv_quant.cuh"
 #include "tl_launch.cuh"
 
@@ -202,8 +203,12 @@ __global__ void rope_kv_kernel(RopeKvArgs a) {
   pdl_enter();
   if (!active) return;
   if (a.decode) {
-    kv_lane = a.lane_of_row[row];
-    pos = a.hdr->pos[kv_lane];
+    if (a.decode == 1) {
+      kv_lane = a.lane_of_row[row];
+      pos = a.hdr->pos[kv_lane];
+    } else {
+      pos = a.hdr->pos[kv_lane] + row;
+    }
 #pragma unroll
     for (int p = 0; p < 2; ++p)
       if (p < npair) csp[p] = a.rope_cs[(size_t)pos * half + lane + 32 * p];
@@ -279,7 +284,48 @@ __global__ void rope_kv_kernel(RopeKvArgs a) {
   if (!a.kv_base) return;
   char* layer = a.kv_base + (size_t)(cum + a.layer) * a.layer_bytes;
   const size_t eoff = ((size_t)head * a.max_ctx + pos) * a.hd;
-  if (!a.kv_int8) {
+  if (a.kv_int4) {
+    // the 32 lanes of (p, hh) are one group of the row: group p + hh * npair
+    const size_t slot = (size_t)head * a.max_ctx + pos;
+    uint32_t* kc = reinterpret_cast<uint32_t*>(layer) + slot * (a.hd / 8);
+    uint32_t* vc = reinterpret_cast<uint32_t*>(layer + a.kv_region_bytes) + slot * (a.hd / 8);
+    uint32_t* kp = reinterpret_cast<uint32_t*>(layer + 2 * a.kv_region_bytes) + slot * (a.hd / kInt4Group);
+    uint32_t* vp = reinterpret_cast<uint32_t*>(layer + a.kv_region_bytes + a.layer_bytes / 2) +
+                   slot * (a.hd / kInt4Group);
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      if (p < npair) {
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          const int grp = p + hh * npair;
+          const __half2 kv = __halves2half2(kh[p][hh], vh[p][hh]);   // K and V reduced together
+          __half2 mn = kv, mx = kv;
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) {
+            mn = __hmin2_nan(mn, kv_bits_h2(__shfl_xor_sync(0xffffffffu, kv_h2_bits(mn), o)));
+            mx = __hmax2_nan(mx, kv_bits_h2(__shfl_xor_sync(0xffffffffu, kv_h2_bits(mx), o)));
+          }
+          const Int4Group gk = kv_int4_group(__low2float(mn), __low2float(mx));
+          const Int4Group gv = kv_int4_group(__high2float(mn), __high2float(mx));
+          uint32_t wk = kv_int4_code(__low2float(kv), gk) << (4 * (lane & 7));
+          uint32_t wv = kv_int4_code(__high2float(kv), gv) << (4 * (lane & 7));
+#pragma unroll
+          for (int o = 1; o < 8; o <<= 1) {
+            wk |= __shfl_xor_sync(0xffffffffu, wk, o);
+            wv |= __shfl_xor_sync(0xffffffffu, wv, o);
+          }
+          if ((lane & 7) == 0) {
+            kc[4 * grp + (lane >> 3)] = wk;
+            vc[4 * grp + (lane >> 3)] = wv;
+          }
+          if (lane == 0) {
+            kp[grp] = gk.param;
+            vp[grp] = gv.param;
+          }
+        }
+      }
+    }
+  } else if (!a.kv_int8) {
     __half* K = reinterpret_cast<__half*>(layer) + eoff;
     __half* V = reinterpret_cast<__half*>(layer + a.kv_region_bytes) + eoff;
 #pragma unroll

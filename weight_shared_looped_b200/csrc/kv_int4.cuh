@@ -1,0 +1,80 @@
+// The 4-bit KV cache format: one K or V row of a (token, head) in groups of 32
+// values, each group asymmetric with an fp16 scale and an fp16 zero point.
+//
+//   lo, hi = least and largest value of the group (fp16 values, widened to fp32)
+//   scale  = fp16, rounded towards zero, of fl32((hi - lo) / 15);   zero = lo
+//   code   = clamp(rint(fl32(fl32(x - lo) * fl32(1 / scale))), 0, 15)   (0 when scale == 0)
+//   value  = zero + code * scale
+//
+// Every step is an IEEE fp32 operation, so codes and parameters are a pure
+// function of the row: the standalone writer, the prefill append and the
+// decode append give the same bits.  The scale is rounded towards zero so that
+// no value leaves [lo, hi] (with a scale rounded up, a group that spans the
+// fp16 range would read back as infinity); that costs at most 15 * 2^-10 of a
+// step at the group's upper end.  A zero point of -0 is stored as +0, which
+// keeps the bits independent of the order of the minimum.  A group holding a
+// NaN or an infinity gets NaN parameters and codes 0: whoever attends it sees
+// NaN, nobody a plausible number.
+//
+// Layout: code words as the packed INT4 weights have them (word j of a row
+// holds elements 8j .. 8j + 7, element 8j + i in bits 4i .. 4i + 3), unsigned;
+// parameters one 32-bit pair per group, scale in the low half.
+#pragma once
+
+#include <cuda_fp16.h>
+#include <math_constants.h>
+#include <stdint.h>
+
+namespace tl {
+
+constexpr int kInt4Group = 32;
+
+struct Int4Group {
+  float lo, inv;      // code = rint((x - lo) * inv)
+  uint32_t param;     // scale | zero << 16
+};
+
+// lo, hi: the group's extremes as fp32 (NaN if any value is NaN)
+__device__ __forceinline__ Int4Group kv_int4_group(float lo, float hi) {
+  Int4Group g;
+  const float range = __fsub_rn(hi, lo);
+  if (!(range < CUDART_INF_F)) {   // NaN, infinities of either sign
+    g.lo = 0.f;
+    g.inv = 0.f;
+    g.param = 0x7fff7fffu;
+    return g;
+  }
+  const __half s = __float2half_rz(__fdiv_rn(range, 15.0f));
+  const float sf = __half2float(s);
+  g.lo = lo;
+  g.inv = sf > 0.f ? __frcp_rn(sf) : 0.f;
+  const __half z = __float2half_rn(__fadd_rn(lo, 0.f));
+  g.param = (uint32_t)__half_as_ushort(s) | ((uint32_t)__half_as_ushort(z) << 16);
+  return g;
+}
+
+__device__ __forceinline__ uint32_t kv_int4_code(float x, const Int4Group& g) {
+  // inv == 0 also covers a group with NaN parameters, where x itself may be NaN
+  if (g.inv == 0.f) return 0u;
+  const float r = rintf(__fmul_rn(__fsub_rn(x, g.lo), g.inv));
+  return (uint32_t)fminf(fmaxf(r, 0.f), 15.f);
+}
+
+__device__ __forceinline__ uint32_t kv_h2_bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
+__device__ __forceinline__ __half2 kv_bits_h2(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
+
+// The codes in bits 0-3 (LOW) or 4-7 of both halves of x, as an exact fp16
+// pair: the nibble becomes the low mantissa bits of 1024 (1024 + c, or
+// 1024 + 16 c), and one exact half2 operation takes the rest away.
+template <bool LOW>
+__device__ __forceinline__ __half2 kv_int4_pair(uint32_t x) {
+  uint32_t v;
+  if (LOW) {
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(v) : "r"(x), "r"(0x000F000Fu), "r"(0x64006400u));
+    return __hadd2(kv_bits_h2(v), __float2half2_rn(-1024.f));
+  }
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(v) : "r"(x), "r"(0x00F000F0u), "r"(0x64006400u));
+  return __hfma2(kv_bits_h2(v), __float2half2_rn(0.0625f), __float2half2_rn(-64.f));
+}
+
+}  // namespace tl

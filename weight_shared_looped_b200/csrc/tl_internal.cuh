@@ -208,9 +208,11 @@ struct RopeKvArgs {
   const KvHeader* hdr;
   size_t layer_bytes, kv_region_bytes;   // region = K or V array bytes (256-aligned)
   int layer, max_ctx, kv_int8;
+  int kv_int4;
   const int32_t* lane_of_row;  // decode: lane of each row; null = prefill of `lane`
   int lane;
-  int decode;                  // 1: position = hdr->pos[lane]; 0: position = row index
+  int decode;                  // 1: position = hdr->pos[lane]; 0: position = row index;
+                               // 2: position = hdr->pos[lane] + row index (rows of one lane)
   int kv_only;                 // 1: part holds [S][rows][2d] K|V sums only; no q is written
   int pos0;                    // decode == 0: position = pos0 + row index
 };
@@ -264,6 +266,61 @@ struct DecodeAttnArgs {
   int* status;               // null, or the status word a timed-out merge wait sets
 };
 tl_status launch_attn_decode_fused(const DecodeAttnArgs& a, cudaStream_t s);
+
+// 4-bit KV cache (kv_int4.cu): packed fp16 rows to or from the lanes' caches
+struct Kv4RowsArgs {
+  uint32_t *k_codes, *v_codes;     // [lane][H][max_ctx][hd / 8], lanes code_stride words apart
+  uint32_t *k_params, *v_params;   // [lane][H][max_ctx][hd / 32], lanes param_stride words apart
+  size_t code_stride, param_stride;
+  int n_lanes, H, hd, max_ctx;
+  const __half *k_in, *v_in;       // write: rows [n_rows][row_stride]
+  __half *k_out, *v_out;           // read: the same
+  long row_stride;
+  const int32_t* cu;               // [n_lanes + 1] first row of each lane, or null: equal shares
+  const int32_t* pos;              // [n_lanes] position of each lane's first row
+  int n_rows;
+};
+tl_status launch_kv4_rows(const Kv4RowsArgs& a, bool write, cudaStream_t s);
+
+// attention over a 4-bit cache (attention_int4.cu): n_q queries per row (lane),
+// query i at position length - n_q + i
+struct AttnInt4Args {
+  const __half* q;                 // [n_rows * n_q][q_stride], query head h at h * hd
+  __half* out;                     // [n_rows * n_q][out_stride]
+  long q_stride, out_stride;
+  int n_rows, n_q, H, group, hd, max_ctx, window;   // group: query heads per cache head
+  // caller's cache (hdr null): lanes as in Kv4RowsArgs, lengths on the device
+  const uint32_t *k_codes, *v_codes, *k_params, *v_params;
+  size_t code_stride, param_stride;
+  const int32_t* lens;             // [n_rows]
+  // a model's cache: row r is lane row_lane[r], its length hdr->pos + n_q
+  const KvHeader* hdr;
+  const char* kv_base;
+  size_t layer_bytes, region_bytes;
+  int layer;
+  int row_lane[kMaxLanes], row_cum[kMaxLanes];
+  int split_pairs;                 // (lane, cache head) pairs the work split is chosen for
+  int col_tiles;                   // set by the launcher
+};
+void attn_int4_split(int max_ctx, int pairs, int* cls, int* nw);
+tl_status launch_attn_int4(const AttnInt4Args& a, cudaStream_t s);
+
+// scoring head (score_head.cu): log probabilities under logits y . E
+struct ScoreArgs {
+  const __half* E;                 // [V][d]
+  int V, d;
+  const float* y;                  // [n][y_stride]
+  long y_stride;
+  int n;
+  const int32_t* targets;          // [n] or null
+  float *logp, *entropy;           // [n] or null
+  int k;
+  int32_t* top_ids;                // [n][k]
+  float* top_logp;
+  char* ws;
+};
+size_t score_workspace(int n, int V, int d, int k);
+tl_status launch_score_head(const ScoreArgs& a, cudaStream_t s);
 
 // read-bandwidth probe (probe.cu)
 tl_status launch_read_probe(const void* buf, size_t bytes, int passes, uint32_t* sink,

@@ -9,12 +9,13 @@ from typing import Dict, List, Optional, Sequence
 import numpy as np
 import torch
 
-from . import (TL_KV_FP16, TL_KV_INT8, TL_KV_H, tl_block_create, tl_block_destroy, tl_decode_step,
+from . import (TL_KV_FP16, TL_KV_INT4, TL_KV_INT8, TL_KV_H, tl_block_create, tl_block_destroy, tl_decode_step,
                tl_kv_bytes, tl_kv_create, tl_kv_destroy, tl_kv_layer_ptrs, tl_kv_position,
                tl_kv_reset, tl_kv_set_position, tl_model_create, tl_model_destroy,
                tl_model_device_bytes, tl_model_set_decode_chunks, tl_model_set_graphs,
                tl_pack_weights, tl_packed_bytes, tl_prefill, tl_sync_status, tl_extend,
                tl_greedy_head, tl_spec_step, tl_model_set_exit_threshold, tl_loops_used,
+               tl_score_head, tl_score_head_workspace_bytes,
                tl_sign_bits_bytes, tl_pack_sign_bits, tl_model_set_cross_iter,
                tl_model_set_iteration_blocks)
 
@@ -149,6 +150,27 @@ class DeviceModel:
         tl_greedy_head(self.handle, y, ids, stream=stream)
         return ids
 
+    def score(self, y, targets=None, k: int = 0, stream=None) -> Dict[str, torch.Tensor]:
+        """Log probabilities under the tied embedding of final-norm outputs y fp32 [n, d]:
+        "logp" of the given tokens (targets int32 [n], -1: none), the distributions' "entropy",
+        and the k most probable tokens, "ids" and "top"."""
+        if self.embed is None:
+            raise ValueError("the model has no embedding to use as its head")
+        n, dev = y.shape[0], y.device
+        out = {"entropy": torch.empty(n, dtype=torch.float32, device=dev)}
+        if targets is not None:
+            out["logp"] = torch.empty(n, dtype=torch.float32, device=dev)
+        if k:
+            out["ids"] = torch.empty(n, k, dtype=torch.int32, device=dev)
+            out["top"] = torch.empty(n, k, dtype=torch.float32, device=dev)
+        ws = torch.empty(tl_score_head_workspace_bytes(n, self.embed.shape[0], self.d, k),
+                         dtype=torch.uint8, device=dev)
+        if stream is not None and not isinstance(stream, int):
+            ws.record_stream(stream)   # freed at return, used until the stream gets there
+        tl_score_head(self.embed, y, targets, out.get("logp"), out["entropy"], out.get("ids"),
+                      out.get("top"), ws, stream=stream)
+        return out
+
     def spec_step(self, kv: "DeviceKV", token: int, *, lane: int = 0, K: int, L_draft: int,
                   L_verify: int, stream=None):
         return tl_spec_step(self.handle, kv.handle, lane, token, K, L_draft, L_verify,
@@ -167,7 +189,7 @@ class DeviceKV:
     def __init__(self, model: DeviceModel, L_per_lane: Sequence[int], max_ctx: int,
                  dtype: str = "fp16"):
         self.model = model
-        self.dtype = {"int8": TL_KV_INT8, "h": TL_KV_H}.get(dtype, TL_KV_FP16)
+        self.dtype = {"int8": TL_KV_INT8, "int4": TL_KV_INT4, "h": TL_KV_H}.get(dtype, TL_KV_FP16)
         self.L = list(L_per_lane)
         self.max_ctx = max_ctx
         nbytes = tl_kv_bytes(model.handle, max_ctx, self.L, self.dtype)
