@@ -33,10 +33,7 @@
 // Every wait on an mbarrier is bounded: when a wait runs out the CTA records
 // TL_ERR_TIMEOUT, stops issuing work, waits (bounded) for its copies in
 // flight, frees its TMEM and returns.
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
-#include "tl_launch.cuh"
+#include "tc_util.cuh"
 
 namespace tl {
 namespace {
@@ -51,81 +48,10 @@ constexpr int TMEM_COLS = 512;     // the whole of TMEM: one CTA per SM
 constexpr int A_COLS = BK / 2;     // TMEM columns per A stage (two fp16 per column)
 constexpr int BATCH = DQ_GROUPS;   // k blocks per batch: one per dequantisation group
 constexpr size_t kMinSmem = 120 * 1024;   // also keeps it to one CTA per SM
-constexpr uint64_t kWaitLimitNs = 2000000000ull;   // a bounded wait gives up after 2 s
 template <int BN> struct TcCfg {
   static constexpr int X_STAGES = BN >= 128 ? 12 : 16;        // activation ring (k blocks)
   static constexpr int A_BATCHES = (TMEM_COLS - BN) / (A_COLS * BATCH);   // TMEM A ring (batches)
 };
-
-__device__ __forceinline__ uint64_t globaltimer_ns() {
-  uint64_t t;
-  asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
-  return t;
-}
-
-__device__ __forceinline__ uint32_t smem_u32(const void* p) {
-  return (uint32_t)__cvta_generic_to_shared(p);
-}
-
-__device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {
-  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(count));
-}
-
-__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
-
-// Bounded wait for the phase with the given parity to complete: false after
-// limit_ns of global time.
-__device__ __forceinline__ bool mbar_try(uint32_t addr, uint32_t parity) {
-  uint32_t done;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-      " selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(done)
-      : "r"(addr), "r"(parity)
-      : "memory");
-  return done != 0;
-}
-
-// Bounded wait for the phase with the given parity to complete: false after
-// limit_ns of global time.  The clock is read only once the first try fails.
-__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity,
-                                          uint64_t limit_ns = kWaitLimitNs) {
-  const uint32_t addr = smem_u32(bar);
-  if (mbar_try(addr, parity)) return true;
-  const uint64_t start = globaltimer_ns();
-  for (uint32_t i = 1;; ++i) {
-    if (mbar_try(addr, parity)) return true;
-    if ((i & 63) == 0 && globaltimer_ns() - start > limit_ns) return false;
-  }
-}
-
-// The producer and MMA warps run their loops with all 32 lanes converged and
-// issue each TMA copy, MMA and commit from one lane chosen by elect.sync: a
-// lone active lane issues far more slowly while the dequantisation warps on
-// the same SM sub-partition keep its issue slots busy.
-__device__ __forceinline__ void tma_issue_elect(uint64_t* bar, uint32_t bytes, void* dst,
-                                                const CUtensorMap* map, int x, int y) {
-  asm volatile(
-      "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
-      " @e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n"
-      " @e cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%2], [%3, "
-      "{%4, %5}], [%0];\n}\n" ::"r"(smem_u32(bar)),
-      "r"(bytes), "r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y)
-      : "memory");
-}
-
-__device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t addr) {
-  // K-major, 128-byte swizzle: rows of 128 bytes, 8-row groups 1024 bytes apart
-  uint64_t d = 0;
-  d |= (uint64_t)((addr >> 4) & 0x3FFF);
-  d |= (uint64_t)1 << 16;                 // leading byte offset (unused for this layout)
-  d |= (uint64_t)(1024 >> 4) << 32;       // stride byte offset
-  d |= (uint64_t)1 << 46;                 // descriptor version for sm_100
-  d |= (uint64_t)2 << 61;                 // SWIZZLE_128B
-  return d;
-}
 
 // The four K=16 MMAs of one 64-wide k block (A columns +8, B descriptor +2
 // (32 bytes) per step), then a commit that frees the block's activation slot;
@@ -149,24 +75,6 @@ __device__ __forceinline__ void mma_kblock(uint32_t d_tmem, uint32_t a_tmem, uin
       : "memory");
 }
 
-__device__ __forceinline__ void mma_commit_elect(uint64_t* bar) {
-  asm volatile(
-      "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
-      " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(
-          smem_u32(bar))
-      : "memory");
-}
-
-// Bounded wait (when needed) by lane 0 with the outcome (and the CTA's abort flag) broadcast
-// to the warp, so the warp stays converged.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const int* abort_flag,
-                                          bool needed) {
-  bool ok = true;
-  if ((threadIdx.x & 31) == 0)
-    ok = (!needed || mbar_wait(bar, parity)) && !*(volatile const int*)abort_flag;
-  return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-}
-
 struct TcArgs {
   int N, K, G, T, n_split;   // n_split % 128 == 0
   int wpr;                   // packed words per row (K / 8 for INT4, the padded INT3 row)
@@ -181,14 +89,6 @@ struct TcArgs {
   int* status;
   __half* swiglu_u;          // fused SwiGLU epilogue: fp16 [T][n_split] (N = 2 * n_split)
 };
-
-// The elected lane arrives once on a barrier for the whole warp.
-__device__ __forceinline__ void mbar_arrive_elect(uint64_t* bar) {
-  asm volatile(
-      "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
-      " @e mbarrier.arrive.shared::cta.b64 _, [%0];\n}\n" ::"r"(smem_u32(bar))
-      : "memory");
-}
 
 // Cross-iteration rounding: the odd-iteration code is code + 1 where the
 // sign-of-frac bit is set and code - 1 where it is clear.  A k block's 64
@@ -651,6 +551,8 @@ tl_status get_encoder() {
   return ok();
 }
 
+}  // namespace
+
 tl_status encode_2d(CUtensorMap* map, CUtensorMapDataType dt, const void* base, uint64_t inner,
                     uint64_t outer, uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer,
                     CUtensorMapSwizzle swz) {
@@ -665,6 +567,8 @@ tl_status encode_2d(CUtensorMap* map, CUtensorMapDataType dt, const void* base, 
   if (r != CUDA_SUCCESS) return set_error(TL_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
   return ok();
 }
+
+namespace {
 
 int tc_tile_n(int T) { return T <= 64 ? 64 : 128; }
 
