@@ -37,9 +37,13 @@ __device__ __forceinline__ bool sc_better(float x, int v, float bx, int bv) {
   return x > bx || (x == bx && v < bv);
 }
 
-// slice record of one row: m, l, s (base 2, s in units of log2), then kc
-// candidates (logit, id), best first
-__host__ __device__ inline int rec_words(int kc) { return 3 + 2 * kc; }
+// Slice records: stat[row][slice] = (m, l, s) in base 2 (s in units of log2);
+// top_x, top_v[row][rank][slice] = the slice's best kc candidates by rank.
+struct ScoreRec {
+  float4* stat;
+  float* top_x;
+  int* top_v;
+};
 
 __device__ __forceinline__ float sc_ex2(float x) {
   float y;
@@ -105,29 +109,35 @@ __global__ void __launch_bounds__(256) score_split_kernel(const float* __restric
 }
 
 // ------------------------------------------------------------------ pass 1
-__device__ __forceinline__ void sc_mma_elect(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+// One thread issues the copies and one the MMAs: a lone lane has its SM
+// sub-partition nearly to itself here, and its loop is shorter than a converged
+// warp's with an election per instruction (a stage took 830 cycles that way,
+// waits included, however small its copies).
+__device__ __forceinline__ void sc_mma(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
   asm volatile(
-      "{\n .reg .pred p, e;\n setp.ne.b32 p, %4, 0;\n elect.sync _|e, 0xffffffff;\n"
-      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
       "l"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u)
       : "memory");
 }
-
-// one expect_tx for two copies of the stage, then the copies
-__device__ __forceinline__ void sc_expect_elect(uint64_t* bar, uint32_t bytes) {
-  asm volatile(
-      "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
-      " @e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n}\n" ::"r"(smem_u32(bar)),
-      "r"(bytes)
-      : "memory");
+__device__ __forceinline__ void sc_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+               : "memory");
 }
-__device__ __forceinline__ void sc_copy_elect(uint64_t* bar, void* dst, const CUtensorMap* map, int x, int y) {
+__device__ __forceinline__ void sc_expect(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void sc_copy(uint64_t* bar, void* dst, const CUtensorMap* map, int x, int y) {
   asm volatile(
-      "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
-      " @e cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%1], [%2, "
-      "{%3, %4}], [%0];\n}\n" ::"r"(smem_u32(bar)),
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%1], [%2, {%3, %4}], [%0];" ::"r"(
+          smem_u32(bar)),
       "r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y)
       : "memory");
+}
+// a bounded wait by one thread; false once it ran out or another role gave up
+__device__ __forceinline__ bool sc_wait(uint64_t* bar, uint32_t parity, const int* abort_flag) {
+  if (mbar_try(smem_u32(bar), parity)) return true;
+  return mbar_wait(bar, parity) && !*(volatile const int*)abort_flag;
 }
 
 __device__ __forceinline__ void sc_ld16(uint32_t* u, uint32_t addr) {
@@ -163,12 +173,12 @@ struct ScoreTc {
   int pad;                // rows of one activation part
   int bn;                 // vocabulary entries per tile
   int vt;                 // tiles of the vocabulary
-  int units, upc;         // (row tile, vocabulary tile) units, and how many a CTA takes
+  int mt, groups;         // row tiles; CTAs that share one row tile's vocabulary tiles
   int stages;
   uint32_t stage_bytes;
   int slices;             // records per row
   const float* scale;
-  float* rec;
+  ScoreRec rec;
   int* flag;              // set when a bounded wait ran out
 };
 
@@ -185,6 +195,7 @@ struct ScoreBars {
 // w / 4), warp 8 copies, warp 9 issues the MMAs; two accumulators of 256 columns
 // let the epilogue of one tile run under the next tile's MMAs.
 constexpr int SR_THREADS = 320;
+constexpr int SR_QUEUE = 12;       // newcomers a statistics thread can hold
 
 template <int KC>
 __global__ void __launch_bounds__(SR_THREADS, 1)
@@ -193,7 +204,9 @@ __global__ void __launch_bounds__(SR_THREADS, 1)
   __shared__ ScoreBars bars;
   uint8_t* smem = (uint8_t*)(((uintptr_t)sr_raw + 1023) & ~(uintptr_t)1023);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int u0 = blockIdx.x * a.upc, u1 = min(a.units, u0 + a.upc);
+  // row tile blockIdx.x mod mt, every groups-th vocabulary tile: the CTAs of one
+  // group read the same embedding tile together, so it leaves HBM once
+  const int mt = blockIdx.x % a.mt, group = blockIdx.x / a.mt;
   if (threadIdx.x == 0) {
     for (int s = 0; s < a.stages; ++s) {
       mbar_init(&bars.full[s], 1);
@@ -219,87 +232,112 @@ __global__ void __launch_bounds__(SR_THREADS, 1)
 
   if (warp == 8) {
     // ---------------------------------------------------------------- copies
-    int s = 0, it = 0, issued = 0;
-    bool ok = true;
-    for (int u = u0; u < u1 && ok; ++u) {
-      const int r0 = u / a.vt * 128, v0 = u % a.vt * a.bn;
-      for (int kb = 0; kb < a.nkb; ++kb) {
-        if (!warp_wait(&bars.empty[s], (it & 1) ^ 1, &bars.abort, it > 0)) {
-          if (lane == 0) atomicExch(&bars.abort, 1);
-          ok = false;
-          break;
-        }
-        uint8_t* st = smem + (size_t)s * a.stage_bytes;
-        sc_expect_elect(&bars.full[s], a.stage_bytes);
-        sc_copy_elect(&bars.full[s], st, &map_y, kb * SC_BK, r0);
-        sc_copy_elect(&bars.full[s], st + 16384, &map_y, kb * SC_BK, a.pad + r0);
-        sc_copy_elect(&bars.full[s], st + 32768, &map_e, kb * SC_BK, v0);
-        ++issued;
-        if (++s == a.stages) {
-          s = 0;
-          ++it;
+    if (lane == 0) {
+      int s = 0, ph = 1, issued = 0;
+      bool ok = true;
+      const int r0 = mt * 128;
+      for (int vt = group; vt < a.vt && ok; vt += a.groups) {
+        const int v0 = vt * a.bn;
+        for (int kb = 0; kb < a.nkb; ++kb) {
+          if (issued >= a.stages && !sc_wait(&bars.empty[s], ph, &bars.abort)) {
+            ok = false;
+            break;
+          }
+          uint8_t* st = smem + (size_t)s * a.stage_bytes;
+          sc_expect(&bars.full[s], a.stage_bytes);
+          sc_copy(&bars.full[s], st, &map_y, kb * SC_BK, r0);
+          sc_copy(&bars.full[s], st + 16384, &map_y, kb * SC_BK, a.pad + r0);
+          sc_copy(&bars.full[s], st + 32768, &map_e, kb * SC_BK, v0);
+          ++issued;
+          if (++s == a.stages) {
+            s = 0;
+            ph ^= 1;
+          }
         }
       }
+      if (!ok) atomicExch(&bars.abort, 1);
+      if (*(volatile int*)&bars.abort)               // the copies still in flight land before the CTA leaves
+        for (int i = max(0, issued - a.stages); i < issued; ++i) mbar_wait(&bars.full[i % a.stages], (i / a.stages) & 1);
     }
-    if (lane == 0 && *(volatile int*)&bars.abort)      // the copies still in flight land before the CTA leaves
-      for (int i = max(0, issued - a.stages); i < issued; ++i) mbar_wait(&bars.full[i % a.stages], (i / a.stages) & 1);
     __syncwarp();
   } else if (warp == 9) {
     // ---------------------------------------------------------------- MMAs
-    const uint32_t idesc = (1u << 4) | ((uint32_t)(a.bn >> 3) << 17) | (8u << 24);
-    int s = 0, ph = 0;
-    bool ok = true;
-    for (int u = u0; u < u1 && ok; ++u) {
-      const int buf = (u - u0) & 1, use = (u - u0) >> 1;
-      ok = warp_wait(&bars.acc_empty[buf], (use & 1) ^ 1, &bars.abort, use > 0);
-      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-      const uint32_t acc = tmem + buf * 256;
-      for (int kb = 0; kb < a.nkb && ok; ++kb) {
-        ok = warp_wait(&bars.full[s], ph, &bars.abort, true);
-        if (!ok) break;
+    if (lane == 0) {
+      const uint32_t idesc = (1u << 4) | ((uint32_t)(a.bn >> 3) << 17) | (8u << 24);
+      const uint64_t desc0 = smem_desc_sw128(smem_u32(smem));   // + stage bytes / 16 per stage: stays below 2^14
+      int s = 0, ph = 0, i = 0;
+      bool ok = true;
+      for (int vt = group; vt < a.vt && ok; vt += a.groups, ++i) {
+        const int buf = i & 1, use = i >> 1;
+        if (use > 0) ok = sc_wait(&bars.acc_empty[buf], (use & 1) ^ 1, &bars.abort);
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        const uint32_t st = smem_u32(smem + (size_t)s * a.stage_bytes);
-        const uint64_t hi = smem_desc_sw128(st), lo = smem_desc_sw128(st + 16384), e = smem_desc_sw128(st + 32768);
+        const uint32_t acc = tmem + buf * 256;
+        for (int kb = 0; kb < a.nkb && ok; ++kb) {
+          ok = sc_wait(&bars.full[s], ph, &bars.abort);
+          if (!ok) break;
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+          const uint64_t hi = desc0 + (uint64_t)(s * (a.stage_bytes >> 4)), lo = hi + (16384 >> 4), e = hi + (32768 >> 4);
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks) {
-          sc_mma_elect(acc, hi + 2 * ks, e + 2 * ks, idesc, (kb | ks) != 0);
-          sc_mma_elect(acc, lo + 2 * ks, e + 2 * ks, idesc, true);
+          for (int ks = 0; ks < 4; ++ks) {
+            sc_mma(acc, hi + 2 * ks, e + 2 * ks, idesc, (kb | ks) != 0);
+            sc_mma(acc, lo + 2 * ks, e + 2 * ks, idesc, true);
+          }
+          sc_commit(&bars.empty[s]);
+          if (++s == a.stages) {
+            s = 0;
+            ph ^= 1;
+          }
         }
-        mma_commit_elect(&bars.empty[s]);
-        if (++s == a.stages) {
-          s = 0;
-          ph ^= 1;
-        }
+        if (ok) sc_commit(&bars.acc_full[buf]);
       }
-      if (ok) mma_commit_elect(&bars.acc_full[buf]);
+      if (!ok) atomicExch(&bars.abort, 1);
     }
-    if (!ok && lane == 0) atomicExch(&bars.abort, 1);
     __syncwarp();
   } else {
     // ---------------------------------------------------------------- statistics
     const int half = warp >> 2, r = (warp & 3) * 32 + lane;
     const uint32_t laddr = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const int cols = a.bn / 2;                         // a multiple of 16
+    const int row = mt * 128 + r;
+    const float rs = row < a.n ? a.scale[row] : 1.f, rs2 = rs * 1.4426950408889634f;
     float m = -INFINITY, l = 0.f, sx = 0.f;            // in log2 units
-    float rs2 = 0.f, rs = 0.f;
+    // the row's best so far, and a queue of newcomers in shared memory: logits
+    // above the list's last are queued (a predicated store each) and inserted when
+    // some lane's queue fills, so the insertion network runs about as often as the
+    // busiest lane needs, not as often as any lane does
     float cx[KC > 0 ? KC : 1];
     int cv[KC > 0 ? KC : 1];
-    bool ok = true;
-    for (int u = u0; u < u1; ++u) {
-      const int mt = u / a.vt, vt = u % a.vt;
-      const int row = mt * 128 + r;
-      if (u == u0 || vt == 0) {                        // a new row tile
-        m = -INFINITY;
-        l = sx = 0.f;
-        rs = row < a.n ? a.scale[row] : 1.f;
-        rs2 = rs * 1.4426950408889634f;
 #pragma unroll
-        for (int p = 0; p < KC; ++p) {
-          cx[p] = -INFINITY;
-          cv[p] = 0x7fffffff;
+    for (int p = 0; p < KC; ++p) {
+      cx[p] = -INFINITY;
+      cv[p] = 0x7fffffff;
+    }
+    uint2* queue = reinterpret_cast<uint2*>(smem + (size_t)a.stages * a.stage_bytes) + threadIdx.x;   // [SR_QUEUE][256]
+    int queued = 0;
+    auto drain = [&]() {
+      const int most = __reduce_max_sync(0xffffffffu, queued);
+      for (int q = 0; q < most; ++q) {
+        const uint2 w = q < queued ? queue[q * 256] : make_uint2(0xff800000u, 0u);
+        const float xv = __uint_as_float(w.x);
+        const int id = (int)w.y;
+        // an equal entry seen earlier (a lower id) stays before
+#pragma unroll
+        for (int p = KC - 1; p > 0; --p) {
+          const bool up = xv > cx[p - 1], in = xv > cx[p];
+          cv[p] = up ? cv[p - 1] : in ? id : cv[p];
+          cx[p] = up ? cx[p - 1] : in ? xv : cx[p];
+        }
+        if (xv > cx[0]) {
+          cx[0] = xv;
+          cv[0] = id;
         }
       }
-      const int buf = (u - u0) & 1, use = (u - u0) >> 1;
+      queued = 0;
+    };
+    bool ok = true;
+    int i = 0;
+    for (int vt = group; vt < a.vt; vt += a.groups, ++i) {
+      const int buf = i & 1, use = i >> 1;
       if (!warp_wait(&bars.acc_full[buf], use & 1, &bars.abort, true)) {
         if (lane == 0) atomicExch(&bars.abort, 1);
         ok = false;
@@ -343,23 +381,13 @@ __global__ void __launch_bounds__(SR_THREADS, 1)
               sx = fmaf(e, t, sx);
             }
           }
-          if (KC > 0) {
+          if (KC > 0 && __any_sync(0xffffffffu, top > cx[KC > 0 ? KC - 1 : 0])) {
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
-              if (j < nv && x[j] > cx[KC - 1]) {
-                // one insertion pass: an equal entry seen earlier (a lower id) stays before
-                const float xv = x[j];
-                const int id = v0 + c0 + j;
-#pragma unroll
-                for (int p = KC - 1; p > 0; --p) {
-                  const bool up = xv > cx[p - 1], in = xv > cx[p];
-                  cv[p] = up ? cv[p - 1] : in ? id : cv[p];
-                  cx[p] = up ? cx[p - 1] : in ? xv : cx[p];
-                }
-                if (xv > cx[0]) {
-                  cx[0] = xv;
-                  cv[0] = id;
-                }
+              if ((j & 3) == 0 && __any_sync(0xffffffffu, queued > SR_QUEUE - 4)) drain();
+              if (j < nv && x[j] > cx[KC > 0 ? KC - 1 : 0]) {
+                queue[queued * 256] = make_uint2(__float_as_uint(x[j]), (uint32_t)(v0 + c0 + j));
+                ++queued;
               }
             }
           }
@@ -368,17 +396,15 @@ __global__ void __launch_bounds__(SR_THREADS, 1)
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars.acc_empty[buf]);
-      if ((u + 1 == u1 || vt + 1 == a.vt) && row < a.n) {
-        const int first = mt * a.vt / a.upc;           // the first CTA with units of this row tile
-        float* o = a.rec + ((size_t)row * a.slices + 2 * (blockIdx.x - first) + half) * rec_words(KC);
-        o[0] = m;
-        o[1] = l;
-        o[2] = sx;
+    }
+    if (KC > 0) drain();
+    if (row < a.n) {
+      const size_t at = (size_t)row * a.slices + 2 * group + half;
+      a.rec.stat[at] = make_float4(m, l, sx, 0.f);
 #pragma unroll
-        for (int p = 0; p < KC; ++p) {
-          o[3 + 2 * p] = cx[p] * rs;
-          o[4 + 2 * p] = __int_as_float(cv[p]);
-        }
+      for (int p = 0; p < KC; ++p) {
+        a.rec.top_x[((size_t)row * KC + p) * a.slices + 2 * group + half] = cx[p] * rs;
+        a.rec.top_v[((size_t)row * KC + p) * a.slices + 2 * group + half] = cv[p];
       }
     }
     if (!ok && lane == 0) atomicExch(a.flag, 1);
@@ -445,63 +471,70 @@ __global__ void __launch_bounds__(SV_THREADS, 1)
   const uint32_t ybytes = (uint32_t)(2 * tp) * 128, ebytes = (uint32_t)a.bn * 128;
 
   if (warp == 8) {
-    // the embedding of the first stages is requested before the wait for pass 0:
-    // pass 0 has itself waited for everything before it
-    const int total = (a.vt - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x * a.nkb;
-    const int ahead = min(a.stages, total);
-    int issued = 0;
-    bool ok = true;
-    for (int i = 0; i < ahead; ++i) {
-      uint8_t* sp = smem + (size_t)i * a.stage_bytes;
-      sc_expect_elect(&bars.full[i], ybytes + ebytes);
-      sc_copy_elect(&bars.full[i], sp, &map_e, i % a.nkb * SC_BK, ((int)blockIdx.x + i / a.nkb * (int)gridDim.x) * a.bn);
-    }
-    pdl_enter();
-    for (int i = 0; i < total && ok; ++i) {
-      const int s = i % a.stages, use = i / a.stages;
-      const int kb = i % a.nkb, v0 = ((int)blockIdx.x + i / a.nkb * (int)gridDim.x) * a.bn;
-      uint8_t* sp = smem + (size_t)s * a.stage_bytes;
-      if (use > 0) {
-        if (!warp_wait(&bars.empty[s], (use & 1) ^ 1, &bars.abort, true)) {
-          if (lane == 0) atomicExch(&bars.abort, 1);
-          ok = false;
-          break;
-        }
-        sc_expect_elect(&bars.full[s], ybytes + ebytes);
-        sc_copy_elect(&bars.full[s], sp, &map_e, kb * SC_BK, v0);
+    if (lane == 0) {
+      // the embedding of the first stages is requested before the wait for pass 0:
+      // pass 0 has itself waited for everything before it
+      const int total = (a.vt - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x * a.nkb;
+      const int ahead = min(a.stages, total);
+      for (int i = 0; i < ahead; ++i) {
+        sc_expect(&bars.full[i], ybytes + ebytes);
+        sc_copy(&bars.full[i], smem + (size_t)i * a.stage_bytes, &map_e, i % a.nkb * SC_BK,
+                ((int)blockIdx.x + i / a.nkb * (int)gridDim.x) * a.bn);
       }
-      sc_copy_elect(&bars.full[s], sp + 16384, &map_y, kb * SC_BK, 0);
-      issued = i + 1;
-    }
-    if (lane == 0 && *(volatile int*)&bars.abort)
-      for (int i = max(0, issued - a.stages); i < issued; ++i) mbar_wait(&bars.full[i % a.stages], (i / a.stages) & 1);
-    __syncwarp();
-  } else if (warp == 9) {
-    pdl_enter();
-    const uint32_t idesc = (1u << 4) | ((uint32_t)(2 * tp >> 3) << 17) | (8u << 24);
-    int s = 0, ph = 0, j = 0;
-    bool ok = true;
-    for (int t = blockIdx.x; t < a.vt && ok; t += gridDim.x, ++j) {
-      const int buf = j & 1, use = j >> 1;
-      ok = warp_wait(&bars.acc_empty[buf], (use & 1) ^ 1, &bars.abort, use > 0);
-      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-      for (int kb = 0; kb < a.nkb && ok; ++kb) {
-        ok = warp_wait(&bars.full[s], ph, &bars.abort, true);
-        if (!ok) break;
-        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        const uint32_t sp = smem_u32(smem + (size_t)s * a.stage_bytes);
-        const uint64_t e = smem_desc_sw128(sp), yy = smem_desc_sw128(sp + 16384);
-#pragma unroll
-        for (int ks = 0; ks < 4; ++ks) sc_mma_elect(tmem + buf * 128, e + 2 * ks, yy + 2 * ks, idesc, (kb | ks) != 0);
-        mma_commit_elect(&bars.empty[s]);
+      pdl_enter();
+      int s = 0, ph = 1, kb = 0, v0 = (int)blockIdx.x * a.bn, issued = 0;
+      for (; issued < total; ++issued) {
+        uint8_t* sp = smem + (size_t)s * a.stage_bytes;
+        if (issued >= a.stages) {
+          if (!sc_wait(&bars.empty[s], ph, &bars.abort)) {
+            atomicExch(&bars.abort, 1);
+            break;
+          }
+          sc_expect(&bars.full[s], ybytes + ebytes);
+          sc_copy(&bars.full[s], sp, &map_e, kb * SC_BK, v0);
+        }
+        sc_copy(&bars.full[s], sp + 16384, &map_y, kb * SC_BK, 0);
         if (++s == a.stages) {
           s = 0;
           ph ^= 1;
         }
+        if (++kb == a.nkb) {
+          kb = 0;
+          v0 += (int)gridDim.x * a.bn;
+        }
       }
-      if (ok) mma_commit_elect(&bars.acc_full[buf]);
+      if (*(volatile int*)&bars.abort)
+        for (int i = max(0, issued - a.stages); i < issued; ++i) mbar_wait(&bars.full[i % a.stages], (i / a.stages) & 1);
     }
-    if (!ok && lane == 0) atomicExch(&bars.abort, 1);
+    __syncwarp();
+  } else if (warp == 9) {
+    if (lane == 0) {
+      pdl_enter();
+      const uint32_t idesc = (1u << 4) | ((uint32_t)(2 * tp >> 3) << 17) | (8u << 24);
+      const uint64_t desc0 = smem_desc_sw128(smem_u32(smem));
+      int s = 0, ph = 0, j = 0;
+      bool ok = true;
+      for (int t = blockIdx.x; t < a.vt && ok; t += gridDim.x, ++j) {
+        const int buf = j & 1, use = j >> 1;
+        if (use > 0) ok = sc_wait(&bars.acc_empty[buf], (use & 1) ^ 1, &bars.abort);
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        for (int kb = 0; kb < a.nkb && ok; ++kb) {
+          ok = sc_wait(&bars.full[s], ph, &bars.abort);
+          if (!ok) break;
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+          const uint64_t e = desc0 + (uint64_t)(s * (a.stage_bytes >> 4)), yy = e + (16384 >> 4);
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks) sc_mma(tmem + buf * 128, e + 2 * ks, yy + 2 * ks, idesc, (kb | ks) != 0);
+          sc_commit(&bars.empty[s]);
+          if (++s == a.stages) {
+            s = 0;
+            ph ^= 1;
+          }
+        }
+        if (ok) sc_commit(&bars.acc_full[buf]);
+      }
+      if (!ok) atomicExch(&bars.abort, 1);
+    }
     __syncwarp();
   } else {
     pdl_enter();
@@ -614,12 +647,11 @@ __global__ void __launch_bounds__(SV_THREADS, 1)
     }
     __syncwarp();
     for (int row = warp; row < a.n; row += 8) {
-      float* o = a.rec + ((size_t)row * a.slices + blockIdx.x) * rec_words(KC);
-      const float rs = a.scale[row];
-      if (lane < 3) o[lane] = st[row][lane];
+      const size_t at = (size_t)row * a.slices + blockIdx.x;
+      if (lane == 0) a.rec.stat[at] = make_float4(st[row][0], st[row][1], st[row][2], 0.f);
       if (lane < KC) {
-        o[3 + 2 * lane] = lx[row][lane] * rs;
-        o[4 + 2 * lane] = __int_as_float(lv[row][lane]);
+        a.rec.top_x[((size_t)row * KC + lane) * a.slices + blockIdx.x] = lx[row][lane] * a.scale[row];
+        a.rec.top_v[((size_t)row * KC + lane) * a.slices + blockIdx.x] = lv[row][lane];
       }
     }
   }
@@ -631,46 +663,65 @@ __global__ void __launch_bounds__(SV_THREADS, 1)
   if (threadIdx.x == 0 && bars.abort) atomicExch(a.flag, 1);
 }
 
-constexpr int SM_THREADS = 256;
+// ------------------------------------------------------------------ pass 2
+constexpr int SM_THREADS = 256, SM_WARPS = SM_THREADS / 32;
+constexpr int kMaxSlices = 2 * kScoreSms;
 
-// One CTA per row: the slices' statistics and candidates merged, the chosen
-// candidates and the given token scored in fp64.
-__global__ void __launch_bounds__(SM_THREADS) score_merge_kernel(ScoreArgs a, int kc, ScoreTc tc, int by_rows) {
+// fp32 values as unsigned integers in the same order (no NaN)
+__device__ __forceinline__ uint32_t sc_key(float x) {
+  const uint32_t u = __float_as_uint(x);
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+// One CTA per row.  The slices' lists come into shared memory at once; each warp
+// picks the best of its share (lists are sorted, so a lane looks at the heads of its
+// own), the warps' picks are ranked by counting, and the chosen and the given
+// token are scored in fp64, a warp per token.
+__global__ void __launch_bounds__(SM_THREADS) score_merge_kernel(ScoreArgs a, int kc, ScoreTc tc) {
   pdl_enter();
-  __shared__ float wx[SM_THREADS / 32];
-  __shared__ int wv[SM_THREADS / 32], wi[SM_THREADS / 32];
+  extern __shared__ float sm_dyn[];                 // [kc][ld] logits, then ids
+  __shared__ float wred[3][SM_WARPS];
+  __shared__ float px[SM_WARPS * kMaxCand];
+  __shared__ int pv[SM_WARPS * kMaxCand];
   __shared__ double zs[kMaxCand + 1];
   __shared__ int ids[kMaxCand + 1];
-  __shared__ float red[2][SM_THREADS / 32];
   const int row = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int rw = rec_words(kc);
-  const float* base = tc.rec + (size_t)row * tc.slices * rw;
-  int slices = tc.slices;
-  if (by_rows) {   // the CTAs that had units of this row's tile, two column halves each
-    const int mt = row / 128;
-    slices = 2 * (((mt + 1) * tc.vt - 1) / tc.upc - mt * tc.vt / tc.upc + 1);
-  }
-  // statistics, in a fixed order: thread-strided slices, lanes, warps
+  const int slices = tc.slices;
+  const float4* stat = tc.rec.stat + (size_t)row * slices;
+  const int ld = (slices + 31) & ~31;               // a list per bank: lanes read their heads without conflicts
+  float* lx = sm_dyn;
+  int* lv = reinterpret_cast<int*>(sm_dyn + ld * kc);
+  for (int p = 0; p < kc; ++p)
+    for (int i = tid; i < slices; i += SM_THREADS) {
+      lx[p * ld + i] = tc.rec.top_x[((size_t)row * kc + p) * slices + i];
+      lv[p * ld + i] = tc.rec.top_v[((size_t)row * kc + p) * slices + i];
+    }
+  const int target = a.targets ? a.targets[row] : -1;
+  // statistics, in a fixed order: a thread's slices, lanes, warps
+  constexpr int PER = (kMaxSlices + SM_THREADS - 1) / SM_THREADS;
+  float4 v[PER];
   float M = -INFINITY;
-  bool nan = false;
-  for (int i = tid; i < slices; i += SM_THREADS) {
-    const float m = base[(size_t)i * rw];
-    nan |= isnan(base[(size_t)i * rw + 1]) || isnan(base[(size_t)i * rw + 2]);
-    M = fmaxf(M, m);
+  bool bad = false;
+#pragma unroll
+  for (int u = 0; u < PER; ++u) {
+    const int i = tid + u * SM_THREADS;
+    v[u] = i < slices ? stat[i] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+    bad |= isnan(v[u].y) || isnan(v[u].z);
+    M = fmaxf(M, v[u].x);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  if (lane == 0) wx[warp] = M;
-  nan = __syncthreads_or(nan);
-  for (int w = 0; w < SM_THREADS / 32; ++w) M = fmaxf(M, wx[w]);
+  if (lane == 0) wred[0][warp] = M;
+  bad = __syncthreads_or(bad) || *tc.flag != 0;
+#pragma unroll
+  for (int w = 0; w < SM_WARPS; ++w) M = fmaxf(M, wred[0][w]);
   float L = 0.f, S = 0.f;
-  for (int i = tid; i < slices; i += SM_THREADS) {
-    const float m = base[(size_t)i * rw];
-    if (m == -INFINITY) continue;
-    const float dm = m - M, f = exp2f(dm);
-    const float l = base[(size_t)i * rw + 1];
-    L += l * f;
-    S += (base[(size_t)i * rw + 2] + l * dm) * f;
+#pragma unroll
+  for (int u = 0; u < PER; ++u) {
+    if (v[u].x == -INFINITY) continue;
+    const float dm = v[u].x - M, f = exp2f(dm);
+    L += v[u].y * f;
+    S += (v[u].z + v[u].y * dm) * f;
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -678,95 +729,123 @@ __global__ void __launch_bounds__(SM_THREADS) score_merge_kernel(ScoreArgs a, in
     S += __shfl_xor_sync(0xffffffffu, S, o);
   }
   if (lane == 0) {
-    red[0][warp] = L;
-    red[1][warp] = S;
+    wred[1][warp] = L;
+    wred[2][warp] = S;
+  }
+  // this warp's best kc of its share of the lists, 64 at most: a lane keeps the
+  // heads of two in registers
+  {
+    const int share = (slices + SM_WARPS - 1) / SM_WARPS, end = min(slices, (warp + 1) * share);
+    const int l[2] = {warp * share + lane, warp * share + lane + 32};
+    int h[2] = {0, 0}, hv[2];
+    float hx[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const bool has = l[u] < end && kc > 0;
+      hx[u] = has ? lx[l[u]] : -INFINITY;
+      hv[u] = has ? lv[l[u]] : 0x7fffffff;
+    }
+    for (int p = 0; p < kc; ++p) {
+      const bool second = sc_better(hx[1], hv[1], hx[0], hv[0]);
+      const float x = second ? hx[1] : hx[0];
+      const int id = second ? hv[1] : hv[0];
+      const uint32_t key = sc_key(x), best = __reduce_max_sync(0xffffffffu, key);
+      const int low = __reduce_min_sync(0xffffffffu, key == best ? id : 0x7fffffff);   // 0x7fffffff: nothing left
+      if (lane == 0) pv[warp * kMaxCand + p] = low;
+      if (low == 0x7fffffff ? lane == 0 : id == low) px[warp * kMaxCand + p] = x;
+      if (low != 0x7fffffff && id == low) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+          if (u == (second ? 1 : 0)) {
+            const bool more = ++h[u] < kc;
+            hx[u] = more ? lx[h[u] * ld + l[u]] : -INFINITY;
+            hv[u] = more ? lv[h[u] * ld + l[u]] : 0x7fffffff;
+          }
+      }
+    }
   }
   __syncthreads();
   L = S = 0.f;
-  for (int w = 0; w < SM_THREADS / 32; ++w) {
-    L += red[0][w];
-    S += red[1][w];
+#pragma unroll
+  for (int w = 0; w < SM_WARPS; ++w) {
+    L += wred[1][w];
+    S += wred[2][w];
   }
-  const bool bad = nan || !isfinite(M) || !isfinite(L) || *tc.flag != 0;
+  bad = bad || !isfinite(M) || !isfinite(L);
   constexpr double kLn2 = 0.693147180559945309;
   const double lse = (double)M * kLn2 + log((double)L);
   if (tid == 0 && a.entropy)
     a.entropy[row] = bad ? CUDART_NAN_F : (float)(log((double)L) - (double)S / (double)L * kLn2);
-
-  // candidates: the slices' lists are sorted, so each pick looks at their heads
-  int n_pick = bad ? 0 : min(kc, a.V);
-  {
-    int h0 = 0, h1 = 0;   // heads of this thread's two lists (slices <= 2 * SM_THREADS)
-    for (int p = 0; p < n_pick; ++p) {
-      float bx = -INFINITY;
-      int bv = 0x7fffffff, bi = -1;
+  if (bad) {
+    if (tid == 0 && a.logp) a.logp[row] = target < 0 ? 0.f : CUDART_NAN_F;
+    if (tid < a.k) {
+      a.top_ids[(size_t)row * a.k + tid] = -1;
+      a.top_logp[(size_t)row * a.k + tid] = CUDART_NAN_F;
+    }
+    return;
+  }
+  // the best kc of the warps' picks by counting who is before whom
+  const int n_pick = min(kc, a.V);
+  if (tid == 0) ids[n_pick] = target;
+  if (tid < SM_WARPS * kc) {
+    const int w0 = tid / kc, at = w0 * kMaxCand + tid % kc;
+    const float x = px[at];
+    const int id = pv[at];
+    int rank = 0;
+    for (int w = 0; w < SM_WARPS; ++w)
+      for (int p = 0; p < kc; ++p) rank += sc_better(px[w * kMaxCand + p], pv[w * kMaxCand + p], x, id);
+    if (rank < n_pick && id != 0x7fffffff) ids[rank] = id;
+  }
+  __syncthreads();
+  const float* yr = a.y + (size_t)row * a.y_stride;
+  for (int p0 = warp; p0 <= n_pick; p0 += 2 * SM_WARPS) {
+    // two tokens at a time, 1024 elements of each requested at once
+    double acc[2][2] = {{0.0, 0.0}, {0.0, 0.0}};
+    const __half* e[2];
+    bool has[2];
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int i = tid + u * SM_THREADS, h = u ? h1 : h0;
-        if (i < slices && h < kc) {
-          const float x = base[(size_t)i * rw + 3 + 2 * h];
-          const int v = __float_as_int(base[(size_t)i * rw + 4 + 2 * h]);
-          if (sc_better(x, v, bx, bv)) {
-            bx = x;
-            bv = v;
-            bi = i;
+    for (int u = 0; u < 2; ++u) {
+      const int p = p0 + u * SM_WARPS, id = p <= n_pick ? ids[p] : -1;
+      has[u] = id >= 0 && id < a.V;
+      e[u] = a.E + (size_t)(has[u] ? id : 0) * a.d;
+    }
+    for (int j0 = 8 * lane; j0 < a.d; j0 += 1024) {
+      uint4 w[2][4];
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          w[u][q] = has[u] && j0 + 256 * q < a.d ? *reinterpret_cast<const uint4*>(e[u] + j0 + 256 * q)
+                                                 : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        if (j0 + 256 * q >= a.d) break;
+        const float4 y0 = *reinterpret_cast<const float4*>(yr + j0 + 256 * q);
+        const float4 y1 = *reinterpret_cast<const float4*>(yr + j0 + 256 * q + 4);
+        const float yy[8] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w};
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const uint32_t ww[4] = {w[u][q].x, w[u][q].y, w[u][q].z, w[u][q].w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&ww[i]));
+            acc[u][0] = fma((double)f.x, (double)yy[2 * i], acc[u][0]);
+            acc[u][1] = fma((double)f.y, (double)yy[2 * i + 1], acc[u][1]);
           }
         }
       }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        const float x = __shfl_xor_sync(0xffffffffu, bx, o);
-        const int v = __shfl_xor_sync(0xffffffffu, bv, o), i = __shfl_xor_sync(0xffffffffu, bi, o);
-        if (sc_better(x, v, bx, bv)) {
-          bx = x;
-          bv = v;
-          bi = i;
-        }
-      }
-      __syncthreads();
-      if (lane == 0) {
-        wx[warp] = bx;
-        wv[warp] = bv;
-        wi[warp] = bi;
-      }
-      __syncthreads();
-      for (int w = 0; w < SM_THREADS / 32; ++w)
-        if (sc_better(wx[w], wv[w], bx, bv)) {
-          bx = wx[w];
-          bv = wv[w];
-          bi = wi[w];
-        }
-      if (bi == tid) ++h0;
-      if (bi == tid + SM_THREADS) ++h1;
-      if (tid == 0) ids[p] = bv;
     }
-  }
-  const int target = a.targets ? a.targets[row] : -1;
-  if (tid == 0) ids[n_pick] = target;
-  __syncthreads();
-  for (int p = warp; p <= n_pick; p += SM_THREADS / 32) {
-    const int v = ids[p];
-    double acc = 0.0;
-    if (v >= 0 && v < a.V) {
-      const __half* e = a.E + (size_t)v * a.d;
-      const float* yr = a.y + (size_t)row * a.y_stride;
-      for (int j = 2 * lane; j < a.d; j += 64) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(e + j));
-        const float2 yy = *reinterpret_cast<const float2*>(yr + j);
-        acc = fma((double)f.y, (double)yy.y, fma((double)f.x, (double)yy.x, acc));
-      }
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+    for (int u = 0; u < 2; ++u) {
+      double z = acc[u][0] + acc[u][1];
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+      if (lane == 0 && p0 + u * SM_WARPS <= n_pick) zs[p0 + u * SM_WARPS] = z;
     }
-    if (lane == 0) zs[p] = acc;
   }
   __syncthreads();
   if (tid == 0 && a.logp)
-    a.logp[row] = target < 0 ? 0.f : target >= a.V || bad ? CUDART_NAN_F : (float)(zs[n_pick] - lse);
-  if (tid < a.k && bad) {
-    a.top_ids[(size_t)row * a.k + tid] = -1;
-    a.top_logp[(size_t)row * a.k + tid] = CUDART_NAN_F;
-  }
+    a.logp[row] = target < 0 ? 0.f : target >= a.V ? CUDART_NAN_F : (float)(zs[n_pick] - lse);
   // each candidate's rank among them; the first k are the answer
   if (tid < n_pick) {
     int rank = 0;
@@ -780,14 +859,16 @@ __global__ void __launch_bounds__(SM_THREADS) score_merge_kernel(ScoreArgs a, in
 
 int score_cand(int k) { return k == 0 ? 0 : k <= 4 ? 8 : k <= 8 ? 12 : 20; }
 
-constexpr int kScoreChunk = 4096;      // rows per sweep over the embedding: bounds the workspace
-constexpr size_t kScoreSmem = 212 * 1024;   // beside up to 11 KB of static shared memory
+constexpr int kScoreChunk = 37 * 128;  // rows per sweep over the embedding: bounds the workspace; 37 row
+                                       // tiles share 148 SMs evenly
+constexpr size_t kVocabSmem = 215 * 1024;   // beside up to 11 KB of static shared memory
+constexpr size_t kRowsSmem = 226 * 1024;
 
 struct ScorePlan {
   ScoreTc t;
   bool by_rows;
   int grid;
-  size_t smem, parts_off, scale_off, flag_off, rec_off, bytes;
+  size_t smem, parts_off, scale_off, flag_off, stat_off, top_x_off, top_v_off, bytes;
 };
 
 // Up to 64 rows the embedding streams as the M side (its bytes are the bound);
@@ -810,37 +891,41 @@ ScorePlan score_plan(int n, int V, int d, int k) {
     t.slices = p.grid;
     t.stage_bytes = 16384 + (uint32_t)(2 * t.pad * 128 + 1023) / 1024 * 1024;
     const size_t zb = (size_t)t.pad * 132 * 4;
-    t.stages = (int)std::min<size_t>(12, (kScoreSmem - zb - 1024) / t.stage_bytes);
+    t.stages = (int)std::min<size_t>(12, (kVocabSmem - zb - 1024) / t.stage_bytes);
     p.smem = 1024 + (size_t)t.stages * t.stage_bytes + zb;
   } else {
     t.pad = (n + 127) / 128 * 128;
-    const int mt = t.pad / 128;
+    t.mt = t.pad / 128;
+    t.groups = kScoreSms / t.mt;
     // the tile width (a multiple of 32) with the least work on the busiest CTA,
     // counting a tile's fixed cost as 16 columns
     long best = -1;
     for (int bn = 256; bn >= 128; bn -= 32) {
-      const long units = (long)mt * ((V + bn - 1) / bn);
-      const long cost = (units + kScoreSms - 1) / kScoreSms * (bn + 16);
+      const int vt = (V + bn - 1) / bn;
+      const long cost = (long)((vt + t.groups - 1) / t.groups) * (bn + 16);
       if (best < 0 || cost < best) {
         best = cost;
         t.bn = bn;
       }
     }
     t.vt = (V + t.bn - 1) / t.bn;
-    t.units = mt * t.vt;
-    t.upc = (t.units + kScoreSms - 1) / kScoreSms;
-    p.grid = (t.units + t.upc - 1) / t.upc;
-    t.slices = 2 * ((t.vt + t.upc - 1) / t.upc + 1);
+    t.groups = std::min(t.groups, t.vt);
+    p.grid = t.mt * t.groups;
+    t.slices = 2 * t.groups;
     t.stage_bytes = 32768 + (uint32_t)t.bn * 128;
-    t.stages = (int)std::min<size_t>(12, (kScoreSmem - 1024) / t.stage_bytes);
-    p.smem = 1024 + (size_t)t.stages * t.stage_bytes;
+    const size_t queue = (size_t)SR_QUEUE * 256 * 8;
+    t.stages = (int)std::min<size_t>(12, (kRowsSmem - queue - 1024) / t.stage_bytes);
+    p.smem = 1024 + (size_t)t.stages * t.stage_bytes + queue;
   }
   auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
   p.parts_off = 0;
   p.scale_off = up((size_t)2 * t.pad * d * 2);
   p.flag_off = p.scale_off + up((size_t)t.pad * 4);
-  p.rec_off = p.flag_off + 256;
-  p.bytes = p.rec_off + up((size_t)n * t.slices * rec_words(score_cand(k)) * 4);
+  p.stat_off = p.flag_off + 256;
+  p.top_x_off = p.stat_off + up((size_t)n * t.slices * 16);
+  const size_t top = up((size_t)n * t.slices * score_cand(k) * 4);
+  p.top_v_off = p.top_x_off + top;
+  p.bytes = p.top_v_off + top;
   return p;
 }
 
@@ -848,8 +933,8 @@ template <int KC>
 tl_status launch_score_pass1(const ScorePlan& p, const CUtensorMap& my, const CUtensorMap& me, cudaStream_t s) {
   static std::atomic<uint64_t> attr_done{0};
   TL_TRY(once_per_device(attr_done, []() -> tl_status {
-    TL_CUDA(cudaFuncSetAttribute(score_rows_kernel<KC>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kScoreSmem));
-    TL_CUDA(cudaFuncSetAttribute(score_vocab_kernel<KC>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kScoreSmem));
+    TL_CUDA(cudaFuncSetAttribute(score_rows_kernel<KC>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRowsSmem));
+    TL_CUDA(cudaFuncSetAttribute(score_vocab_kernel<KC>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kVocabSmem));
     return ok();
   }));
   if (p.by_rows) TL_LAUNCH_PDL(score_rows_kernel<KC>, p.grid, SR_THREADS, p.smem, s, my, me, p.t);
@@ -867,6 +952,12 @@ size_t score_workspace(int n, int V, int d, int k) {
 }
 
 tl_status launch_score_head(const ScoreArgs& a0, cudaStream_t s) {
+  static std::atomic<uint64_t> attr_done{0};
+  TL_TRY(once_per_device(attr_done, []() -> tl_status {
+    TL_CUDA(cudaFuncSetAttribute(score_merge_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (kMaxSlices + 31) * kMaxCand * 8));
+    return ok();
+  }));
   for (int r0 = 0; r0 < a0.n; r0 += kScoreChunk) {
     ScoreArgs a = a0;
     a.n = std::min(kScoreChunk, a0.n - r0);
@@ -884,7 +975,9 @@ tl_status launch_score_head(const ScoreArgs& a0, cudaStream_t s) {
     float* scale = (float*)(a.ws + p.scale_off);
     t.scale = scale;
     t.flag = (int*)(a.ws + p.flag_off);
-    t.rec = (float*)(a.ws + p.rec_off);
+    t.rec.stat = (float4*)(a.ws + p.stat_off);
+    t.rec.top_x = (float*)(a.ws + p.top_x_off);
+    t.rec.top_v = (int*)(a.ws + p.top_v_off);
     CUtensorMap my, me;
     TL_TRY(encode_2d(&my, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, parts, a.d, 2 * t.pad, (uint64_t)a.d * 2, SC_BK,
                      p.by_rows ? 128 : 2 * t.pad, CU_TENSOR_MAP_SWIZZLE_128B));
@@ -895,7 +988,7 @@ tl_status launch_score_head(const ScoreArgs& a0, cudaStream_t s) {
     TL_TRY(kc == 0 ? launch_score_pass1<0>(p, my, me, s)
                    : kc == 8 ? launch_score_pass1<8>(p, my, me, s)
                              : kc == 12 ? launch_score_pass1<12>(p, my, me, s) : launch_score_pass1<20>(p, my, me, s));
-    TL_LAUNCH_PDL(score_merge_kernel, a.n, SM_THREADS, 0, s, a, kc, t, p.by_rows ? 1 : 0);
+    TL_LAUNCH_PDL(score_merge_kernel, a.n, SM_THREADS, (size_t)((t.slices + 31) & ~31) * kc * 8, s, a, kc, t);
   }
   return ok();
 }
