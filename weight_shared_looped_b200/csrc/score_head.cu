@@ -17,7 +17,9 @@
 // Pass 2, one CTA per row, merges the slices and decides the order of the best
 // k + kSpare candidates, and the given token's logit, by fp64 dot products of the
 // inputs, so the ranking does not depend on pass 1's rounding (ties go to the
-// lowest token id).
+// lowest token id; equal embedding rows tie in pass 1 already, and for another
+// token to be missed, three logits would have to lie within pass 1's error of the
+// k-th).
 #include <math_constants.h>
 
 #include <algorithm>
@@ -28,8 +30,8 @@
 namespace tl {
 namespace {
 
-constexpr int kSpare = 4;          // candidates kept beyond k
-constexpr int kMaxCand = 16 + kSpare;
+constexpr int kSpare = 2;          // candidates scored in fp64 beyond k
+constexpr int kMaxCand = 20;       // candidates kept per slice, at most
 constexpr int SC_BK = 64;          // k per stage (one 128-byte swizzled row)
 constexpr int kScoreSms = 148;
 
@@ -666,58 +668,83 @@ __global__ void __launch_bounds__(SV_THREADS, 1)
 // ------------------------------------------------------------------ pass 2
 constexpr int SM_THREADS = 256, SM_WARPS = SM_THREADS / 32;
 constexpr int kMaxSlices = 2 * kScoreSms;
+constexpr int SM_PER = (kMaxSlices + SM_THREADS - 1) / SM_THREADS;   // lists of a thread
 
-// fp32 values as unsigned integers in the same order (no NaN)
-__device__ __forceinline__ uint32_t sc_key(float x) {
-  const uint32_t u = __float_as_uint(x);
-  return u & 0x80000000u ? ~u : u | 0x80000000u;
-}
+struct ScoreCand {
+  float x;
+  int v;
+};
 
-// One CTA per row.  The slices' lists come into shared memory at once; each warp
-// picks the best of its share (lists are sorted, so a lane looks at the heads of its
-// own), the warps' picks are ranked by counting, and the chosen and the given
-// token are scored in fp64, a warp per token.
-__global__ void __launch_bounds__(SM_THREADS) score_merge_kernel(ScoreArgs a, int kc, ScoreTc tc) {
+// One CTA per row.  The kc-th best of 32 groups' best list heads bounds the kc-th
+// best logit from below, so only entries at or above it are candidates: a few
+// more than kc, whatever the number of lists.  They are ranked by counting; the
+// chosen and the given token are scored in fp64, two tokens a warp.  With one CTA
+// on the SM every step is a round trip: loads that do not depend on one another
+// are issued together.
+__global__ void __launch_bounds__(SM_THREADS, 3) score_merge_kernel(ScoreArgs a, int kc, ScoreTc tc) {
   pdl_enter();
-  extern __shared__ float sm_dyn[];                 // [kc][ld] logits, then ids
+  extern __shared__ double sm_dyn[];
+  double* yd = sm_dyn;                                              // [d] the row's activations
+  ScoreCand* cand = reinterpret_cast<ScoreCand*>(sm_dyn + a.d);     // [slices * kc]
   __shared__ float wred[3][SM_WARPS];
-  __shared__ float px[SM_WARPS * kMaxCand];
-  __shared__ int pv[SM_WARPS * kMaxCand];
+  __shared__ float gmax[SM_WARPS][32];
+  __shared__ float bound;
+  __shared__ int n_cand;
   __shared__ double zs[kMaxCand + 1];
   __shared__ int ids[kMaxCand + 1];
   const int row = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int slices = tc.slices;
   const float4* stat = tc.rec.stat + (size_t)row * slices;
-  const int ld = (slices + 31) & ~31;               // a list per bank: lanes read their heads without conflicts
-  float* lx = sm_dyn;
-  int* lv = reinterpret_cast<int*>(sm_dyn + ld * kc);
-  for (int p = 0; p < kc; ++p)
-    for (int i = tid; i < slices; i += SM_THREADS) {
-      lx[p * ld + i] = tc.rec.top_x[((size_t)row * kc + p) * slices + i];
-      lv[p * ld + i] = tc.rec.top_v[((size_t)row * kc + p) * slices + i];
-    }
+  const float* gx = tc.rec.top_x + (size_t)row * kc * slices;
+  const int* gv = tc.rec.top_v + (size_t)row * kc * slices;
+  const float* yr = a.y + (size_t)row * a.y_stride;
   const int target = a.targets ? a.targets[row] : -1;
-  // statistics, in a fixed order: a thread's slices, lanes, warps
-  constexpr int PER = (kMaxSlices + SM_THREADS - 1) / SM_THREADS;
-  float4 v[PER];
-  float M = -INFINITY;
-  bool bad = false;
+  const int gave_up = *tc.flag;
+  float4 v[SM_PER];
+  float hx[SM_PER];
 #pragma unroll
-  for (int u = 0; u < PER; ++u) {
+  for (int u = 0; u < SM_PER; ++u) {
     const int i = tid + u * SM_THREADS;
     v[u] = i < slices ? stat[i] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+    hx[u] = i < slices && kc > 0 ? gx[i] : -INFINITY;
+  }
+  for (int j = 4 * tid; j < a.d; j += 4 * SM_THREADS) {
+    const float4 f = *reinterpret_cast<const float4*>(yr + j);
+    *reinterpret_cast<double2*>(yd + j) = make_double2((double)f.x, (double)f.y);
+    *reinterpret_cast<double2*>(yd + j + 2) = make_double2((double)f.z, (double)f.w);
+  }
+  // statistics, in a fixed order: a thread's slices, lanes, warps
+  float M = -INFINITY, head = -INFINITY;
+  bool bad = gave_up != 0;
+#pragma unroll
+  for (int u = 0; u < SM_PER; ++u) {
     bad |= isnan(v[u].y) || isnan(v[u].z);
     M = fmaxf(M, v[u].x);
+    head = fmaxf(head, hx[u]);
   }
+  gmax[warp][lane] = head;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   if (lane == 0) wred[0][warp] = M;
-  bad = __syncthreads_or(bad) || *tc.flag != 0;
+  if (tid == 0) n_cand = 0;
+  bad = __syncthreads_or(bad);
+  if (warp == 0 && kc > 0) {
+    float g = gmax[0][lane];
+#pragma unroll
+    for (int w = 1; w < SM_WARPS; ++w) g = fmaxf(g, gmax[w][lane]);
+    int rank = 0;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      const float o = __shfl_sync(0xffffffffu, g, j);
+      rank += o > g || (o == g && j < lane);
+    }
+    if (rank == kc - 1) bound = g;
+  }
 #pragma unroll
   for (int w = 0; w < SM_WARPS; ++w) M = fmaxf(M, wred[0][w]);
   float L = 0.f, S = 0.f;
 #pragma unroll
-  for (int u = 0; u < PER; ++u) {
+  for (int u = 0; u < SM_PER; ++u) {
     if (v[u].x == -INFINITY) continue;
     const float dm = v[u].x - M, f = exp2f(dm);
     L += v[u].y * f;
@@ -732,38 +759,6 @@ __global__ void __launch_bounds__(SM_THREADS) score_merge_kernel(ScoreArgs a, in
     wred[1][warp] = L;
     wred[2][warp] = S;
   }
-  // this warp's best kc of its share of the lists, 64 at most: a lane keeps the
-  // heads of two in registers
-  {
-    const int share = (slices + SM_WARPS - 1) / SM_WARPS, end = min(slices, (warp + 1) * share);
-    const int l[2] = {warp * share + lane, warp * share + lane + 32};
-    int h[2] = {0, 0}, hv[2];
-    float hx[2];
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const bool has = l[u] < end && kc > 0;
-      hx[u] = has ? lx[l[u]] : -INFINITY;
-      hv[u] = has ? lv[l[u]] : 0x7fffffff;
-    }
-    for (int p = 0; p < kc; ++p) {
-      const bool second = sc_better(hx[1], hv[1], hx[0], hv[0]);
-      const float x = second ? hx[1] : hx[0];
-      const int id = second ? hv[1] : hv[0];
-      const uint32_t key = sc_key(x), best = __reduce_max_sync(0xffffffffu, key);
-      const int low = __reduce_min_sync(0xffffffffu, key == best ? id : 0x7fffffff);   // 0x7fffffff: nothing left
-      if (lane == 0) pv[warp * kMaxCand + p] = low;
-      if (low == 0x7fffffff ? lane == 0 : id == low) px[warp * kMaxCand + p] = x;
-      if (low != 0x7fffffff && id == low) {
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-          if (u == (second ? 1 : 0)) {
-            const bool more = ++h[u] < kc;
-            hx[u] = more ? lx[h[u] * ld + l[u]] : -INFINITY;
-            hv[u] = more ? lv[h[u] * ld + l[u]] : 0x7fffffff;
-          }
-      }
-    }
-  }
   __syncthreads();
   L = S = 0.f;
 #pragma unroll
@@ -772,11 +767,8 @@ __global__ void __launch_bounds__(SM_THREADS) score_merge_kernel(ScoreArgs a, in
     S += wred[2][w];
   }
   bad = bad || !isfinite(M) || !isfinite(L);
-  constexpr double kLn2 = 0.693147180559945309;
-  const double lse = (double)M * kLn2 + log((double)L);
-  if (tid == 0 && a.entropy)
-    a.entropy[row] = bad ? CUDART_NAN_F : (float)(log((double)L) - (double)S / (double)L * kLn2);
   if (bad) {
+    if (tid == 0 && a.entropy) a.entropy[row] = CUDART_NAN_F;
     if (tid == 0 && a.logp) a.logp[row] = target < 0 ? 0.f : CUDART_NAN_F;
     if (tid < a.k) {
       a.top_ids[(size_t)row * a.k + tid] = -1;
@@ -784,22 +776,47 @@ __global__ void __launch_bounds__(SM_THREADS) score_merge_kernel(ScoreArgs a, in
     }
     return;
   }
-  // the best kc of the warps' picks by counting who is before whom
-  const int n_pick = min(kc, a.V);
+  // candidates: a list's entries from its head down to the bound, four at a time
+#pragma unroll
+  for (int u = 0; u < SM_PER; ++u) {
+    const int i = tid + u * SM_THREADS;
+    if (kc == 0 || i >= slices || !(hx[u] >= bound)) continue;
+    bool more = true;
+    for (int p0 = 0; p0 < kc && more; p0 += 4) {      // kc is a multiple of 4
+      float x4[4];
+      int v4[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        x4[q] = gx[(size_t)(p0 + q) * slices + i];
+        v4[q] = gv[(size_t)(p0 + q) * slices + i];
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        more = more && x4[q] >= bound && v4[q] != 0x7fffffff;
+        if (more) {
+          const int at = atomicAdd(&n_cand, 1);
+          cand[at].x = x4[q];
+          cand[at].v = v4[q];
+        }
+      }
+    }
+  }
+  const int n_pick = min(kc == 0 ? 0 : a.k + kSpare, a.V);
   if (tid == 0) ids[n_pick] = target;
-  if (tid < SM_WARPS * kc) {
-    const int w0 = tid / kc, at = w0 * kMaxCand + tid % kc;
-    const float x = px[at];
-    const int id = pv[at];
+  __syncthreads();
+  // a candidate's rank: how many come before it (their order in memory is of no matter)
+  const int nc = n_cand;
+  for (int i = warp; i < nc; i += SM_WARPS) {
+    const float x = cand[i].x;
+    const int id = cand[i].v;
     int rank = 0;
-    for (int w = 0; w < SM_WARPS; ++w)
-      for (int p = 0; p < kc; ++p) rank += sc_better(px[w * kMaxCand + p], pv[w * kMaxCand + p], x, id);
-    if (rank < n_pick && id != 0x7fffffff) ids[rank] = id;
+    for (int j = lane; j < nc; j += 32) rank += sc_better(cand[j].x, cand[j].v, x, id);
+    rank = __reduce_add_sync(0xffffffffu, rank);
+    if (lane == 0 && rank < n_pick) ids[rank] = id;
   }
   __syncthreads();
-  const float* yr = a.y + (size_t)row * a.y_stride;
   for (int p0 = warp; p0 <= n_pick; p0 += 2 * SM_WARPS) {
-    // two tokens at a time, 1024 elements of each requested at once
+    // two tokens, 1024 elements of each requested at once
     double acc[2][2] = {{0.0, 0.0}, {0.0, 0.0}};
     const __half* e[2];
     bool has[2];
@@ -820,17 +837,18 @@ __global__ void __launch_bounds__(SM_THREADS) score_merge_kernel(ScoreArgs a, in
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         if (j0 + 256 * q >= a.d) break;
-        const float4 y0 = *reinterpret_cast<const float4*>(yr + j0 + 256 * q);
-        const float4 y1 = *reinterpret_cast<const float4*>(yr + j0 + 256 * q + 4);
-        const float yy[8] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w};
+        double2 yy[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) yy[i] = *reinterpret_cast<const double2*>(yd + j0 + 256 * q + 2 * i);
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
+          if (!has[u]) continue;
           const uint32_t ww[4] = {w[u][q].x, w[u][q].y, w[u][q].z, w[u][q].w};
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&ww[i]));
-            acc[u][0] = fma((double)f.x, (double)yy[2 * i], acc[u][0]);
-            acc[u][1] = fma((double)f.y, (double)yy[2 * i + 1], acc[u][1]);
+            acc[u][0] = fma((double)f.x, yy[i].x, acc[u][0]);
+            acc[u][1] = fma((double)f.y, yy[i].y, acc[u][1]);
           }
         }
       }
@@ -843,21 +861,29 @@ __global__ void __launch_bounds__(SM_THREADS) score_merge_kernel(ScoreArgs a, in
       if (lane == 0 && p0 + u * SM_WARPS <= n_pick) zs[p0 + u * SM_WARPS] = z;
     }
   }
+  constexpr double kLn2 = 0.693147180559945309;
+  const double log_l = log((double)L), lse = (double)M * kLn2 + log_l;
   __syncthreads();
+  if (tid == 0 && a.entropy) a.entropy[row] = (float)(log_l - (double)S / (double)L * kLn2);
   if (tid == 0 && a.logp)
     a.logp[row] = target < 0 ? 0.f : target >= a.V ? CUDART_NAN_F : (float)(zs[n_pick] - lse);
-  // each candidate's rank among them; the first k are the answer
-  if (tid < n_pick) {
-    int rank = 0;
-    for (int p = 0; p < n_pick; ++p) rank += zs[p] > zs[tid] || (zs[p] == zs[tid] && ids[p] < ids[tid]);
-    if (rank < a.k) {
-      a.top_ids[(size_t)row * a.k + rank] = ids[tid];
-      a.top_logp[(size_t)row * a.k + rank] = (float)(zs[tid] - lse);
+  // the chosen ones' final order: a warp per token, a lane per rival
+  for (int i = warp; i < n_pick; i += SM_WARPS) {
+    const double z = zs[i];
+    const int id = ids[i];
+    const bool before = lane < n_pick && (zs[lane] > z || (zs[lane] == z && ids[lane] < id));
+    const int rank = __popc(__ballot_sync(0xffffffffu, before));
+    if (lane == 0 && rank < a.k) {
+      a.top_ids[(size_t)row * a.k + rank] = id;
+      a.top_logp[(size_t)row * a.k + rank] = (float)(z - lse);
     }
   }
 }
 
-int score_cand(int k) { return k == 0 ? 0 : k <= 4 ? 8 : k <= 8 ? 12 : 20; }
+size_t score_merge_smem(int slices, int kc, int d) { return (size_t)d * 8 + (size_t)slices * kc * sizeof(ScoreCand); }
+
+// candidates a slice keeps: k + kSpare, in the sizes that are instantiated
+int score_cand(int k) { return k == 0 ? 0 : k + kSpare <= 8 ? 8 : k + kSpare <= 12 ? 12 : 20; }
 
 constexpr int kScoreChunk = 37 * 128;  // rows per sweep over the embedding: bounds the workspace; 37 row
                                        // tiles share 148 SMs evenly
@@ -955,7 +981,7 @@ tl_status launch_score_head(const ScoreArgs& a0, cudaStream_t s) {
   static std::atomic<uint64_t> attr_done{0};
   TL_TRY(once_per_device(attr_done, []() -> tl_status {
     TL_CUDA(cudaFuncSetAttribute(score_merge_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (kMaxSlices + 31) * kMaxCand * 8));
+                                 (int)score_merge_smem(kMaxSlices, kMaxCand, 8192)));
     return ok();
   }));
   for (int r0 = 0; r0 < a0.n; r0 += kScoreChunk) {
@@ -988,7 +1014,7 @@ tl_status launch_score_head(const ScoreArgs& a0, cudaStream_t s) {
     TL_TRY(kc == 0 ? launch_score_pass1<0>(p, my, me, s)
                    : kc == 8 ? launch_score_pass1<8>(p, my, me, s)
                              : kc == 12 ? launch_score_pass1<12>(p, my, me, s) : launch_score_pass1<20>(p, my, me, s));
-    TL_LAUNCH_PDL(score_merge_kernel, a.n, SM_THREADS, (size_t)((t.slices + 31) & ~31) * kc * 8, s, a, kc, t);
+    TL_LAUNCH_PDL(score_merge_kernel, a.n, SM_THREADS, score_merge_smem(t.slices, kc, a.d), s, a, kc, t);
   }
   return ok();
 }
