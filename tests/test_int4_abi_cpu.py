@@ -136,14 +136,14 @@ def test_the_binding_refuses_what_the_library_cannot_see():
         tl.tl_score_head(torch.zeros(4, 64, dtype=torch.bfloat16), torch.zeros(1, 64), None, None, None, None, None,
                          torch.zeros(1, dtype=torch.uint8))
     with pytest.raises(tl.TLError, match="shape"):
-        tl._kv_int4("x", c(), p()[:, :, :4], c(), p(), None, None)
+        tl._kv_int4("x", c(), p()[:, :, :4], c(), p())
     with pytest.raises(tl.TLError, match="strides"):
         wide = torch.zeros(lanes, H * ctx + 4, hd // 8, dtype=torch.int32)
         far = torch.as_strided(wide, (lanes, H, ctx, hd // 8), (wide.stride(0), ctx * hd // 8, hd // 8, 1))
-        tl._kv_int4("x", far, p(), c(), p(), None, None)
+        tl._kv_int4("x", far, p(), c(), p())
     with pytest.raises(tl.TLError, match="contiguous"):
-        tl._kv_int4("x", c().transpose(1, 2).contiguous().transpose(1, 2), p(), c(), p(), None, None)
-    d = tl._kv_int4("x", c(), p(), c(), p(), None, None)
+        tl._kv_int4("x", c().transpose(1, 2).contiguous().transpose(1, 2), p(), c(), p())
+    d = tl._kv_int4("x", c(), p(), c(), p())
     assert (d.n_lanes, d.n_heads, d.head_dim, d.max_ctx) == (lanes, H, hd, ctx)
     assert (d.code_stride, d.param_stride) == (H * ctx * hd // 8, H * ctx * hd // 32)
 

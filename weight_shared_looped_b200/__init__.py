@@ -195,87 +195,116 @@ def tl_attention_prefill(q, k, v, H: int, hd: int, out, stream=None) -> None:
 
 
 # --------------------------------------------------------------------- 4-bit KV cache
+# These calls take tensors of free shapes and are made once a layer or a step, so
+# what the C side cannot see (types, shapes, layouts, devices) is checked here in a
+# few attribute reads; only when a check fails is it worked out which.
 
 def _fail(message: str) -> None:
     raise TLError(TL_ERR_INVALID_ARG, message)
 
 
-def _tensors(what: str, **named):
-    """Checks that the C side cannot make: every tensor (None entries aside) is a CUDA
-    tensor of the given type and number of dimensions, all on one device.  named: name ->
-    (tensor, torch dtypes, dims).  Returns the device."""
-    device = None
+_TORCH: dict = {}
+
+
+def _torch_names() -> dict:
+    if not _TORCH:
+        import torch
+        f16 = {torch.float16: True, torch.int16: True}   # fp16 values, also as raw bits
+        _TORCH.update(f16=f16, i32=torch.int32, f32=torch.float32, u8=torch.uint8,
+                      stream=getattr(torch._C, "_cuda_getCurrentRawStream", None),
+                      device=getattr(torch._C, "_cuda_getDevice", None), torch=torch)
+    return _TORCH
+
+
+def _explain(what: str, **named) -> None:
+    """Raises for the first tensor that is not of its types and dimensions, not on a CUDA
+    device, or on another device than the first.  named: name -> (tensor, dtypes, dims)."""
     named = {name: v for name, v in named.items() if v[0] is not None}
     for name, (t, dtypes, dims) in named.items():
         if t.dtype not in dtypes:
             _fail(f"{what}: {name} has dtype {t.dtype}, not {' or '.join(str(d) for d in dtypes)}")
         if t.dim() != dims:
             _fail(f"{what}: {name} has {t.dim()} dimensions, not {dims}")
+    device = None
     for name, (t, _, _) in named.items():
         if not t.is_cuda:
             _fail(f"{what}: {name} is not on a CUDA device")
-        if device is None:
-            device = t.device
-        elif t.device != device:
+        device = t.device if device is None else device
+        if t.device != device:
             _fail(f"{what}: {name} is on {t.device}, not {device}")
-    return device
 
 
-def _dtypes():
-    """fp16 values (also as raw int16 bits), int32, fp32, 4-byte parameter pairs."""
-    import torch
-    return (torch.float16, torch.int16), (torch.int32,), (torch.float32,)
-
-
-def _on(device, call, *args, stream=None) -> None:
-    """The C call on `device`'s current stream (or `stream`), with `device` current."""
-    import torch
-    if device.index == torch.cuda.current_device():
-        _check(call(*args, _stream(stream)))
+def _launch(n, device: int, stream, call, *args) -> None:
+    """The C call on `stream` (default: `device`'s current one) with `device` current."""
+    if stream is not None:
+        s = _stream(stream)
+    elif n["stream"] is not None:
+        s = n["stream"](device)
     else:
-        with torch.cuda.device(device):
-            _check(call(*args, _stream(stream)))
+        s = n["torch"].cuda.current_stream(device).cuda_stream
+    now = n["device"]() if n["device"] is not None else n["torch"].cuda.current_device()
+    if now == device:
+        _check(call(*args, s))
+    else:
+        with n["torch"].cuda.device(device):
+            _check(call(*args, s))
 
 
-def _kv_int4(what: str, k_codes, k_params, v_codes, v_params, f16, i32):
+def _kv_int4(what: str, k_codes, k_params, v_codes, v_params) -> KvInt4Desc:
     """The cache description of codes int32 [lanes, heads, ctx, hd / 8] and parameters fp16
     [lanes, heads, ctx, hd / 32, 2]; only the lane stride is free."""
-    lanes, heads, ctx, words = k_codes.shape
-    strides = []
-    for name, t, want in (("k_codes", k_codes, (lanes, heads, ctx, words)),
-                          ("v_codes", v_codes, (lanes, heads, ctx, words)),
-                          ("k_params", k_params, (lanes, heads, ctx, words // 4, 2)),
-                          ("v_params", v_params, (lanes, heads, ctx, words // 4, 2))):
-        if tuple(t.shape) != want:
-            _fail(f"{what}: {name} has shape {tuple(t.shape)}, not {want}")
-        if not t.is_contiguous() and not (lanes > 0 and t[0].is_contiguous()):
-            _fail(f"{what}: {name} is not contiguous within a lane")
-        inner = want[1] * want[2] * want[3] * (2 if len(want) == 5 else 1)
-        strides.append(t.stride(0) if lanes > 1 else inner)
-    if strides[0] != strides[1] or strides[2] != strides[3] or strides[2] % 2:
-        _fail(f"{what}: K and V have different lane strides")
-    return KvInt4Desc(_ptr(k_codes), _ptr(v_codes), _ptr(k_params), _ptr(v_params), strides[0],
-                      strides[2] // 2, lanes, heads, words * 8, ctx)
+    shape, pshape = k_codes.shape, k_params.shape
+    lanes, heads, ctx, words = shape
+    if (v_codes.shape != shape or v_params.shape != pshape
+            or pshape != (lanes, heads, ctx, words // 4, 2)):
+        _fail(f"{what}: codes {tuple(shape)} and {tuple(v_codes.shape)}, parameters {tuple(pshape)} and "
+              f"{tuple(v_params.shape)} do not have the shapes [lanes, heads, ctx, hd / 8] and "
+              "[lanes, heads, ctx, hd / 32, 2]")
+    if (k_codes.is_contiguous() and k_params.is_contiguous() and v_codes.is_contiguous()
+            and v_params.is_contiguous()):
+        cs, ps = heads * ctx * words, heads * ctx * (words // 4)
+    else:
+        for name, t in (("k_codes", k_codes), ("k_params", k_params), ("v_codes", v_codes),
+                        ("v_params", v_params)):
+            if lanes == 0 or not t[0].is_contiguous():
+                _fail(f"{what}: {name} is not contiguous within a lane")
+        cs, ps = k_codes.stride(0), k_params.stride(0)
+        if lanes > 1 and (v_codes.stride(0) != cs or v_params.stride(0) != ps or ps % 2):
+            _fail(f"{what}: K and V have different lane strides")
+        ps //= 2
+    return KvInt4Desc(k_codes.data_ptr(), v_codes.data_ptr(), k_params.data_ptr(),
+                      v_params.data_ptr(), cs, ps, lanes, heads, words * 8, ctx)
 
 
 def _kv_int4_rows(what, fn, k, v, k_codes, k_params, v_codes, v_params, pos, cu, stream):
-    f16, i32, _ = _dtypes()
-    device = _tensors(what, k=(k, f16, 2), v=(v, f16, 2), k_codes=(k_codes, i32, 4),
-                      k_params=(k_params, f16, 5), v_codes=(v_codes, i32, 4),
-                      v_params=(v_params, f16, 5), pos=(pos, i32, 1), cu=(cu, i32, 1))
-    d = _kv_int4(what, k_codes, k_params, v_codes, v_params, f16, i32)
-    n, width = k.shape
-    if tuple(v.shape) != (n, width) or width != d.n_heads * d.head_dim:
+    n = _TORCH or _torch_names()
+    f16, i32 = n["f16"], n["i32"]
+    dev = k.get_device()
+    if not (dev >= 0 and k.dtype in f16 and v.dtype in f16 and k_codes.dtype is i32
+            and v_codes.dtype is i32 and k_params.dtype in f16 and v_params.dtype in f16
+            and pos.dtype is i32 and (cu is None or cu.dtype is i32)
+            and k.dim() == 2 == v.dim() and k_codes.dim() == 4 == v_codes.dim()
+            and k_params.dim() == 5 == v_params.dim() and pos.dim() == 1
+            and (cu is None or (cu.dim() == 1 and cu.get_device() == dev))
+            and v.get_device() == dev == k_codes.get_device() == v_codes.get_device()
+            and k_params.get_device() == dev == v_params.get_device() == pos.get_device()):
+        i = (i32,)
+        _explain(what, k=(k, f16, 2), v=(v, f16, 2), k_codes=(k_codes, i, 4), k_params=(k_params, f16, 5),
+                 v_codes=(v_codes, i, 4), v_params=(v_params, f16, 5), pos=(pos, i, 1), cu=(cu, i, 1))
+    d = _kv_int4(what, k_codes, k_params, v_codes, v_params)
+    rows, width = k.shape
+    if v.shape != k.shape or width != d.n_heads * d.head_dim:
         _fail(f"{what}: k {tuple(k.shape)} and v {tuple(v.shape)} are not rows of "
               f"{d.n_heads} x {d.head_dim} values")
-    if n and (k.stride(1) != 1 or v.stride(1) != 1 or (n > 1 and k.stride(0) != v.stride(0))):
+    stride, unit = k.stride()
+    if rows and (unit != 1 or v.stride() != (stride, 1)) and (rows > 1 or unit != 1 or v.stride(1) != 1):
         _fail(f"{what}: k and v need unit column stride and the same row stride")
     if pos.shape[0] != d.n_lanes or not pos.is_contiguous():
         _fail(f"{what}: pos is not a contiguous [{d.n_lanes}]")
     if cu is not None and (cu.shape[0] != d.n_lanes + 1 or not cu.is_contiguous()):
         _fail(f"{what}: cu is not a contiguous [{d.n_lanes + 1}]")
-    stride = k.stride(0) if n > 1 else width
-    _on(device, fn, ctypes.byref(d), _ptr(k), _ptr(v), stride, _ptr(cu), _ptr(pos), n, stream=stream)
+    _launch(n, dev, stream, fn, d, k.data_ptr(), v.data_ptr(), stride if rows > 1 else width,
+            None if cu is None else cu.data_ptr(), pos.data_ptr(), rows)
 
 
 def tl_kv_write_int4(k, v, k_codes, k_params, v_codes, v_params, pos, cu=None, stream=None) -> None:
@@ -296,30 +325,42 @@ def tl_attention_int4(q, k_codes, k_params, v_codes, v_params, lens, out, n_q: i
                       window: int = 0, stream=None) -> None:
     """q, out: fp16 [lanes * n_q, q_heads * hd]; lens int32 [lanes], the queries' own
     positions included."""
-    f16, i32, _ = _dtypes()
+    n = _TORCH or _torch_names()
+    f16, i32 = n["f16"], n["i32"]
     what = "tl_attention_int4"
-    device = _tensors(what, q=(q, f16, 2), k_codes=(k_codes, i32, 4), k_params=(k_params, f16, 5),
-                      v_codes=(v_codes, i32, 4), v_params=(v_params, f16, 5), lens=(lens, i32, 1),
-                      out=(out, f16, 2))
-    d = _kv_int4(what, k_codes, k_params, v_codes, v_params, f16, i32)
-    n, width = q.shape
-    if n != d.n_lanes * n_q or width % d.head_dim or tuple(out.shape) != (n, width):
+    dev = q.get_device()
+    if not (dev >= 0 and q.dtype in f16 and out.dtype in f16 and k_codes.dtype is i32
+            and v_codes.dtype is i32 and k_params.dtype in f16 and v_params.dtype in f16
+            and lens.dtype is i32 and q.dim() == 2 == out.dim()
+            and k_codes.dim() == 4 == v_codes.dim() and k_params.dim() == 5 == v_params.dim()
+            and lens.dim() == 1 and out.get_device() == dev == k_codes.get_device()
+            and v_codes.get_device() == dev == k_params.get_device()
+            and v_params.get_device() == dev == lens.get_device()):
+        i = (i32,)
+        _explain(what, q=(q, f16, 2), k_codes=(k_codes, i, 4), k_params=(k_params, f16, 5),
+                 v_codes=(v_codes, i, 4), v_params=(v_params, f16, 5), lens=(lens, i, 1), out=(out, f16, 2))
+    d = _kv_int4(what, k_codes, k_params, v_codes, v_params)
+    rows, width = q.shape
+    if rows != d.n_lanes * n_q or width % d.head_dim or out.shape != q.shape:
         _fail(f"{what}: q {tuple(q.shape)} and out {tuple(out.shape)} are not {d.n_lanes} x {n_q} "
               f"rows of heads of {d.head_dim}")
-    if n and (q.stride(1) != 1 or out.stride(1) != 1):
+    qs, qu = q.stride()
+    os_, ou = out.stride()
+    if rows and (qu != 1 or ou != 1):
         _fail(f"{what}: q and out need unit column stride")
     if lens.shape[0] != d.n_lanes or not lens.is_contiguous():
         _fail(f"{what}: lens is not a contiguous [{d.n_lanes}]")
-    _on(device, lib.tl_attention_int4, ctypes.byref(d), _ptr(q), q.stride(0) if n > 1 else width,
-        n_q, width // d.head_dim, _ptr(lens), window, _ptr(out),
-        out.stride(0) if n > 1 else width, stream=stream)
+    if rows <= 1:
+        qs = os_ = width
+    _launch(n, dev, stream, lib.tl_attention_int4, d, q.data_ptr(), qs, n_q, width // d.head_dim,
+            lens.data_ptr(), window, out.data_ptr(), os_)
 
 
 # --------------------------------------------------------------------- scoring head
 
 def tl_score_head_workspace_bytes(n: int, vocab: int, d: int, k: int) -> int:
     b = SZ()
-    _check(lib.tl_score_head_workspace_bytes(n, vocab, d, k, ctypes.byref(b)))
+    _check(lib.tl_score_head_workspace_bytes(n, vocab, d, k, b))
     return b.value
 
 
@@ -329,16 +370,29 @@ def tl_score_head(embed, y, targets, logp, entropy, top_ids, top_logp, workspace
     fp16 [vocab, d]) into logp fp32 [n]; entropy fp32 [n]; the k most probable tokens into
     top_ids int32 [n, k] and top_logp fp32 [n, k].  targets with logp, entropy, and top_ids
     with top_logp may be None."""
-    f16, i32, f32 = _dtypes()
+    n_ = _TORCH or _torch_names()
+    f16, i32, f32 = n_["f16"], n_["i32"], n_["f32"]
     what = "tl_score_head"
-    device = _tensors(what, embed=(embed, f16, 2), y=(y, f32, 2), targets=(targets, i32, 1),
-                      logp=(logp, f32, 1), entropy=(entropy, f32, 1), top_ids=(top_ids, i32, 2),
-                      top_logp=(top_logp, f32, 2), workspace=(workspace, (_uint8(),), 1))
+    dev = y.get_device()
+    ok = (dev >= 0 and embed.dtype in f16 and y.dtype is f32 and workspace.dtype is n_["u8"]
+          and embed.dim() == 2 == y.dim() and workspace.dim() == 1
+          and embed.get_device() == dev == workspace.get_device())
+    for t, dtype, dims in ((targets, i32, 1), (logp, f32, 1), (entropy, f32, 1), (top_ids, i32, 2),
+                           (top_logp, f32, 2)):
+        ok = ok and (t is None or (t.dtype is dtype and t.dim() == dims and t.get_device() == dev
+                                   and t.is_contiguous()))
+    if not ok:
+        i, f = (i32,), (f32,)
+        _explain(what, embed=(embed, f16, 2), y=(y, f, 2), targets=(targets, i, 1), logp=(logp, f, 1),
+                 entropy=(entropy, f, 1), top_ids=(top_ids, i, 2), top_logp=(top_logp, f, 2),
+                 workspace=(workspace, (n_["u8"],), 1))
+        _fail(f"{what}: an output or the targets are not contiguous")
     n, d = y.shape
-    vocab = embed.shape[0]
-    if embed.shape[1] != d or not embed.is_contiguous():
+    vocab, ed = embed.shape
+    if ed != d or not embed.is_contiguous():
         _fail(f"{what}: embed {tuple(embed.shape)} is not a contiguous [vocab, {d}]")
-    if n and y.stride(1) != 1:
+    ys, unit = y.stride()
+    if n and unit != 1:
         _fail(f"{what}: y needs unit column stride")
     if (top_ids is None) != (top_logp is None):
         _fail(f"{what}: top_ids and top_logp go together")
@@ -346,16 +400,12 @@ def tl_score_head(embed, y, targets, logp, entropy, top_ids, top_logp, workspace
     for name, t, want in (("targets", targets, (n,)), ("logp", logp, (n,)),
                           ("entropy", entropy, (n,)), ("top_ids", top_ids, (n, k)),
                           ("top_logp", top_logp, (n, k))):
-        if t is not None and (tuple(t.shape) != want or not t.is_contiguous()):
-            _fail(f"{what}: {name} is not a contiguous {want}")
-    _on(device, lib.tl_score_head, _ptr(embed), vocab, d, _ptr(y), y.stride(0) if n > 1 else d, n,
-        _ptr(targets), _ptr(logp), _ptr(entropy), k, _ptr(top_ids) if k else None,
-        _ptr(top_logp) if k else None, _ptr(workspace), workspace.numel(), stream=stream)
-
-
-def _uint8():
-    import torch
-    return torch.uint8
+        if t is not None and t.shape != want:
+            _fail(f"{what}: {name} has shape {tuple(t.shape)}, not {want}")
+    _launch(n_, dev, stream, lib.tl_score_head, embed.data_ptr(), vocab, d, y.data_ptr(),
+            ys if n > 1 else d, n, _ptr(targets), _ptr(logp), _ptr(entropy), k,
+            _ptr(top_ids) if k else None, _ptr(top_logp) if k else None, workspace.data_ptr(),
+            workspace.numel())
 
 
 # --------------------------------------------------------------------- blocks / model
