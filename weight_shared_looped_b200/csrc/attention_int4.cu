@@ -10,12 +10,13 @@
 // Codes become fp16 values in registers (three half2 operations a pair: the
 // nibble under the exponent of 1024, less the bias, times the scale plus the
 // zero point; the one rounding of the value to fp16 is the read-back's own), so
-// the cache is read once, as it is stored, straight from global memory: in
-// the K tile lane (g, t) takes a whole 32-code group of keys g and g + 8, in
-// the V tile the same 16 head_dim elements of four keys; every load instruction
-// of a warp covers whole contiguous rows, and the k order inside an MMA
-// is free as long as both operands agree.  A warp's next tile is requested
-// before the current one is used.
+// the cache is read once, as it is stored: each warp copies its tiles of 16 keys
+// (2.5 KB for head_dim 128) through a ring of its own in shared memory, three tiles
+// ahead (loads into registers one tile ahead left a warp waiting for memory at
+// every tile: 1.3 us a tile against 0.2 of work).  From the K tile lane (g, t)
+// takes a whole 32-code group of two keys, from the V tile the same 16 head_dim
+// elements of four keys; the k order inside an MMA is free as long as both
+// operands agree, and is chosen so that no read has a bank conflict.
 //
 // Bound by memory (head_dim 128: 160 bytes per key and head); about 280
 // instructions per 16 keys keep the issue slots about two thirds busy at that
@@ -50,6 +51,7 @@ namespace {
 constexpr int A4_COLS = 8;          // queries per CTA (MMA N)
 constexpr int A4_TILE = 16;         // keys per warp tile (MMA M)
 constexpr int A4_MAX_CLUSTER = 16;
+constexpr int A4_STAGES = 4;         // tiles of a warp's ring
 constexpr float A4_SLACK = 8.f;     // the running maximum may lag by 2^8
 constexpr float A4_NONE = -1e30f;   // below every score: no key yet
 
@@ -59,6 +61,12 @@ __device__ __forceinline__ void a4_mma(float* c, const uint32_t* a, uint32_t b0,
       "{%8,%9}, {%0,%1,%2,%3};\n"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ float a4_ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 // 8x8 transpose of fp16 pairs across the warp
@@ -85,17 +93,22 @@ __device__ __forceinline__ float a4_remote(const float* local, uint32_t rank) {
 }
 
 // Words of a row's codes that one lane holds: K, a run of head_dim / 4 codes;
-// V, head_dim / 8 codes of each of four keys.
+// V, head_dim / 8 codes of each of four keys.  A tile in shared memory: K rows, V
+// rows, K parameters, V parameters, as the cache has them; of the V rows, those
+// with bit 2 set have their 16-byte pieces swapped in pairs.
 template <int HD>
 struct A4 {
   static constexpr int KW = HD / 32, VW = HD / 64;
   static constexpr int KSTEPS = HD / 16, MT = HD / 16;
   static constexpr int RW = HD / 8;               // code words per row
   static constexpr int RP = HD / kInt4Group;      // parameter pairs per row
+  static constexpr int V0 = A4_TILE * RW, KP0 = 2 * V0, VP0 = KP0 + A4_TILE * RP;
+  static constexpr int WORDS = VP0 + A4_TILE * RP;   // words of a tile
+  static constexpr int VSWAP = HD == 128 ? 8 : 0;    // word index bit the swap flips
 };
 
 template <int N>
-__device__ __forceinline__ void a4_load(uint32_t* r, const uint32_t* p) {
+__device__ __forceinline__ void a4_lds(uint32_t* r, const uint32_t* p) {
   if constexpr (N == 4) {
     const uint4 v = *reinterpret_cast<const uint4*>(p);
     r[0] = v.x;
@@ -111,22 +124,26 @@ __device__ __forceinline__ void a4_load(uint32_t* r, const uint32_t* p) {
   }
 }
 
-template <int HD>
-struct A4Tile {
-  uint32_t k[2][A4<HD>::KW], kp[2];
-  uint32_t v[4][A4<HD>::VW], vp[4];
-};
+__device__ __forceinline__ void a4_copy16(uint32_t* dst, const uint32_t* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
+               : "memory");
+}
 
 // a parameter pair whose values might not be finite in fp16
 __device__ __forceinline__ bool a4_odd(uint32_t p) {
   return (p & 0x7fffu) >= 0x6800u || ((p >> 16) & 0x7fffu) >= 0x7800u;
 }
 
+__device__ __forceinline__ void a4_copy4(uint32_t* dst, const uint32_t* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
+               : "memory");
+}
+
 template <int HD>
 __global__ void __launch_bounds__(512) attn_int4_kernel(AttnInt4Args a) {
   using C = A4<HD>;
   pdl_enter();
-  extern __shared__ __align__(16) float a4_smem[];
+  extern __shared__ __align__(128) float a4_smem[];
   const int nw = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const int cls = gridDim.x, rank = blockIdx.x;
@@ -163,12 +180,6 @@ __global__ void __launch_bounds__(512) attn_int4_kernel(AttnInt4Args a) {
   auto first_of = [&](int last) { return a.window > 0 ? max(0, last - a.window + 1) : 0; };
   const int lo_all = first_of(last_of(c0)), hi_all = last_of(c0 + cols - 1);
   const int full_lo = first_of(hi_all), full_hi = last_of(c0);   // seen by every column
-  int chi[2], clo[2];                                            // this lane's columns 2t, 2t + 1
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    chi[e] = last_of(c0 + min(2 * t + e, cols - 1));
-    clo[e] = first_of(chi[e]);
-  }
 
   // q as the B operand: column g, k step s = 2 jj + h covers the pairs (i, i + 4)
   // of word KW * t + jj with i = 2h (k indices 2t, 2t + 1) and 2h + 1 (+ 8)
@@ -192,41 +203,63 @@ __global__ void __launch_bounds__(512) attn_int4_kernel(AttnInt4Args a) {
 #pragma unroll
   for (int i = 0; i < C::MT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
 
-  // MMA row r stands for key kr(r) of the tile: the four keys of a lane's V
-  // pairs are then t, t + 4, t + 8, t + 12, and each load covers contiguous rows
-  const int kr = (g >> 1) + 4 * (g & 1);
+  // MMA row r stands for key kr(r) of the tile: a lane's V pairs are then the keys
+  // kr(2t), kr(2t + 1) and those + 8, and the reads of a quarter (half) warp fall on
+  // distinct banks
+  const int kr = g ^ ((g >> 1) & 1);
+  const int vk[4] = {2 * t ^ (t & 1), (2 * t + 1) ^ (t & 1), (2 * t ^ (t & 1)) + 8, ((2 * t + 1) ^ (t & 1)) + 8};
   const int slots = cls * nw;
   const int slot = rank * nw + warp;
   const int tile_lo = lo_all / A4_TILE;
   const int tile_hi = hi_all < 0 ? -1 : hi_all / A4_TILE;      // last tile with a key
   int tile = tile_lo + (slot - tile_lo % slots + slots) % slots;
-  auto fetch = [&](int ti, A4Tile<HD>& d) {
-    const int base = ti * A4_TILE;
+  uint32_t* ring = reinterpret_cast<uint32_t*>(a4_smem) + (size_t)warp * A4_STAGES * C::WORDS;
+  // head_dim 64 with an odd max_ctx, or a caller's strides, leave parameters on 4 bytes
+  const bool par16 = (((uintptr_t)kp | (uintptr_t)vp) & 15) == 0;
+  // copies tile ti into its ring slot: whole 16-byte pieces, in the order of memory;
+  // where the cache ends inside the tile its last row repeats
+  auto fetch = [&](int ti, int slot_) {
+    uint32_t* dst = ring + slot_ * C::WORDS;
+    const int base = ti * A4_TILE, last = a.max_ctx - 1;
+    constexpr int PR = C::RW / 4;                  // pieces per code row
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int key = min(base + kr + 8 * h, hi_all);          // a masked place repeats the last key
-      a4_load<C::KW>(d.k[h], kc + (size_t)key * C::RW + C::KW * t);
-      d.kp[h] = kp[(size_t)key * C::RP + (HD == 128 ? t : t >> 1)];
+    for (int i = 0; i < A4_TILE * PR / 32; ++i) {
+      const int p = lane + 32 * i, r = p / PR, c = p % PR;
+      const size_t src = (size_t)min(base + r, last) * C::RW + 4 * c;
+      a4_copy16(dst + 4 * p, kc + src);
+      a4_copy16(dst + C::V0 + r * C::RW + ((4 * c) ^ ((r & 4) ? C::VSWAP : 0)), vc + src);
     }
-#pragma unroll
-    for (int h = 0; h < 4; ++h) {
-      const int key = min(base + t + 4 * h, hi_all);
-      a4_load<C::VW>(d.v[h], vc + (size_t)key * C::RW + C::VW * g);
-      d.vp[h] = vp[(size_t)key * C::RP + (HD == 128 ? g >> 1 : g >> 2)];
+    if (par16 && base + A4_TILE <= a.max_ctx) {
+      constexpr int NP = A4_TILE * C::RP / 4;      // 16-byte pieces of K's parameters (and of V's)
+      if (lane < 2 * NP) {
+        const int p = lane % NP;
+        a4_copy16(dst + (lane < NP ? C::KP0 : C::VP0) + 4 * p, (lane < NP ? kp : vp) + (size_t)base * C::RP + 4 * p);
+      }
+    } else {
+#pragma unroll 1
+      for (int p = lane; p < A4_TILE * C::RP; p += 32) {
+        const size_t src = (size_t)min(base + p / C::RP, last) * C::RP + p % C::RP;
+        a4_copy4(dst + C::KP0 + p, kp + src);
+        a4_copy4(dst + C::VP0 + p, vp + src);
+      }
     }
   };
 
   // O^T += V^T P^T for one tile; only: -1, or the one column that takes it
-  auto pv = [&](const A4Tile<HD>& d, const uint32_t* prm, uint32_t pb0, uint32_t pb1, int only) {
+  auto pv = [&](const uint32_t* tw, const uint32_t* prm, uint32_t pb0, uint32_t pb1, int only) {
+    uint32_t dv[4][C::VW];
+#pragma unroll
+    for (int h = 0; h < 4; ++h)
+      a4_lds<C::VW>(dv[h], tw + C::V0 + vk[h] * C::RW + ((C::VW * g) ^ ((vk[h] & 4) ? C::VSWAP : 0)));
     const __half2 s0 = kv_bits_h2(__byte_perm(prm[0], prm[1], 0x5410)), z0 = kv_bits_h2(__byte_perm(prm[0], prm[1], 0x7632));
     const __half2 s1 = kv_bits_h2(__byte_perm(prm[2], prm[3], 0x5410)), z1 = kv_bits_h2(__byte_perm(prm[2], prm[3], 0x7632));
 #pragma unroll
     for (int j = 0; j < C::VW; ++j) {
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
-        // nibbles 4hf .. 4hf + 3 of the word, keys (t, t + 4) and (t + 8, t + 12) paired
-        uint32_t x0 = __byte_perm(d.v[0][j], d.v[1][j], hf ? 0x7632 : 0x5410);
-        uint32_t x1 = __byte_perm(d.v[2][j], d.v[3][j], hf ? 0x7632 : 0x5410);
+        // nibbles 4hf .. 4hf + 3 of the word, the lane's keys paired
+        uint32_t x0 = __byte_perm(dv[0][j], dv[1][j], hf ? 0x7632 : 0x5410);
+        uint32_t x1 = __byte_perm(dv[2][j], dv[3][j], hf ? 0x7632 : 0x5410);
 #pragma unroll
         for (int sel = 0; sel < 2; ++sel) {
           uint32_t af[4];
@@ -244,28 +277,43 @@ __global__ void __launch_bounds__(512) attn_int4_kernel(AttnInt4Args a) {
             for (int e = 0; e < 4; ++e)
               if (2 * t + (e & 1) == only) acc[e] = r[e];
           }
-          x0 >>= 8;
-          x1 >>= 8;
+          if (sel == 0) {
+            x0 >>= 8;
+            x1 >>= 8;
+          }
         }
       }
     }
   };
 
-  A4Tile<HD> cur;
-  if (tile <= tile_hi) fetch(tile, cur);
-  while (tile <= tile_hi) {
-    const int next = tile + slots;
-    A4Tile<HD> nxt;
-    if (next <= tile_hi) fetch(next, nxt);
-    else nxt = cur;
+  int ahead = tile, in_slot = 0, out_slot = 0;
+  auto request = [&]() {                           // one group per tile, empty behind the last
+    if (ahead <= tile_hi) fetch(ahead, in_slot);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    ahead += slots;
+    in_slot = in_slot + 1 == A4_STAGES ? 0 : in_slot + 1;
+  };
+#pragma unroll
+  for (int i = 0; i < A4_STAGES - 1; ++i) request();
+#pragma unroll 1
+  for (; tile <= tile_hi; tile += slots) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(A4_STAGES - 2) : "memory");
+    __syncwarp();                                  // every lane's copies of this tile; the slot before is free
+    request();
+    const uint32_t* tw = ring + out_slot * C::WORDS;
+    out_slot = out_slot + 1 == A4_STAGES ? 0 : out_slot + 1;
     // S^T = K q^T: lane (g, t) gets keys kr and kr + 8, columns 2t and 2t + 1
     float s[4] = {0.f, 0.f, 0.f, 0.f};
     {
-      const __half2 p0 = kv_bits_h2(cur.kp[0]), p1 = kv_bits_h2(cur.kp[1]);
+      uint32_t k0[C::KW], k1[C::KW];
+      a4_lds<C::KW>(k0, tw + kr * C::RW + C::KW * t);
+      a4_lds<C::KW>(k1, tw + (kr + 8) * C::RW + C::KW * t);
+      const __half2 p0 = kv_bits_h2(tw[C::KP0 + kr * C::RP + (HD == 128 ? t : t >> 1)]);
+      const __half2 p1 = kv_bits_h2(tw[C::KP0 + (kr + 8) * C::RP + (HD == 128 ? t : t >> 1)]);
       const __half2 s0 = __low2half2(p0), z0 = __high2half2(p0), s1 = __low2half2(p1), z1 = __high2half2(p1);
 #pragma unroll
       for (int jj = 0; jj < C::KW; ++jj) {
-        uint32_t x0 = cur.k[0][jj], x1 = cur.k[1][jj];
+        uint32_t x0 = k0[jj], x1 = k1[jj];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           uint32_t af[4];
@@ -274,33 +322,33 @@ __global__ void __launch_bounds__(512) attn_int4_kernel(AttnInt4Args a) {
           af[2] = kv_h2_bits(__hfma2(kv_int4_pair<false>(x0), s0, z0));
           af[3] = kv_h2_bits(__hfma2(kv_int4_pair<false>(x1), s1, z1));
           a4_mma(s, af, qb[2 * jj + h][0], qb[2 * jj + h][1]);
-          x0 >>= 8;
-          x1 >>= 8;
+          if (h == 0) {
+            x0 >>= 8;
+            x1 >>= 8;
+          }
         }
       }
     }
     const int base = tile * A4_TILE;
-    const bool edge = base < full_lo || base + A4_TILE - 1 > full_hi;   // uniform over the CTA's lanes
-    float x[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) x[e] = s[e] * csc;
+    const bool edge = base < full_lo || base + A4_TILE - 1 > full_hi;   // uniform over the CTA
     if (edge) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int key = base + kr + 8 * (e >> 1);
-        if (key > chi[e & 1] || key < clo[e & 1]) x[e] = -INFINITY;
+        const int key = base + kr + 8 * (e >> 1), hi = last_of(c0 + min(2 * t + (e & 1), cols - 1));
+        if (key > hi || key < first_of(hi)) s[e] = -INFINITY;
       }
     }
-    const float mx0 = fmaxf(x[0], x[2]), mx1 = fmaxf(x[1], x[3]);
-    if (__any_sync(0xffffffffu, mx0 > m[0] + A4_SLACK || mx1 > m[1] + A4_SLACK)) {
+    const float mx0 = fmaxf(s[0], s[2]), mx1 = fmaxf(s[1], s[3]);
+    if (__any_sync(0xffffffffu, mx0 * csc > m[0] + A4_SLACK || mx1 * csc > m[1] + A4_SLACK)) {
       // raise the maxima that are due, each column by its own scores alone
       float mx[2] = {mx0, mx1}, al[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
 #pragma unroll
         for (int w = 4; w < 32; w <<= 1) mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], w));
+        mx[e] *= csc;
         const bool up = mx[e] > m[e] + A4_SLACK;
-        al[e] = up ? exp2f(m[e] - mx[e]) : 1.f;
+        al[e] = up ? a4_ex2(m[e] - mx[e]) : 1.f;
         if (up) m[e] = mx[e];
         l[e] *= al[e];
       }
@@ -312,39 +360,47 @@ __global__ void __launch_bounds__(512) attn_int4_kernel(AttnInt4Args a) {
         o[i][3] *= al[1];
       }
     }
-    const float p0 = exp2f(x[0] - m[0]), p1 = exp2f(x[1] - m[1]);
-    const float p2 = exp2f(x[2] - m[0]), p3 = exp2f(x[3] - m[1]);
+    const float p0 = a4_ex2(fmaf(s[0], csc, -m[0])), p1 = a4_ex2(fmaf(s[1], csc, -m[1]));
+    const float p2 = a4_ex2(fmaf(s[2], csc, -m[0])), p3 = a4_ex2(fmaf(s[3], csc, -m[1]));
     l[0] += p0 + p2;
     l[1] += p1 + p3;
     // weights as fp16 (a rounding of 2^-11 each, of values the sum has in fp32),
     // key pairs of column g
     const uint32_t pb0 = a4_transpose(a4_pack(p0, p1)), pb1 = a4_transpose(a4_pack(p2, p3));
+    uint32_t prm[4];
+#pragma unroll
+    for (int h = 0; h < 4; ++h) prm[h] = tw[C::VP0 + vk[h] * C::RP + (HD == 128 ? g >> 1 : g >> 2)];
+    // keys that no query sees may hold anything: they count as zero
     bool odd = false;
     if (edge) {
 #pragma unroll
-      for (int h = 0; h < 4; ++h) odd |= a4_odd(cur.vp[h]);
+      for (int h = 0; h < 4; ++h) {
+        const int key = base + vk[h];
+        if (key > hi_all || key < lo_all) prm[h] = 0u;
+        odd |= a4_odd(prm[h]);
+      }
       odd = __any_sync(0xffffffffu, odd);
     }
     if (!odd) {
-      pv(cur, cur.vp, pb0, pb1, -1);
+      pv(tw, prm, pb0, pb1, -1);
     } else {
       // some value may not be finite and some query may not see it: column by
       // column, the keys it does not see zeroed, the same arithmetic otherwise
 #pragma unroll 1
       for (int c = 0; c < cols; ++c) {
-        uint32_t prm[4];
+        uint32_t own[4];
         const int hi = last_of(c0 + c), lo = first_of(hi);
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
-          const int key = base + t + 4 * h;
-          prm[h] = key <= hi && key >= lo ? cur.vp[h] : 0u;
+          const int key = base + vk[h];
+          own[h] = key <= hi && key >= lo ? prm[h] : 0u;
         }
-        pv(cur, prm, pb0, pb1, c);
+        pv(tw, own, pb0, pb1, c);
       }
     }
-    cur = nxt;
-    tile = next;
   }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncthreads();                                 // the rings' memory holds the merge from here on
 
   // ---- merge: warps (in warp order), then the cluster's CTAs (in rank order)
 #pragma unroll
@@ -433,7 +489,9 @@ __global__ void __launch_bounds__(512) attn_int4_kernel(AttnInt4Args a) {
 
 template <int HD>
 size_t a4_smem_bytes(int nw) {
-  return ((size_t)(nw + 1) * A4_COLS * HD + 2 * (size_t)(nw + 1) * A4_COLS) * sizeof(float);
+  const size_t ring = (size_t)nw * A4_STAGES * A4<HD>::WORDS * 4;
+  const size_t merge = ((size_t)(nw + 1) * A4_COLS * HD + 2 * (size_t)(nw + 1) * A4_COLS) * sizeof(float);
+  return std::max(ring, merge);
 }
 
 template <int HD>
