@@ -49,9 +49,9 @@ namespace tl {
 namespace {
 
 constexpr int A4_COLS = 8;          // queries per CTA (MMA N)
-constexpr int A4_TILE = 16;         // keys per warp tile (MMA M)
+constexpr int A4_TILE = 32;         // keys per warp tile: two sub-tiles of 16 (MMA M)
 constexpr int A4_MAX_CLUSTER = 16;
-constexpr int A4_STAGES = 4;         // tiles of a warp's ring
+constexpr int A4_STAGES = 2;         // tiles of a warp's ring
 constexpr float A4_SLACK = 8.f;     // the running maximum may lag by 2^8
 constexpr float A4_NONE = -1e30f;   // below every score: no key yet
 
@@ -140,7 +140,7 @@ __device__ __forceinline__ void a4_copy4(uint32_t* dst, const uint32_t* src) {
 }
 
 template <int HD>
-__global__ void __launch_bounds__(512) attn_int4_kernel(AttnInt4Args a) {
+__global__ void __launch_bounds__(256, 2) attn_int4_kernel(AttnInt4Args a) {
   using C = A4<HD>;
   pdl_enter();
   extern __shared__ __align__(128) float a4_smem[];
@@ -220,22 +220,34 @@ __global__ void __launch_bounds__(512) attn_int4_kernel(AttnInt4Args a) {
   // where the cache ends inside the tile its last row repeats
   auto fetch = [&](int ti, int slot_) {
     uint32_t* dst = ring + slot_ * C::WORDS;
-    const int base = ti * A4_TILE, last = a.max_ctx - 1;
+    const int base = ti * A4_TILE;
     constexpr int PR = C::RW / 4;                  // pieces per code row
-#pragma unroll
-    for (int i = 0; i < A4_TILE * PR / 32; ++i) {
-      const int p = lane + 32 * i, r = p / PR, c = p % PR;
-      const size_t src = (size_t)min(base + r, last) * C::RW + 4 * c;
-      a4_copy16(dst + 4 * p, kc + src);
-      a4_copy16(dst + C::V0 + r * C::RW + ((4 * c) ^ ((r & 4) ? C::VSWAP : 0)), vc + src);
-    }
+    constexpr int NP = A4_TILE * C::RP / 4;        // 16-byte pieces of K's parameters (and of V's)
     if (par16 && base + A4_TILE <= a.max_ctx) {
-      constexpr int NP = A4_TILE * C::RP / 4;      // 16-byte pieces of K's parameters (and of V's)
-      if (lane < 2 * NP) {
-        const int p = lane % NP;
-        a4_copy16(dst + (lane < NP ? C::KP0 : C::VP0) + 4 * p, (lane < NP ? kp : vp) + (size_t)base * C::RP + 4 * p);
+      const uint32_t* sk = kc + (size_t)base * C::RW + 4 * lane;
+      const uint32_t* sv = vc + (size_t)base * C::RW + 4 * lane;
+      // the row of piece lane + 32 i has the swap bit of row lane / PR (32 pieces are 8 or 16 rows)
+      uint32_t* dv = dst + C::V0 + ((4 * lane) ^ ((lane / PR) & 4 ? C::VSWAP : 0));
+#pragma unroll
+      for (int i = 0; i < A4_TILE * PR / 32; ++i) {
+        a4_copy16(dst + 4 * lane + 128 * i, sk + 128 * i);
+        a4_copy16(dv + 128 * i, sv + 128 * i);
       }
+#pragma unroll
+      for (int i = 0; i < (NP + 31) / 32; ++i)
+        if (lane < NP) {
+          a4_copy16(dst + C::KP0 + 4 * lane, kp + (size_t)base * C::RP + 4 * lane);
+          a4_copy16(dst + C::VP0 + 4 * lane, vp + (size_t)base * C::RP + 4 * lane);
+        }
     } else {
+      const int last = a.max_ctx - 1;
+#pragma unroll 1
+      for (int p = lane; p < A4_TILE * PR; p += 32) {
+        const int r = p / PR, c = p % PR;
+        const size_t src = (size_t)min(base + r, last) * C::RW + 4 * c;
+        a4_copy16(dst + 4 * p, kc + src);
+        a4_copy16(dst + C::V0 + r * C::RW + ((4 * c) ^ ((r & 4) ? C::VSWAP : 0)), vc + src);
+      }
 #pragma unroll 1
       for (int p = lane; p < A4_TILE * C::RP; p += 32) {
         const size_t src = (size_t)min(base + p / C::RP, last) * C::RP + p % C::RP;
@@ -245,12 +257,12 @@ __global__ void __launch_bounds__(512) attn_int4_kernel(AttnInt4Args a) {
     }
   };
 
-  // O^T += V^T P^T for one tile; only: -1, or the one column that takes it
-  auto pv = [&](const uint32_t* tw, const uint32_t* prm, uint32_t pb0, uint32_t pb1, int only) {
+  // O^T += V^T P^T for one sub-tile; only: -1, or the one column that takes it
+  auto pv = [&](const uint32_t* tw, int sub, const uint32_t* prm, uint32_t pb0, uint32_t pb1, int only) {
     uint32_t dv[4][C::VW];
 #pragma unroll
     for (int h = 0; h < 4; ++h)
-      a4_lds<C::VW>(dv[h], tw + C::V0 + vk[h] * C::RW + ((C::VW * g) ^ ((vk[h] & 4) ? C::VSWAP : 0)));
+      a4_lds<C::VW>(dv[h], tw + C::V0 + (16 * sub + vk[h]) * C::RW + ((C::VW * g) ^ ((vk[h] & 4) ? C::VSWAP : 0)));
     const __half2 s0 = kv_bits_h2(__byte_perm(prm[0], prm[1], 0x5410)), z0 = kv_bits_h2(__byte_perm(prm[0], prm[1], 0x7632));
     const __half2 s1 = kv_bits_h2(__byte_perm(prm[2], prm[3], 0x5410)), z1 = kv_bits_h2(__byte_perm(prm[2], prm[3], 0x7632));
 #pragma unroll
@@ -302,14 +314,17 @@ __global__ void __launch_bounds__(512) attn_int4_kernel(AttnInt4Args a) {
     request();
     const uint32_t* tw = ring + out_slot * C::WORDS;
     out_slot = out_slot + 1 == A4_STAGES ? 0 : out_slot + 1;
-    // S^T = K q^T: lane (g, t) gets keys kr and kr + 8, columns 2t and 2t + 1
-    float s[4] = {0.f, 0.f, 0.f, 0.f};
-    {
+    // S^T = K q^T: lane (g, t) gets keys kr and kr + 8 of each sub-tile, columns 2t and 2t + 1
+    float s[2][4];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      s[u][0] = s[u][1] = s[u][2] = s[u][3] = 0.f;
+      const int r0 = 16 * u + kr, r1 = r0 + 8;
       uint32_t k0[C::KW], k1[C::KW];
-      a4_lds<C::KW>(k0, tw + kr * C::RW + C::KW * t);
-      a4_lds<C::KW>(k1, tw + (kr + 8) * C::RW + C::KW * t);
-      const __half2 p0 = kv_bits_h2(tw[C::KP0 + kr * C::RP + (HD == 128 ? t : t >> 1)]);
-      const __half2 p1 = kv_bits_h2(tw[C::KP0 + (kr + 8) * C::RP + (HD == 128 ? t : t >> 1)]);
+      a4_lds<C::KW>(k0, tw + r0 * C::RW + C::KW * t);
+      a4_lds<C::KW>(k1, tw + r1 * C::RW + C::KW * t);
+      const __half2 p0 = kv_bits_h2(tw[C::KP0 + r0 * C::RP + (HD == 128 ? t : t >> 1)]);
+      const __half2 p1 = kv_bits_h2(tw[C::KP0 + r1 * C::RP + (HD == 128 ? t : t >> 1)]);
       const __half2 s0 = __low2half2(p0), z0 = __high2half2(p0), s1 = __low2half2(p1), z1 = __high2half2(p1);
 #pragma unroll
       for (int jj = 0; jj < C::KW; ++jj) {
@@ -321,7 +336,7 @@ __global__ void __launch_bounds__(512) attn_int4_kernel(AttnInt4Args a) {
           af[1] = kv_h2_bits(__hfma2(kv_int4_pair<true>(x1), s1, z1));
           af[2] = kv_h2_bits(__hfma2(kv_int4_pair<false>(x0), s0, z0));
           af[3] = kv_h2_bits(__hfma2(kv_int4_pair<false>(x1), s1, z1));
-          a4_mma(s, af, qb[2 * jj + h][0], qb[2 * jj + h][1]);
+          a4_mma(s[u], af, qb[2 * jj + h][0], qb[2 * jj + h][1]);
           if (h == 0) {
             x0 >>= 8;
             x1 >>= 8;
@@ -334,11 +349,16 @@ __global__ void __launch_bounds__(512) attn_int4_kernel(AttnInt4Args a) {
     if (edge) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int key = base + kr + 8 * (e >> 1), hi = last_of(c0 + min(2 * t + (e & 1), cols - 1));
-        if (key > hi || key < first_of(hi)) s[e] = -INFINITY;
+        const int hi = last_of(c0 + min(2 * t + (e & 1), cols - 1)), lo = first_of(hi);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int key = base + 16 * u + kr + 8 * (e >> 1);
+          if (key > hi || key < lo) s[u][e] = -INFINITY;
+        }
       }
     }
-    const float mx0 = fmaxf(s[0], s[2]), mx1 = fmaxf(s[1], s[3]);
+    const float mx0 = fmaxf(fmaxf(s[0][0], s[0][2]), fmaxf(s[1][0], s[1][2]));
+    const float mx1 = fmaxf(fmaxf(s[0][1], s[0][3]), fmaxf(s[1][1], s[1][3]));
     if (__any_sync(0xffffffffu, mx0 * csc > m[0] + A4_SLACK || mx1 * csc > m[1] + A4_SLACK)) {
       // raise the maxima that are due, each column by its own scores alone
       float mx[2] = {mx0, mx1}, al[2];
@@ -360,42 +380,50 @@ __global__ void __launch_bounds__(512) attn_int4_kernel(AttnInt4Args a) {
         o[i][3] *= al[1];
       }
     }
-    const float p0 = a4_ex2(fmaf(s[0], csc, -m[0])), p1 = a4_ex2(fmaf(s[1], csc, -m[1]));
-    const float p2 = a4_ex2(fmaf(s[2], csc, -m[0])), p3 = a4_ex2(fmaf(s[3], csc, -m[1]));
-    l[0] += p0 + p2;
-    l[1] += p1 + p3;
     // weights as fp16 (a rounding of 2^-11 each, of values the sum has in fp32),
     // key pairs of column g
-    const uint32_t pb0 = a4_transpose(a4_pack(p0, p1)), pb1 = a4_transpose(a4_pack(p2, p3));
-    uint32_t prm[4];
+    uint32_t pb[2][2];
 #pragma unroll
-    for (int h = 0; h < 4; ++h) prm[h] = tw[C::VP0 + vk[h] * C::RP + (HD == 128 ? g >> 1 : g >> 2)];
-    // keys that no query sees may hold anything: they count as zero
-    bool odd = false;
-    if (edge) {
-#pragma unroll
-      for (int h = 0; h < 4; ++h) {
-        const int key = base + vk[h];
-        if (key > hi_all || key < lo_all) prm[h] = 0u;
-        odd |= a4_odd(prm[h]);
-      }
-      odd = __any_sync(0xffffffffu, odd);
+    for (int u = 0; u < 2; ++u) {
+      const float p0 = a4_ex2(fmaf(s[u][0], csc, -m[0])), p1 = a4_ex2(fmaf(s[u][1], csc, -m[1]));
+      const float p2 = a4_ex2(fmaf(s[u][2], csc, -m[0])), p3 = a4_ex2(fmaf(s[u][3], csc, -m[1]));
+      l[0] += p0 + p2;
+      l[1] += p1 + p3;
+      pb[u][0] = a4_transpose(a4_pack(p0, p1));
+      pb[u][1] = a4_transpose(a4_pack(p2, p3));
     }
-    if (!odd) {
-      pv(tw, prm, pb0, pb1, -1);
-    } else {
-      // some value may not be finite and some query may not see it: column by
-      // column, the keys it does not see zeroed, the same arithmetic otherwise
-#pragma unroll 1
-      for (int c = 0; c < cols; ++c) {
-        uint32_t own[4];
-        const int hi = last_of(c0 + c), lo = first_of(hi);
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      uint32_t prm[4];
+#pragma unroll
+      for (int h = 0; h < 4; ++h) prm[h] = tw[C::VP0 + (16 * u + vk[h]) * C::RP + (HD == 128 ? g >> 1 : g >> 2)];
+      // keys that no query sees may hold anything: they count as zero
+      bool odd = false;
+      if (edge) {
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
-          const int key = base + vk[h];
-          own[h] = key <= hi && key >= lo ? prm[h] : 0u;
+          const int key = base + 16 * u + vk[h];
+          if (key > hi_all || key < lo_all) prm[h] = 0u;
+          odd |= a4_odd(prm[h]);
         }
-        pv(tw, own, pb0, pb1, c);
+        odd = __any_sync(0xffffffffu, odd);
+      }
+      if (!odd) {
+        pv(tw, u, prm, pb[u][0], pb[u][1], -1);
+      } else {
+        // some value may not be finite and some query may not see it: column by
+        // column, the keys it does not see zeroed, the same arithmetic otherwise
+#pragma unroll 1
+        for (int c = 0; c < cols; ++c) {
+          uint32_t own[4];
+          const int hi = last_of(c0 + c), lo = first_of(hi);
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            const int key = base + 16 * u + vk[h];
+            own[h] = key <= hi && key >= lo ? prm[h] : 0u;
+          }
+          pv(tw, u, own, pb[u][0], pb[u][1], c);
+        }
       }
     }
   }
@@ -499,7 +527,7 @@ tl_status launch_a4(const AttnInt4Args& a0, cudaStream_t s) {
   static std::atomic<uint64_t> attr_done{0};
   TL_TRY(once_per_device(attr_done, []() -> tl_status {
     TL_CUDA(cudaFuncSetAttribute(attn_int4_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)a4_smem_bytes<HD>(16)));
+                                 (int)a4_smem_bytes<HD>(8)));
     TL_CUDA(cudaFuncSetAttribute(attn_int4_kernel<HD>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
     return ok();
   }));
@@ -521,7 +549,7 @@ tl_status launch_a4(const AttnInt4Args& a0, cudaStream_t s) {
 // cache of max_ctx positions.
 void attn_int4_split(int max_ctx, int pairs, int* cls, int* nw) {
   const int tiles = (max_ctx + A4_TILE - 1) / A4_TILE;
-  *nw = tiles >= 2048 && pairs < 64 ? 16 : tiles >= 512 && pairs < 128 ? 8 : 4;
+  *nw = 4;
   int c = 1;
   while (c < A4_MAX_CLUSTER && c * *nw * 2 <= tiles && pairs * c * *nw < 148 * 16) c *= 2;
   *cls = c;

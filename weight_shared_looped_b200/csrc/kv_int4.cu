@@ -4,11 +4,11 @@
 // Both directions move a batch of packed rows (tokens) between fp16 rows
 // [n_rows][row_stride] (head h in columns [h * hd, (h + 1) * hd)) and the
 // lanes' caches [H][max_ctx][hd]: row r of lane b, the (r - cu[b])-th of its
-// rows, is position pos[b] + r - cu[b].  A thread owns 8 values: one 16-byte
-// vector of the fp16 row and one code word of the cache; the four threads of a
-// group share its extremes by two shuffles.  Consecutive threads take
-// consecutive positions of one head, so a CTA's code and parameter accesses
-// are contiguous and its fp16 accesses are whole head rows.
+// rows, is position pos[b] + r - cu[b].  A thread owns 8 values of a row: one
+// 16-byte vector of the fp16 row and one code word of the cache; the four threads
+// of a group share its extremes by two shuffles.  A CTA takes consecutive rows of
+// one head, so its code and parameter accesses are contiguous and its fp16
+// accesses are whole head rows.
 //
 // Bound by memory: written, 4 * H * hd bytes in and 1.25 * H * hd out per
 // token; read back, the reverse.
@@ -45,83 +45,129 @@ __device__ __forceinline__ int kv4_place(const Kv4RowsArgs& a, int r, int* lane)
   return p >= 0 && p < a.max_ctx && r >= first ? (int)p : -1;
 }
 
-template <int HD, bool WRITE>
+// U rows of K and of V per thread: their loads go out together, after one
+// look-up of the CTA's rows (a look-up per thread had cost three dependent loads
+// before each 16 bytes).
+template <int HD, bool WRITE, int U>
 __global__ void __launch_bounds__(KV4_THREADS) kv4_rows_kernel(Kv4RowsArgs a) {
   pdl_enter();
   constexpr int PARTS = HD / 8;                      // threads per row
-  constexpr int ROWS = KV4_THREADS / PARTS;          // rows per CTA
+  constexpr int ROWS = KV4_THREADS / PARTS;          // rows per pass of the CTA
+  constexpr int RP = HD / kInt4Group;
+  __shared__ int2 place[ROWS * U];
   const int part = threadIdx.x % PARTS, head = blockIdx.y;
-  const bool is_v = blockIdx.z != 0;
-  const int r = blockIdx.x * ROWS + threadIdx.x / PARTS;
-  int lane = 0;
-  const int p = r < a.n_rows ? kv4_place(a, r, &lane) : -1;
-  uint32_t* codes = (is_v ? a.v_codes : a.k_codes) + (size_t)lane * a.code_stride;
-  uint32_t* params = (is_v ? a.v_params : a.k_params) + (size_t)lane * a.param_stride;
-  const size_t slot = (size_t)head * a.max_ctx + (p < 0 ? 0 : p);
-  const size_t elem = (size_t)(r < a.n_rows ? r : 0) * a.row_stride + (size_t)head * HD + part * 8;
-  if (WRITE) {
-    uint4 w = make_uint4(0u, 0u, 0u, 0u);
-    if (p >= 0) w = *reinterpret_cast<const uint4*>((is_v ? a.v_in : a.k_in) + elem);
-    const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-    __half2 mn = kv_bits_h2(ws[0]), mx = mn;
-#pragma unroll
-    for (int i = 1; i < 4; ++i) {                    // NaN stays NaN
-      mn = __hmin2_nan(mn, kv_bits_h2(ws[i]));
-      mx = __hmax2_nan(mx, kv_bits_h2(ws[i]));
-    }
-    // the four threads of a group are neighbours
-#pragma unroll
-    for (int o = 1; o < 4; o <<= 1) {
-      mn = __hmin2_nan(mn, kv_bits_h2(__shfl_xor_sync(0xffffffffu, kv_h2_bits(mn), o)));
-      mx = __hmax2_nan(mx, kv_bits_h2(__shfl_xor_sync(0xffffffffu, kv_h2_bits(mx), o)));
-    }
-    if (p < 0) return;
-    const Int4Group g = kv_int4_group(__half2float(__hmin_nan(__low2half(mn), __high2half(mn))),
-                                      __half2float(__hmax_nan(__low2half(mx), __high2half(mx))));
-    uint32_t word = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = __half22float2(kv_bits_h2(ws[i]));
-      word |= kv_int4_code(f.x, g) << (8 * i);
-      word |= kv_int4_code(f.y, g) << (8 * i + 4);
-    }
-    codes[slot * PARTS + part] = word;
-    if (part % 4 == 0) params[slot * (HD / kInt4Group) + part / 4] = g.param;
-  } else {
-    if (p < 0) return;
-    const uint32_t word = codes[slot * PARTS + part];
-    const __half2 pr = kv_bits_h2(params[slot * (HD / kInt4Group) + part / 4]);
-    const __half2 s = __low2half2(pr), z = __high2half2(pr);
-    // pairs (i, i + 4) of the word, each value rounded once (fp16 fma)
-    const uint32_t v0 = kv_h2_bits(__hfma2(kv_int4_pair<true>(word), s, z));
-    const uint32_t v1 = kv_h2_bits(__hfma2(kv_int4_pair<false>(word), s, z));
-    const uint32_t v2 = kv_h2_bits(__hfma2(kv_int4_pair<true>(word >> 8), s, z));
-    const uint32_t v3 = kv_h2_bits(__hfma2(kv_int4_pair<false>(word >> 8), s, z));
-    uint4 o;
-    o.x = __byte_perm(v0, v1, 0x5410);
-    o.y = __byte_perm(v2, v3, 0x5410);
-    o.z = __byte_perm(v0, v1, 0x7632);
-    o.w = __byte_perm(v2, v3, 0x7632);
-    *reinterpret_cast<uint4*>((is_v ? a.v_out : a.k_out) + elem) = o;
+  const int r0 = blockIdx.x * ROWS * U;
+  for (int i = threadIdx.x; i < ROWS * U; i += KV4_THREADS) {
+    int lane = 0;
+    const int p = r0 + i < a.n_rows ? kv4_place(a, r0 + i, &lane) : -1;
+    place[i] = make_int2(lane, p);
   }
+  __syncthreads();
+  const int first = threadIdx.x / PARTS;
+  if (WRITE) {
+    uint4 w[2][U];
+    int2 at[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      at[u] = place[first + u * ROWS];
+      const size_t elem = (size_t)(r0 + first + u * ROWS) * a.row_stride + (size_t)head * HD + part * 8;
+#pragma unroll
+      for (int z = 0; z < 2; ++z)
+        w[z][u] = at[u].y >= 0 ? *reinterpret_cast<const uint4*>((z ? a.v_in : a.k_in) + elem)
+                               : make_uint4(0u, 0u, 0u, 0u);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+#pragma unroll
+      for (int z = 0; z < 2; ++z) {
+        const uint32_t ws[4] = {w[z][u].x, w[z][u].y, w[z][u].z, w[z][u].w};
+        __half2 mn = kv_bits_h2(ws[0]), mx = mn;
+#pragma unroll
+        for (int i = 1; i < 4; ++i) {                  // NaN stays NaN
+          mn = __hmin2_nan(mn, kv_bits_h2(ws[i]));
+          mx = __hmax2_nan(mx, kv_bits_h2(ws[i]));
+        }
+        // least in the low half, largest (negated) in the high: one reduction over
+        // the four neighbours that share the group
+        __half2 e = __halves2half2(__hmin_nan(__low2half(mn), __high2half(mn)),
+                                   __hneg(__hmax_nan(__low2half(mx), __high2half(mx))));
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1)
+          e = __hmin2_nan(e, kv_bits_h2(__shfl_xor_sync(0xffffffffu, kv_h2_bits(e), o)));
+        const Int4Group g = kv_int4_group(__low2float(e), -__high2float(e));
+        // the eight biased codes shifted and added; their biases add up to a constant
+        uint32_t word = 0, bias = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 f = __half22float2(kv_bits_h2(ws[i]));
+          word += kv_int4_biased(f.x, g) << (8 * i);
+          word += kv_int4_biased(f.y, g) << (8 * i + 4);
+          bias += (kInt4CodeBias << (8 * i)) + (kInt4CodeBias << (8 * i + 4));
+        }
+        word = kv_int4_marked(g) ? 0u : word - bias;
+        if (at[u].y >= 0) {
+          const size_t slot = (size_t)head * a.max_ctx + at[u].y;
+          ((z ? a.v_codes : a.k_codes) + (size_t)at[u].x * a.code_stride)[slot * PARTS + part] = word;
+          if (part % 4 == 0)
+            ((z ? a.v_params : a.k_params) + (size_t)at[u].x * a.param_stride)[slot * RP + part / 4] = g.param;
+        }
+      }
+    }
+  } else {
+    uint32_t word[2][U], pr[2][U];
+    int2 at[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      at[u] = place[first + u * ROWS];
+      const size_t slot = (size_t)head * a.max_ctx + (at[u].y < 0 ? 0 : at[u].y);
+#pragma unroll
+      for (int z = 0; z < 2; ++z) {
+        word[z][u] = ((z ? a.v_codes : a.k_codes) + (size_t)at[u].x * a.code_stride)[slot * PARTS + part];
+        pr[z][u] = ((z ? a.v_params : a.k_params) + (size_t)at[u].x * a.param_stride)[slot * RP + part / 4];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (at[u].y < 0) continue;
+      const size_t elem = (size_t)(r0 + first + u * ROWS) * a.row_stride + (size_t)head * HD + part * 8;
+#pragma unroll
+      for (int z = 0; z < 2; ++z) {
+        const uint32_t w = word[z][u];
+        const __half2 s = __low2half2(kv_bits_h2(pr[z][u])), zr = __high2half2(kv_bits_h2(pr[z][u]));
+        // pairs (i, i + 4) of the word, each value rounded once (fp16 fma)
+        const uint32_t v0 = kv_h2_bits(__hfma2(kv_int4_pair<true>(w), s, zr));
+        const uint32_t v1 = kv_h2_bits(__hfma2(kv_int4_pair<false>(w), s, zr));
+        const uint32_t v2 = kv_h2_bits(__hfma2(kv_int4_pair<true>(w >> 8), s, zr));
+        const uint32_t v3 = kv_h2_bits(__hfma2(kv_int4_pair<false>(w >> 8), s, zr));
+        uint4 o;
+        o.x = __byte_perm(v0, v1, 0x5410);
+        o.y = __byte_perm(v2, v3, 0x5410);
+        o.z = __byte_perm(v0, v1, 0x7632);
+        o.w = __byte_perm(v2, v3, 0x7632);
+        *reinterpret_cast<uint4*>((z ? a.v_out : a.k_out) + elem) = o;
+      }
+    }
+  }
+}
+
+template <int HD, bool WRITE>
+tl_status launch_kv4(const Kv4RowsArgs& a, cudaStream_t s) {
+  constexpr int rows = KV4_THREADS / (HD / 8);
+  // four rows a thread once that leaves at least two CTAs per SM
+  if ((long)a.n_rows * a.H >= (long)rows * 4 * 148 * 2)
+    TL_LAUNCH_PDL((kv4_rows_kernel<HD, WRITE, 4>), dim3((a.n_rows + 4 * rows - 1) / (4 * rows), a.H), KV4_THREADS, 0, s, a);
+  else
+    TL_LAUNCH_PDL((kv4_rows_kernel<HD, WRITE, 1>), dim3((a.n_rows + rows - 1) / rows, a.H), KV4_THREADS, 0, s, a);
+  return ok();
 }
 
 }  // namespace
 
 tl_status launch_kv4_rows(const Kv4RowsArgs& a, bool write, cudaStream_t s) {
   if (a.n_rows == 0) return ok();
-  const int rows = KV4_THREADS / (a.hd / 8);
-  const dim3 grid((a.n_rows + rows - 1) / rows, a.H, 2);
-  if (a.hd == 128) {
-    if (write) TL_LAUNCH_PDL((kv4_rows_kernel<128, true>), grid, KV4_THREADS, 0, s, a);
-    else TL_LAUNCH_PDL((kv4_rows_kernel<128, false>), grid, KV4_THREADS, 0, s, a);
-  } else if (a.hd == 64) {
-    if (write) TL_LAUNCH_PDL((kv4_rows_kernel<64, true>), grid, KV4_THREADS, 0, s, a);
-    else TL_LAUNCH_PDL((kv4_rows_kernel<64, false>), grid, KV4_THREADS, 0, s, a);
-  } else {
-    return set_error(TL_ERR_UNSUPPORTED, "head_dim %d not supported", a.hd);
-  }
-  return ok();
+  if (a.hd == 128) return write ? launch_kv4<128, true>(a, s) : launch_kv4<128, false>(a, s);
+  if (a.hd == 64) return write ? launch_kv4<64, true>(a, s) : launch_kv4<64, false>(a, s);
+  return set_error(TL_ERR_UNSUPPORTED, "head_dim %d not supported", a.hd);
 }
 
 }  // namespace tl

@@ -53,11 +53,19 @@ __device__ __forceinline__ Int4Group kv_int4_group(float lo, float hi) {
   return g;
 }
 
+// The code of x as the low bits of an integer: adding 1.5 * 2^23 rounds a value of
+// [0, 15] to the nearest integer, ties to even, in the low mantissa bits (no
+// conversion instruction, of which the GPU has few).  The difference is never
+// negative.  Codes of a group with NaN parameters are set to 0 by the caller
+// (kv_int4_marked).
+constexpr uint32_t kInt4CodeBias = 0x4B400000u;   // the bits of 1.5 * 2^23
+__device__ __forceinline__ uint32_t kv_int4_biased(float x, const Int4Group& g) {
+  return __float_as_uint(__fadd_rn(fminf(__fmul_rn(__fsub_rn(x, g.lo), g.inv), 15.f), 12582912.f));
+}
+__device__ __forceinline__ bool kv_int4_marked(const Int4Group& g) { return g.param == 0x7fff7fffu; }
+
 __device__ __forceinline__ uint32_t kv_int4_code(float x, const Int4Group& g) {
-  // inv == 0 also covers a group with NaN parameters, where x itself may be NaN
-  if (g.inv == 0.f) return 0u;
-  const float r = rintf(__fmul_rn(__fsub_rn(x, g.lo), g.inv));
-  return (uint32_t)fminf(fmaxf(r, 0.f), 15.f);
+  return kv_int4_marked(g) ? 0u : kv_int4_biased(x, g) - kInt4CodeBias;
 }
 
 __device__ __forceinline__ uint32_t kv_h2_bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
