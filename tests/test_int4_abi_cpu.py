@@ -29,9 +29,9 @@ def _rows(fn, cache=None, k=P16, v=P16, stride=256, cu=None, pos=P16, n=2):
     return fn(ctypes.byref(c), _p(k), _p(v), stride, _p(cu), _p(pos), n, None)
 
 
-def _attend(cache=None, q=P16, qs=512, n_q=1, heads=4, lens=P16, window=0, out=P16, os=512):
+def _attend(cache=None, q=P16, qs=512, n_q=1, heads=4, lens=P16, window=0, out=P16, os=512, ws=None, wb=0):
     c = _cache() if cache is None else cache
-    return tl.lib.tl_attention_int4(ctypes.byref(c), _p(q), qs, n_q, heads, _p(lens), window, _p(out), os, None)
+    return tl.lib.tl_attention_int4(ctypes.byref(c), _p(q), qs, n_q, heads, _p(lens), window, _p(out), os, _p(ws), wb, None)
 
 
 BAD_CACHES = [dict(n_lanes=-1), dict(n_lanes=65536), dict(n_heads=0), dict(n_heads=257), dict(max_ctx=0),
@@ -67,7 +67,25 @@ def test_row_calls_refuse(bad):
                                  dict(heads=1), dict(heads=0), dict(heads=1026), dict(window=-1)])
 def test_attention_refuses(bad):
     assert _attend(**bad) == BAD and tl.lib.tl_last_error()
-    assert tl.lib.tl_attention_int4(None, _p(P16), 512, 1, 4, _p(P16), 0, _p(P16), 512, None) == BAD
+    assert tl.lib.tl_attention_int4(None, _p(P16), 512, 1, 4, _p(P16), 0, _p(P16), 512, None, 0, None) == BAD
+
+
+def test_attention_workspace():
+    def need(n_q=1, heads=4, **kw):
+        b = ctypes.c_size_t(7)
+        c = _cache(code_stride=1 << 40, param_stride=1 << 40, **kw)
+        assert tl.lib.tl_attention_int4_workspace_bytes(ctypes.byref(c), n_q, heads, ctypes.byref(b)) == tl.TL_OK
+        return b.value
+    assert need(max_ctx=8191) == 0 and need(max_ctx=8192) > 0       # two lanes of two heads: the split is wide
+    assert need(max_ctx=1 << 20, n_q=0) == 0 and need(max_ctx=1 << 20, n_lanes=0) == 0
+    assert need(max_ctx=65536, n_lanes=512) == 0                     # enough lanes fill the GPU without it
+    big = need(max_ctx=1 << 20)
+    c = dict(max_ctx=1 << 20, code_stride=1 << 40, param_stride=1 << 40)
+    assert _attend(_cache(**c), ws=None, wb=1 << 30) == BAD
+    assert _attend(_cache(**c), ws=P16, wb=big - 1) == BAD
+    assert _attend(_cache(**c), ws=P16 + 8, wb=big) == BAD
+    assert tl.lib.tl_attention_int4_workspace_bytes(ctypes.byref(_cache()), 1, 4, None) == BAD
+    assert tl.lib.tl_attention_int4_workspace_bytes(ctypes.byref(_cache()), 9, 4, ctypes.byref(ctypes.c_size_t())) == BAD
 
 
 def test_empty_calls_do_nothing():

@@ -73,7 +73,8 @@ _SIGS = {
     "tl_kv_quant_int8": ([P, I, I, P, P, P], I),
     "tl_kv_write_int4": ([ctypes.POINTER(KvInt4Desc), P, P, LG, P, P, I, P], I),
     "tl_kv_read_int4": ([ctypes.POINTER(KvInt4Desc), P, P, LG, P, P, I, P], I),
-    "tl_attention_int4": ([ctypes.POINTER(KvInt4Desc), P, LG, I, I, P, I, P, LG, P], I),
+    "tl_attention_int4_workspace_bytes": ([ctypes.POINTER(KvInt4Desc), I, I, ctypes.POINTER(SZ)], I),
+    "tl_attention_int4": ([ctypes.POINTER(KvInt4Desc), P, LG, I, I, P, I, P, LG, P, SZ, P], I),
     "tl_score_head_workspace_bytes": ([I, I, I, I, ctypes.POINTER(SZ)], I),
     "tl_score_head": ([P, I, I, P, LG, I, P, P, P, I, P, P, P, SZ, P], I),
     "tl_attention_prefill": ([P, P, P, I, I, I, P, P], I),
@@ -321,10 +322,22 @@ def tl_kv_read_int4(k_codes, k_params, v_codes, v_params, pos, k, v, cu=None, st
                   v_params, pos, cu, stream)
 
 
+_INT4_SPLIT_CTX = 8192   # caches below this many positions need no workspace
+
+
+def tl_attention_int4_workspace_bytes(k_codes, k_params, v_codes, v_params, n_q: int,
+                                      q_heads: int) -> int:
+    b = SZ()
+    _check(lib.tl_attention_int4_workspace_bytes(
+        _kv_int4("tl_attention_int4", k_codes, k_params, v_codes, v_params), n_q, q_heads, b))
+    return b.value
+
+
 def tl_attention_int4(q, k_codes, k_params, v_codes, v_params, lens, out, n_q: int = 1,
-                      window: int = 0, stream=None) -> None:
+                      window: int = 0, workspace=None, stream=None) -> None:
     """q, out: fp16 [lanes * n_q, q_heads * hd]; lens int32 [lanes], the queries' own
-    positions included."""
+    positions included; workspace: uint8 of tl_attention_int4_workspace_bytes, allocated here
+    if it is needed and not given."""
     n = _TORCH or _torch_names()
     f16, i32 = n["f16"], n["i32"]
     what = "tl_attention_int4"
@@ -352,8 +365,21 @@ def tl_attention_int4(q, k_codes, k_params, v_codes, v_params, lens, out, n_q: i
         _fail(f"{what}: lens is not a contiguous [{d.n_lanes}]")
     if rows <= 1:
         qs = os_ = width
+    ws, ws_bytes = None, 0
+    if d.max_ctx >= _INT4_SPLIT_CTX and rows:
+        if workspace is None:
+            b = SZ()
+            _check(lib.tl_attention_int4_workspace_bytes(d, n_q, width // d.head_dim, b))
+            if b.value:
+                workspace = n["torch"].empty(b.value, dtype=n["u8"], device=q.device)
+                if stream is not None and not isinstance(stream, int):
+                    workspace.record_stream(stream)   # freed at return, used until the stream gets there
+        elif workspace.dtype is not n["u8"] or workspace.get_device() != dev or not workspace.is_contiguous():
+            _fail(f"{what}: workspace is not a contiguous uint8 tensor on {q.device}")
+        if workspace is not None:
+            ws, ws_bytes = workspace.data_ptr(), workspace.numel()
     _launch(n, dev, stream, lib.tl_attention_int4, d, q.data_ptr(), qs, n_q, width // d.head_dim,
-            lens.data_ptr(), window, out.data_ptr(), os_)
+            lens.data_ptr(), window, out.data_ptr(), os_, ws, ws_bytes)
 
 
 # --------------------------------------------------------------------- scoring head

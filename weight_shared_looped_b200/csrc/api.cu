@@ -82,6 +82,7 @@ struct tl_kv {
   char* h_kv = nullptr;
   float* h_part = nullptr;
   size_t h_layer_bytes = 0, h_region_bytes = 0;
+  float* int4_ws = nullptr;   // TL_KV_INT4, after the slots: the attention's split records
 };
 
 struct RowMap {
@@ -275,14 +276,40 @@ TL_API tl_status tl_kv_read_int4(const tl_kv_int4* cache, uint16_t* k, uint16_t*
   return kv4_rows(cache, k, v, row_stride, cu, pos, n_rows, false, (cudaStream_t)stream);
 }
 
-TL_API tl_status tl_attention_int4(const tl_kv_int4* cache, const uint16_t* q, long q_stride, int n_q, int q_heads,
-                                   const int32_t* lens, int window, uint16_t* out, long out_stride,
-                                   tl_stream stream) {
+namespace {
+
+tl_status check_attn4(const tl_kv_int4* cache, int n_q, int q_heads) {
   int width;
   TL_TRY(check_kv4(cache, &width));
   TL_CHECK_ARG(n_q >= 0 && n_q <= 8, "n_q = %d out of [0, 8]", n_q);
   TL_CHECK_ARG(q_heads >= cache->n_heads && q_heads <= 1024 && q_heads % cache->n_heads == 0,
                "q_heads = %d must be a multiple of n_heads = %d, at most 1024", q_heads, cache->n_heads);
+  return ok();
+}
+
+// the units the work split of a caller's attention is chosen for
+int attn4_pairs(const tl_kv_int4* c, int n_q, int q_heads) {
+  const long cols = (long)n_q * (q_heads / c->n_heads);
+  return (int)std::min<long>((long)c->n_lanes * c->n_heads * ((cols + 7) / 8), 1 << 20);
+}
+
+}  // namespace
+
+TL_API tl_status tl_attention_int4_workspace_bytes(const tl_kv_int4* cache, int n_q, int q_heads, size_t* bytes) {
+  TL_CHECK_ARG(bytes, "bytes is NULL");
+  TL_TRY(check_attn4(cache, n_q, q_heads));
+  *bytes = n_q == 0 || cache->n_lanes == 0
+               ? 0
+               : attn_int4_workspace(cache->n_lanes, cache->n_heads, cache->head_dim,
+                                     n_q * (q_heads / cache->n_heads), cache->max_ctx,
+                                     attn4_pairs(cache, n_q, q_heads));
+  return ok();
+}
+
+TL_API tl_status tl_attention_int4(const tl_kv_int4* cache, const uint16_t* q, long q_stride, int n_q, int q_heads,
+                                   const int32_t* lens, int window, uint16_t* out, long out_stride, void* workspace,
+                                   size_t workspace_bytes, tl_stream stream) {
+  TL_TRY(check_attn4(cache, n_q, q_heads));
   TL_CHECK_ARG(window >= 0, "window = %d must be >= 0 (0: the whole context)", window);
   const long qw = (long)q_heads * cache->head_dim;
   TL_CHECK_ARG(q_stride >= qw && q_stride % 8 == 0 && out_stride >= qw && out_stride % 8 == 0,
@@ -294,6 +321,14 @@ TL_API tl_status tl_attention_int4(const tl_kv_int4* cache, const uint16_t* q, l
   TL_CHECK_ARG(((uintptr_t)lens & 3) == 0, "lens must be 4-byte aligned");
   AttnInt4Args a;
   memset(&a, 0, sizeof(a));
+  a.split_pairs = attn4_pairs(cache, n_q, q_heads);
+  if (cache->max_ctx >= kInt4SplitCtx) {
+    size_t need;
+    TL_TRY(tl_attention_int4_workspace_bytes(cache, n_q, q_heads, &need));
+    TL_CHECK_ARG(need == 0 || (workspace && ((uintptr_t)workspace & 15) == 0 && workspace_bytes >= need),
+                 "workspace of %zu bytes (16-byte aligned) needed, %zu given", need, workspace ? workspace_bytes : 0);
+    a.ws = need ? (float*)workspace : nullptr;
+  }
   a.q = (const __half*)q;
   a.out = (__half*)out;
   a.q_stride = q_stride;
@@ -312,7 +347,6 @@ TL_API tl_status tl_attention_int4(const tl_kv_int4* cache, const uint16_t* q, l
   a.code_stride = cache->code_stride;
   a.param_stride = cache->param_stride;
   a.lens = lens;
-  a.split_pairs = (int)std::min<long>((long)cache->n_lanes * cache->n_heads, 1 << 20);
   return launch_attn_int4(a, (cudaStream_t)stream);
 }
 
@@ -728,6 +762,15 @@ size_t h_workspace_bytes(const tl_model* m, int n_lanes, int max_ctx, size_t* la
   return *part_off + align256(part * 2 * m->d * sizeof(float));
 }
 
+// 4-bit caches: the units the attention's split is chosen for.  A lane's split must
+// not depend on how many lanes run, so it is that of four lanes.
+int int4_split_pairs(const tl_model* m) { return 4 * m->H; }
+
+// The attention's workspace for up to 8 rows (decode) or 8 queries of a row (extend).
+size_t int4_workspace_bytes(const tl_model* m, int max_ctx) {
+  return align256(attn_int4_workspace(kMaxLanes, m->H, m->hd, 1, max_ctx, int4_split_pairs(m)));
+}
+
 bool known_kv_dtype(int dtype) {
   return dtype == TL_KV_FP16 || dtype == TL_KV_INT8 || dtype == TL_KV_H || dtype == TL_KV_INT4;
 }
@@ -773,6 +816,7 @@ TL_API tl_status tl_kv_bytes(const tl_model* model, int n_lanes, int max_ctx,
     size_t l16, r16, poff;
     *bytes += h_workspace_bytes(model, n_lanes, max_ctx, &l16, &r16, &poff);
   }
+  if (dtype == TL_KV_INT4) *bytes += int4_workspace_bytes(model, max_ctx);
   return ok();
 }
 
@@ -817,6 +861,8 @@ TL_API tl_status tl_kv_create(const tl_model* model, int n_lanes, int max_ctx,
     for (int b = 0; b < kMaxLanes; ++b) hh.cum_layers[b] = b;   // lane b: rebuilt layer b
     TL_CUDA(cudaMemcpy(kv->h_hdr, &hh, sizeof(hh), cudaMemcpyHostToDevice));
   }
+  if (dtype == TL_KV_INT4 && int4_workspace_bytes(model, max_ctx) > 0)
+    kv->int4_ws = (float*)((char*)buffer + need - int4_workspace_bytes(model, max_ctx));
   *out = kv.release();
   return ok();
 }
@@ -1155,8 +1201,8 @@ tl_status enqueue_int4_attention(tl_model* m, int layer, int rows, tl_kv* kv, co
     a.row_lane[i] = rm->lane[i];
     a.row_cum[i] = rm->cum[i];
   }
-  // a lane's split must not depend on how many lanes run
-  a.split_pairs = 4 * m->H;
+  a.split_pairs = int4_split_pairs(m);
+  a.ws = kv->int4_ws;
   return launch_attn_int4(a, s);
 }
 

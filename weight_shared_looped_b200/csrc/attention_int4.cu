@@ -50,7 +50,12 @@ namespace {
 
 constexpr int A4_COLS = 8;          // queries per CTA (MMA N)
 constexpr int A4_TILE = 32;         // keys per warp tile: two sub-tiles of 16 (MMA M)
-constexpr int A4_MAX_CLUSTER = 16;
+constexpr int A4_WARPS = 4;          // warps per CTA
+#ifndef A4_MINB
+#define A4_MINB 4
+#endif
+constexpr int A4_MAX_CLUSTER = 8;
+constexpr int A4_MAX_SPLIT = 64;
 constexpr int A4_STAGES = 2;         // tiles of a warp's ring
 constexpr float A4_SLACK = 8.f;     // the running maximum may lag by 2^8
 constexpr float A4_NONE = -1e30f;   // below every score: no key yet
@@ -140,11 +145,12 @@ __device__ __forceinline__ void a4_copy4(uint32_t* dst, const uint32_t* src) {
 }
 
 template <int HD>
-__global__ void __launch_bounds__(256, 2) attn_int4_kernel(AttnInt4Args a) {
+__global__ void __launch_bounds__(32 * A4_WARPS, A4_MINB) attn_int4_kernel(AttnInt4Args a) {
   using C = A4<HD>;
   pdl_enter();
   extern __shared__ __align__(128) float a4_smem[];
-  const int nw = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int nw = A4_WARPS;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const int cls = gridDim.x, rank = blockIdx.x;
   const int ctiles = a.col_tiles, head = blockIdx.y / ctiles, c0 = (blockIdx.y % ctiles) * A4_COLS;
@@ -470,6 +476,14 @@ __global__ void __launch_bounds__(256, 2) attn_int4_kernel(AttnInt4Args a) {
       const int cc = c0 + c, qi = cc / a.group, hq = head * a.group + cc % a.group;
       a.out[(size_t)(row * a.n_q + qi) * a.out_stride + (size_t)hq * HD + i % HD] =
           __float2half_rn(L == 0.f ? 0.f : acc / L);
+    } else if (a.ws != nullptr) {
+      // a split beyond a cluster: the record goes to the merge kernel
+      float* rec = a.ws + (((size_t)row * gridDim.y + blockIdx.y) * cls + rank) * (A4_COLS * (HD + 2));
+      rec[i] = acc;
+      if (i % HD == 0) {
+        rec[A4_COLS * HD + c] = M;
+        rec[A4_COLS * HD + A4_COLS + c] = L;
+      }
     } else {
       go[i] = acc;
       if (i % HD == 0) {
@@ -478,7 +492,7 @@ __global__ void __launch_bounds__(256, 2) attn_int4_kernel(AttnInt4Args a) {
       }
     }
   }
-  if (cls == 1) return;
+  if (cls == 1 || a.ws != nullptr) return;
   a4_cluster_sync();
   // rank r finishes elements r * share .. of the record
   const int share = (cols * HD + cls - 1) / cls;
@@ -515,11 +529,69 @@ __global__ void __launch_bounds__(256, 2) attn_int4_kernel(AttnInt4Args a) {
   a4_cluster_sync();   // no CTA leaves while another reads its shared memory
 }
 
+// Joins the records of a split in their order: a CTA per (row, head, column tile),
+// a thread per output element and column.
 template <int HD>
-size_t a4_smem_bytes(int nw) {
-  const size_t ring = (size_t)nw * A4_STAGES * A4<HD>::WORDS * 4;
-  const size_t merge = ((size_t)(nw + 1) * A4_COLS * HD + 2 * (size_t)(nw + 1) * A4_COLS) * sizeof(float);
+__global__ void __launch_bounds__(256) attn_int4_merge_kernel(AttnInt4Args a, int splits) {
+  pdl_enter();
+  const int ctiles = a.col_tiles, head = blockIdx.x / ctiles, c0 = (blockIdx.x % ctiles) * A4_COLS, row = blockIdx.y;
+  const int cols = min(A4_COLS, a.n_q * a.group - c0);
+  constexpr int REC = A4_COLS * (HD + 2);
+  const float* rec = a.ws + ((size_t)row * gridDim.x + blockIdx.x) * splits * REC;
+  __shared__ float w[A4_MAX_SPLIT][A4_COLS];
+  __shared__ float sum[A4_COLS];
+  if (threadIdx.x < 32 * cols) {                     // warp c: column c's weights and their sum
+    const int c = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    float m[2], l[2], M = A4_NONE, L = 0.f;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int s = lane + 32 * u;
+      m[u] = s < splits ? rec[(size_t)s * REC + A4_COLS * HD + c] : A4_NONE;
+      l[u] = s < splits ? rec[(size_t)s * REC + A4_COLS * HD + A4_COLS + c] : 0.f;
+      M = fmaxf(M, m[u]);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const float f = exp2f(m[u] - M);
+      if (lane + 32 * u < splits) w[lane + 32 * u][c] = f;
+      L = fmaf(l[u], f, L);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+    if (lane == 0) sum[c] = L;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < cols * HD; i += 256) {
+    const int c = i / HD;
+    float acc = 0.f;
+#pragma unroll 8
+    for (int s = 0; s < splits; ++s) acc = fmaf(rec[(size_t)s * REC + i], w[s][c], acc);
+    const float L = sum[c];
+    const int cc = c0 + c, qi = cc / a.group, hq = head * a.group + cc % a.group;
+    a.out[(size_t)(row * a.n_q + qi) * a.out_stride + (size_t)hq * HD + i % HD] =
+        __float2half_rn(L == 0.f ? 0.f : acc / L);
+  }
+}
+
+template <int HD>
+size_t a4_smem_bytes() {
+  const size_t ring = (size_t)A4_WARPS * A4_STAGES * A4<HD>::WORDS * 4;
+  const size_t merge =
+      ((size_t)(A4_WARPS + 1) * A4_COLS * HD + 2 * (size_t)(A4_WARPS + 1) * A4_COLS) * sizeof(float);
   return std::max(ring, merge);
+}
+
+// CTAs per (row, cache head, column tile) for `pairs` of those over a cache of
+// max_ctx positions, and whether they merge in a cluster or through the workspace.
+int a4_split(int max_ctx, int pairs, bool* through_ws) {
+  const int tiles = (max_ctx + A4_TILE - 1) / A4_TILE;
+  // as many CTAs as fill the GPU once (four per SM), a tile per warp at least
+  int c = std::min((tiles + A4_WARPS - 1) / A4_WARPS, std::max(1, 148 * 4 / pairs));
+  *through_ws = max_ctx >= kInt4SplitCtx && c > A4_MAX_CLUSTER;
+  if (*through_ws) return std::min(c, A4_MAX_SPLIT);
+  return std::min(c, A4_MAX_CLUSTER);
 }
 
 template <int HD>
@@ -527,32 +599,32 @@ tl_status launch_a4(const AttnInt4Args& a0, cudaStream_t s) {
   static std::atomic<uint64_t> attr_done{0};
   TL_TRY(once_per_device(attr_done, []() -> tl_status {
     TL_CUDA(cudaFuncSetAttribute(attn_int4_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)a4_smem_bytes<HD>(8)));
-    TL_CUDA(cudaFuncSetAttribute(attn_int4_kernel<HD>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
+                                 (int)a4_smem_bytes<HD>()));
     return ok();
   }));
   AttnInt4Args a = a0;
   a.col_tiles = (a.n_q * a.group + A4_COLS - 1) / A4_COLS;
-  int cls, nw;
-  attn_int4_split(a.max_ctx, a.split_pairs * a.col_tiles, &cls, &nw);
-  const dim3 grid(cls, a.H * a.col_tiles, a.n_rows);
-  const cudaError_t e = launch_pdl_cluster(attn_int4_kernel<HD>, grid, dim3(32 * nw), a4_smem_bytes<HD>(nw), s,
-                                           (unsigned)cls, a);
+  bool through_ws;
+  const int c = a4_split(a.max_ctx, a.split_pairs, &through_ws);
+  if (!through_ws) a.ws = nullptr;
+  else if (!a.ws) return set_error(TL_ERR_INVALID_ARG, "4-bit attention: a context of %d needs a workspace", a.max_ctx);
+  const dim3 grid(c, a.H * a.col_tiles, a.n_rows);
+  const cudaError_t e = launch_pdl_cluster(attn_int4_kernel<HD>, grid, dim3(32 * A4_WARPS), a4_smem_bytes<HD>(), s,
+                                           through_ws ? 1u : (unsigned)c, a);
   if (e != cudaSuccess)
     return set_error(TL_ERR_CUDA, "launch of attn_int4_kernel failed: %s", cudaGetErrorString(e));
+  if (through_ws) TL_LAUNCH_PDL(attn_int4_merge_kernel<HD>, dim3(a.H * a.col_tiles, a.n_rows), 256, 0, s, a, c);
   return ok();
 }
 
 }  // namespace
 
-// CTAs of the cluster and warps of a CTA for `pairs` (lane, head) pairs over a
-// cache of max_ctx positions.
-void attn_int4_split(int max_ctx, int pairs, int* cls, int* nw) {
-  const int tiles = (max_ctx + A4_TILE - 1) / A4_TILE;
-  *nw = 4;
-  int c = 1;
-  while (c < A4_MAX_CLUSTER && c * *nw * 2 <= tiles && pairs * c * *nw < 148 * 16) c *= 2;
-  *cls = c;
+// Workspace of a call: n_rows rows of n_q * group queries per cache head.
+size_t attn_int4_workspace(int n_rows, int H, int hd, int cols, int max_ctx, int split_pairs) {
+  bool through_ws;
+  const int c = a4_split(max_ctx, split_pairs, &through_ws);
+  if (!through_ws) return 0;
+  return (size_t)n_rows * H * ((cols + A4_COLS - 1) / A4_COLS) * c * A4_COLS * (hd + 2) * sizeof(float);
 }
 
 tl_status launch_attn_int4(const AttnInt4Args& a, cudaStream_t s) {
