@@ -529,23 +529,30 @@ __global__ void __launch_bounds__(32 * A4_WARPS, A4_MINB) attn_int4_kernel(AttnI
   a4_cluster_sync();   // no CTA leaves while another reads its shared memory
 }
 
-// Joins the records of a split in their order: a CTA per (row, head, column tile),
-// a thread per output element and column.
+// Joins the records of a split in their order: a CTA per query and head, two
+// threads per output element, each with half of the records, all of them
+// requested at once.
 template <int HD>
-__global__ void __launch_bounds__(256) attn_int4_merge_kernel(AttnInt4Args a, int splits) {
+__global__ void __launch_bounds__(2 * HD) attn_int4_merge_kernel(AttnInt4Args a, int splits) {
   pdl_enter();
-  const int ctiles = a.col_tiles, head = blockIdx.x / ctiles, c0 = (blockIdx.x % ctiles) * A4_COLS, row = blockIdx.y;
-  const int cols = min(A4_COLS, a.n_q * a.group - c0);
-  constexpr int REC = A4_COLS * (HD + 2);
-  const float* rec = a.ws + ((size_t)row * gridDim.x + blockIdx.x) * splits * REC;
-  __shared__ float w[A4_MAX_SPLIT][A4_COLS];
-  __shared__ float sum[A4_COLS];
-  if (threadIdx.x < 32 * cols) {                     // warp c: column c's weights and their sum
-    const int c = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int cols_all = a.n_q * a.group;
+  const int head = blockIdx.x / cols_all, cc = blockIdx.x % cols_all, row = blockIdx.y;
+  const int c = cc % A4_COLS;
+  constexpr int REC = A4_COLS * (HD + 2), HALF = A4_MAX_SPLIT / 2;
+  const float* rec =
+      a.ws + (((size_t)row * a.H + head) * a.col_tiles + cc / A4_COLS) * splits * REC;
+  __shared__ float w[A4_MAX_SPLIT];
+  __shared__ float sum, part[HD];
+  const int d = threadIdx.x % HD, h = threadIdx.x / HD;
+  float v[HALF];
+#pragma unroll
+  for (int s = 0; s < HALF; ++s)
+    v[s] = 2 * s + h < splits ? rec[(size_t)(2 * s + h) * REC + c * HD + d] : 0.f;
+  if (threadIdx.x < 32) {
     float m[2], l[2], M = A4_NONE, L = 0.f;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const int s = lane + 32 * u;
+      const int s = threadIdx.x + 32 * u;
       m[u] = s < splits ? rec[(size_t)s * REC + A4_COLS * HD + c] : A4_NONE;
       l[u] = s < splits ? rec[(size_t)s * REC + A4_COLS * HD + A4_COLS + c] : 0.f;
       M = fmaxf(M, m[u]);
@@ -555,23 +562,24 @@ __global__ void __launch_bounds__(256) attn_int4_merge_kernel(AttnInt4Args a, in
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const float f = exp2f(m[u] - M);
-      if (lane + 32 * u < splits) w[lane + 32 * u][c] = f;
+      w[threadIdx.x + 32 * u] = f;
       L = fmaf(l[u], f, L);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-    if (lane == 0) sum[c] = L;
+    if (threadIdx.x == 0) sum = L;
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < cols * HD; i += 256) {
-    const int c = i / HD;
-    float acc = 0.f;
-#pragma unroll 8
-    for (int s = 0; s < splits; ++s) acc = fmaf(rec[(size_t)s * REC + i], w[s][c], acc);
-    const float L = sum[c];
-    const int cc = c0 + c, qi = cc / a.group, hq = head * a.group + cc % a.group;
-    a.out[(size_t)(row * a.n_q + qi) * a.out_stride + (size_t)hq * HD + i % HD] =
-        __float2half_rn(L == 0.f ? 0.f : acc / L);
+  float acc = 0.f;
+#pragma unroll
+  for (int s = 0; s < HALF; ++s)
+    if (2 * s + h < splits) acc = fmaf(v[s], w[2 * s + h], acc);
+  if (h == 1) part[d] = acc;
+  __syncthreads();
+  if (h == 0) {
+    const float L = sum;
+    a.out[(size_t)(row * a.n_q + cc / a.group) * a.out_stride + (size_t)(head * a.group + cc % a.group) * HD + d] =
+        __float2half_rn(L == 0.f ? 0.f : (acc + part[d]) / L);
   }
 }
 
@@ -613,7 +621,8 @@ tl_status launch_a4(const AttnInt4Args& a0, cudaStream_t s) {
                                            through_ws ? 1u : (unsigned)c, a);
   if (e != cudaSuccess)
     return set_error(TL_ERR_CUDA, "launch of attn_int4_kernel failed: %s", cudaGetErrorString(e));
-  if (through_ws) TL_LAUNCH_PDL(attn_int4_merge_kernel<HD>, dim3(a.H * a.col_tiles, a.n_rows), 256, 0, s, a, c);
+  if (through_ws)
+    TL_LAUNCH_PDL(attn_int4_merge_kernel<HD>, dim3(a.H * a.n_q * a.group, a.n_rows), 2 * HD, 0, s, a, c);
   return ok();
 }
 
