@@ -595,7 +595,10 @@ size_t a4_smem_bytes() {
 // max_ctx positions, and whether they merge in a cluster or through the workspace.
 int a4_split(int max_ctx, int pairs, bool* through_ws) {
   const int tiles = (max_ctx + A4_TILE - 1) / A4_TILE;
-  // as many CTAs as fill the GPU once (four per SM), a tile per warp at least
+  // as many CTAs as fill the GPU once (four per SM), a tile per warp at least.  More
+  // than a cluster's eight cost a second launch: 16 heads at 2112 positions 10.3 us
+  // in a cluster and 8.2 through the workspace, 32 heads 10.3 and 10.3; at 4096
+  // positions 12.3 and 10.3, 12.3 and 13.3; at 16384 the cluster takes 26 against 18
   int c = std::min((tiles + A4_WARPS - 1) / A4_WARPS, std::max(1, 148 * 4 / pairs));
   *through_ws = max_ctx >= kInt4SplitCtx && c > A4_MAX_CLUSTER;
   if (*through_ws) return std::min(c, A4_MAX_SPLIT);

@@ -178,6 +178,7 @@ struct ScoreTc {
   int mt, groups;         // row tiles; CTAs that share one row tile's vocabulary tiles
   int stages;
   uint32_t stage_bytes;
+  int kbs;                // vocabulary-major: k blocks per stage
   int slices;             // records per row
   const float* scale;
   ScoreRec rec;
@@ -472,37 +473,53 @@ __global__ void __launch_bounds__(SV_THREADS, 1)
   const uint32_t tmem = bars.tmem;
   const uint32_t ybytes = (uint32_t)(2 * tp) * 128, ebytes = (uint32_t)a.bn * 128;
 
+  // A stage holds up to kbs k blocks: their embedding rows (16 KB each), then their
+  // activations.
+  const uint32_t ybase = (uint32_t)a.kbs * 16384, ystep = (ybytes + 1023) & ~1023u;
+  const int spt = (a.nkb + a.kbs - 1) / a.kbs;       // stages per tile
   if (warp == 8) {
     if (lane == 0) {
+      const int total = (a.vt - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x * spt;
+      const int v_step = (int)gridDim.x * a.bn;
+      auto copy_e = [&](int s, int k0, int v0) {     // expect the stage, request its embedding rows
+        uint8_t* sp = smem + (size_t)s * a.stage_bytes;
+        const bool two = a.kbs == 2 && k0 + 1 < a.nkb;
+        sc_expect(&bars.full[s], two ? 2 * (ybytes + ebytes) : ybytes + ebytes);
+        sc_copy(&bars.full[s], sp, &map_e, k0 * SC_BK, v0);
+        if (two) sc_copy(&bars.full[s], sp + 16384, &map_e, (k0 + 1) * SC_BK, v0);
+      };
       // the embedding of the first stages is requested before the wait for pass 0:
       // pass 0 has itself waited for everything before it
-      const int total = (a.vt - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x * a.nkb;
       const int ahead = min(a.stages, total);
+      int k0 = 0, v0 = (int)blockIdx.x * a.bn;
       for (int i = 0; i < ahead; ++i) {
-        sc_expect(&bars.full[i], ybytes + ebytes);
-        sc_copy(&bars.full[i], smem + (size_t)i * a.stage_bytes, &map_e, i % a.nkb * SC_BK,
-                ((int)blockIdx.x + i / a.nkb * (int)gridDim.x) * a.bn);
+        copy_e(i, k0, v0);
+        if ((k0 += a.kbs) >= a.nkb) {
+          k0 = 0;
+          v0 += v_step;
+        }
       }
       pdl_enter();
-      int s = 0, ph = 1, kb = 0, v0 = (int)blockIdx.x * a.bn, issued = 0;
+      int s = 0, ph = 1, issued = 0, ky = 0;
       for (; issued < total; ++issued) {
-        uint8_t* sp = smem + (size_t)s * a.stage_bytes;
         if (issued >= a.stages) {
           if (!sc_wait(&bars.empty[s], ph, &bars.abort)) {
             atomicExch(&bars.abort, 1);
             break;
           }
-          sc_expect(&bars.full[s], ybytes + ebytes);
-          sc_copy(&bars.full[s], sp, &map_e, kb * SC_BK, v0);
+          copy_e(s, k0, v0);
+          if ((k0 += a.kbs) >= a.nkb) {
+            k0 = 0;
+            v0 += v_step;
+          }
         }
-        sc_copy(&bars.full[s], sp + 16384, &map_y, kb * SC_BK, 0);
+        uint8_t* sp = smem + (size_t)s * a.stage_bytes + ybase;
+        sc_copy(&bars.full[s], sp, &map_y, ky * SC_BK, 0);
+        if (a.kbs == 2 && ky + 1 < a.nkb) sc_copy(&bars.full[s], sp + ystep, &map_y, (ky + 1) * SC_BK, 0);
+        if ((ky += a.kbs) >= a.nkb) ky = 0;
         if (++s == a.stages) {
           s = 0;
           ph ^= 1;
-        }
-        if (++kb == a.nkb) {
-          kb = 0;
-          v0 += (int)gridDim.x * a.bn;
         }
       }
       if (*(volatile int*)&bars.abort)
@@ -520,13 +537,18 @@ __global__ void __launch_bounds__(SV_THREADS, 1)
         const int buf = j & 1, use = j >> 1;
         if (use > 0) ok = sc_wait(&bars.acc_empty[buf], (use & 1) ^ 1, &bars.abort);
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        for (int kb = 0; kb < a.nkb && ok; ++kb) {
+        for (int k0 = 0; k0 < a.nkb && ok; k0 += a.kbs) {
           ok = sc_wait(&bars.full[s], ph, &bars.abort);
           if (!ok) break;
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-          const uint64_t e = desc0 + (uint64_t)(s * (a.stage_bytes >> 4)), yy = e + (16384 >> 4);
+          const uint64_t e0 = desc0 + (uint64_t)(s * (a.stage_bytes >> 4)), y0 = e0 + (ybase >> 4);
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks) sc_mma(tmem + buf * 128, e + 2 * ks, yy + 2 * ks, idesc, (kb | ks) != 0);
+          for (int ks = 0; ks < 4; ++ks) sc_mma(tmem + buf * 128, e0 + 2 * ks, y0 + 2 * ks, idesc, (k0 | ks) != 0);
+          if (a.kbs == 2 && k0 + 1 < a.nkb) {
+            const uint64_t e1 = e0 + (16384 >> 4), y1 = y0 + (ystep >> 4);
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks) sc_mma(tmem + buf * 128, e1 + 2 * ks, y1 + 2 * ks, idesc, true);
+          }
           sc_commit(&bars.empty[s]);
           if (++s == a.stages) {
             s = 0;
@@ -680,7 +702,8 @@ struct ScoreCand {
 // more than kc, whatever the number of lists.  They are ranked by counting; the
 // chosen and the given token are scored in fp64, two tokens a warp.  With one CTA
 // on the SM every step is a round trip: loads that do not depend on one another
-// are issued together.
+// are issued together.  (128 threads, twice the CTAs per SM, took 25 us longer over
+// 1024 rows.)
 __global__ void __launch_bounds__(SM_THREADS, 3) score_merge_kernel(ScoreArgs a, int kc, ScoreTc tc) {
   pdl_enter();
   extern __shared__ double sm_dyn[];
@@ -915,7 +938,10 @@ ScorePlan score_plan(int n, int V, int d, int k) {
     t.vt = (V + t.bn - 1) / t.bn;
     p.grid = std::min(kScoreSms, t.vt);
     t.slices = p.grid;
-    t.stage_bytes = 16384 + (uint32_t)(2 * t.pad * 128 + 1023) / 1024 * 1024;
+    // two k blocks per stage while four stages of them fit: a stage costs its copying
+    // thread about 0.25 us however small, as long as a k block's rows take from HBM
+    t.kbs = t.pad <= 32 ? 2 : 1;
+    t.stage_bytes = (uint32_t)t.kbs * (16384 + (uint32_t)(2 * t.pad * 128 + 1023) / 1024 * 1024);
     const size_t zb = (size_t)t.pad * 132 * 4;
     t.stages = (int)std::min<size_t>(12, (kVocabSmem - zb - 1024) / t.stage_bytes);
     p.smem = 1024 + (size_t)t.stages * t.stage_bytes + zb;
@@ -980,8 +1006,8 @@ size_t score_workspace(int n, int V, int d, int k) {
 tl_status launch_score_head(const ScoreArgs& a0, cudaStream_t s) {
   static std::atomic<uint64_t> attr_done{0};
   TL_TRY(once_per_device(attr_done, []() -> tl_status {
-    TL_CUDA(cudaFuncSetAttribute(score_merge_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)score_merge_smem(kMaxSlices, kMaxCand, 8192)));
+    const int most = (int)score_merge_smem(kMaxSlices, kMaxCand, 8192);
+    TL_CUDA(cudaFuncSetAttribute(score_merge_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most));
     return ok();
   }));
   for (int r0 = 0; r0 < a0.n; r0 += kScoreChunk) {
