@@ -85,6 +85,41 @@ def test_length_above_the_cache_counts_as_the_cache():
     assert (_run(q, cache, [-5], 1, 0) == 0).all()
 
 
+@pytest.mark.parametrize("window", [100, 101, 2 ** 31 - 1])
+def test_windows_beyond_the_context_are_no_windows(window):
+    """Also where some of the queries see nothing."""
+    cache = Cache(*_kv(2, 2, 100, 64, 23))
+    q = _q(10, 2, 64, 24)
+    lens = [100, 3]
+    got = _run(q, cache, lens, 5, window)
+    assert np.array_equal(got, _run(q, cache, lens, 5, 0))
+    _check(got, q, cache, lens, 5, 0)
+
+
+@pytest.mark.parametrize("lanes,H,group,hd,ctx,n_q,window", [
+    (1, 2, 1, 128, 4095, 1, 0), (1, 2, 1, 128, 4096, 1, 0), (1, 1, 8, 64, 4097, 3, 0), (2, 3, 2, 128, 5000, 5, 700),
+    (1, 1, 1, 64, 40001, 1, 0),
+])
+def test_long_contexts_go_through_a_workspace(lanes, H, group, hd, ctx, n_q, window):
+    """From 4096 positions a split may be wider than a cluster; lengths from none to
+    all of the cache, a workspace given and one allocated by the binding."""
+    k, v = _kv(1, H, ctx, hd, 25)
+    cache = Cache(np.repeat(k, lanes, 0), np.repeat(v, lanes, 0))
+    q = _q(lanes * n_q, H * group, hd, 26, 2.0)
+    need = tl.tl_attention_int4_workspace_bytes(*cache.t, n_q, H * group)
+    assert (need > 0) == (ctx >= 4096)
+    for lens in ([ctx] * lanes, [ctx - 1, 4000][:lanes], [1, 0][:lanes], [33, 5][:lanes]):
+        got = _run(q, cache, lens, n_q, window)
+        _check(got, q, cache, lens, n_q, window)
+        ws = torch.full((max(need, 1) + 64,), 0xFF, dtype=torch.uint8, device="cuda")
+        out = torch.zeros(q.shape[0], H * group * hd, dtype=torch.float16, device="cuda")
+        tl.tl_attention_int4(torch.from_numpy(q.reshape(q.shape[0], -1)).cuda(), *cache.t,
+                             torch.tensor(lens, dtype=torch.int32, device="cuda"), out, n_q=n_q, window=window,
+                             workspace=ws[:max(need, 1)])
+        assert np.array_equal(out.cpu().numpy().reshape(got.shape), got)
+        assert (ws[max(need, 1):] == 0xFF).all()
+
+
 @pytest.mark.parametrize("hd", [64, 128])
 def test_equal_keys_give_the_mean(hd):
     """Constant groups have scale 0: the value is the zero point, and equal keys

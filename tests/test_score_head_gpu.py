@@ -122,6 +122,33 @@ def test_one_large_channel():
     _check(E, y, t, 4)
 
 
+def test_more_rows_than_one_sweep():
+    """5000 rows run in two sweeps over the embedding (4736 rows and the rest)."""
+    n, V, d, k = 5000, 700, 128, 3
+    E, y, t = _inputs(n, V, d, 65)
+    _check(E, y, t, k)
+    got = _run(E, y, t, k)
+    for r0, r1 in ((0, 1), (4735, 4737), (4999, 5000)):
+        part = _run(E, y[r0:r1], t[r0:r1], k)
+        assert np.array_equal(got[2][r0:r1], part[2])
+        assert np.abs(got[0][r0:r1] - part[0]).max() <= 1e-5
+
+
+def test_a_token_with_nearly_all_probability():
+    """Peaked rows keep their small log probabilities.  The best tokens' terms of the
+    sum come from fp64 logits, so of the bound eps of the streaming pass's logits
+    only the part that falls on the other tokens remains, (1 - p) eps with p the
+    best token's probability, beside the rounding of exponentials and sums
+    (2^-20, as above)."""
+    for n in (6, 40, 130):
+        E, y, t = _inputs(n, 4000, 2048, 66, lean=60.0)
+        lp = _run(E, y, t, 2)[0]
+        rlp, _, _, rtop, eps, _ = _reference(E, y, t, 2)
+        tol = (1 - np.exp(rtop[:, 0])) * eps + 2.0 ** -20 + 2.0 ** -24 * np.abs(rlp)
+        assert (np.abs(lp - rlp) <= tol).all(), (n, (np.abs(lp - rlp) - tol).max())
+        assert rlp[-1] > -1e-6 and eps[-1] > 1e-4
+
+
 def test_targets_outside_and_missing_outputs():
     E, y, t = _inputs(12, 400, 128, 70)
     t = t.copy()

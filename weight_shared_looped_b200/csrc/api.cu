@@ -339,7 +339,7 @@ TL_API tl_status tl_attention_int4(const tl_kv_int4* cache, const uint16_t* q, l
   a.group = q_heads / cache->n_heads;
   a.hd = cache->head_dim;
   a.max_ctx = cache->max_ctx;
-  a.window = window;
+  a.window = window > cache->max_ctx ? 0 : window;   // at least the whole context
   a.k_codes = cache->k_codes;
   a.v_codes = cache->v_codes;
   a.k_params = cache->k_params;

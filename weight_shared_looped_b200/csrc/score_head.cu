@@ -34,6 +34,7 @@ constexpr int kSpare = 2;          // candidates scored in fp64 beyond k
 constexpr int kMaxCand = 20;       // candidates kept per slice, at most
 constexpr int SC_BK = 64;          // k per stage (one 128-byte swizzled row)
 constexpr int kScoreSms = 148;
+constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ bool sc_better(float x, int v, float bx, int bv) {
   return x > bx || (x == bx && v < bv);
@@ -46,6 +47,13 @@ struct ScoreRec {
   float* top_x;
   int* top_v;
 };
+
+// the largest float below x (x not NaN)
+__device__ __forceinline__ float sc_below(float x) {
+  if (x == -INFINITY) return x;
+  const int u = __float_as_int(x);
+  return __int_as_float(x > 0.f ? u - 1 : x < 0.f ? u + 1 : (int)0x80000001);
+}
 
 __device__ __forceinline__ float sc_ex2(float x) {
   float y;
@@ -302,14 +310,14 @@ __global__ void __launch_bounds__(SR_THREADS, 1)
     const uint32_t laddr = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const int cols = a.bn / 2;                         // a multiple of 16
     const int row = mt * 128 + r;
-    const float rs = row < a.n ? a.scale[row] : 1.f, rs2 = rs * 1.4426950408889634f;
+    const float rs = row < a.n ? a.scale[row] : 1.f, rs2 = rs * kLog2e;
     float m = -INFINITY, l = 0.f, sx = 0.f;            // in log2 units
     // the row's best so far, and a queue of newcomers in shared memory: logits
     // above the list's last are queued (a predicated store each) and inserted when
     // some lane's queue fills, so the insertion network runs about as often as the
     // busiest lane needs, not as often as any lane does
-    float cx[KC > 0 ? KC : 1];
-    int cv[KC > 0 ? KC : 1];
+    float cx[KC];
+    int cv[KC];
 #pragma unroll
     for (int p = 0; p < KC; ++p) {
       cx[p] = -INFINITY;
@@ -384,11 +392,11 @@ __global__ void __launch_bounds__(SR_THREADS, 1)
               sx = fmaf(e, t, sx);
             }
           }
-          if (KC > 0 && __any_sync(0xffffffffu, top > cx[KC > 0 ? KC - 1 : 0])) {
+          if (__any_sync(0xffffffffu, top > cx[KC - 1])) {
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
               if ((j & 3) == 0 && __any_sync(0xffffffffu, queued > SR_QUEUE - 4)) drain();
-              if (j < nv && x[j] > cx[KC > 0 ? KC - 1 : 0]) {
+              if (j < nv && x[j] > cx[KC - 1]) {
                 queue[queued * 256] = make_uint2(__float_as_uint(x[j]), (uint32_t)(v0 + c0 + j));
                 ++queued;
               }
@@ -400,7 +408,7 @@ __global__ void __launch_bounds__(SR_THREADS, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars.acc_empty[buf]);
     }
-    if (KC > 0) drain();
+    drain();
     if (row < a.n) {
       const size_t at = (size_t)row * a.slices + 2 * group + half;
       a.rec.stat[at] = make_float4(m, l, sx, 0.f);
@@ -435,8 +443,10 @@ __global__ void __launch_bounds__(SV_THREADS, 1)
   extern __shared__ uint8_t sv_raw[];
   __shared__ ScoreBars bars;
   __shared__ float st[SV_MAX_ROWS][3];
-  __shared__ float lx[SV_MAX_ROWS][KC > 0 ? KC : 1];
-  __shared__ int lv[SV_MAX_ROWS][KC > 0 ? KC : 1];
+  __shared__ float lx[SV_MAX_ROWS][KC];
+  __shared__ int lv[SV_MAX_ROWS][KC];
+  __shared__ float ex[8][32];                       // a warp's entrants
+  __shared__ int ev[8][32];
   uint8_t* smem = (uint8_t*)(((uintptr_t)sv_raw + 1023) & ~(uintptr_t)1023);
   constexpr int ZLD = 132;
   float* zb = reinterpret_cast<float*>(smem + (size_t)a.stages * a.stage_bytes);   // [tp][ZLD]
@@ -596,7 +606,7 @@ __global__ void __launch_bounds__(SV_THREADS, 1)
       if (sc_barrier_or(!ok)) break;
       const int v0 = t * a.bn, valid = min(a.bn, a.V - v0);
       for (int row = warp; row < a.n; row += 8) {
-        const float rs = a.scale[row], rs2 = rs * 1.4426950408889634f;
+        const float rs = a.scale[row], rs2 = rs * kLog2e;
         float x[4], top = -INFINITY;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -634,37 +644,66 @@ __global__ void __launch_bounds__(SV_THREADS, 1)
           st[row][1] = l;
           st[row][2] = sx;
         }
-        if (KC > 0) {
-          // lane p holds the list's p-th entry
-          float cx = lane < KC ? lx[row][lane] : INFINITY;
-          int cv = lane < KC ? lv[row][lane] : -1;
-          float worst = __shfl_sync(0xffffffffu, cx, KC - 1);
-          bool changed = false;
+        // Entrants of the row's list.  More than a warp's worth of them (a first
+        // tile) are cut at the kc-th best of the lanes' own best, a bound of the
+        // tile's kc-th best from below.
+        const float worst = lx[row][KC - 1];
+        float cut = worst;
+        int hits = 0;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) hits += __popc(__ballot_sync(0xffffffffu, x[q] > worst));
+        if (hits > 32) {
+          int rank = 0;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const float o = __shfl_sync(0xffffffffu, top, j);
+            rank += o > top || (o == top && j < lane);
+          }
+          // just below the lane's best of that rank, so that the test stays x > cut
+          const float kth = __shfl_sync(0xffffffffu, top, __ffs(__ballot_sync(0xffffffffu, rank == KC - 1)) - 1);
+          cut = fmaxf(worst, sc_below(kth));
+          hits = 0;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) hits += __popc(__ballot_sync(0xffffffffu, x[q] > cut));
+        }
+        // in rounds of 32 at most (one, but for many equal logits): the entrants to
+        // lanes, then every entry's place by counting who is before it
+        int done = 0;
+        while (done < hits) {
+          int before = 0;
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            unsigned hit = __ballot_sync(0xffffffffu, x[q] > worst);   // ids ascend: an equal logit seen later loses
-            while (hit) {
-              const int src = __ffs(hit) - 1;
-              hit &= hit - 1;
-              const float xv = __shfl_sync(0xffffffffu, x[q], src);
-              if (!(xv > worst)) continue;
-              const int id = v0 + src + 32 * q;
-              const bool in = xv > cx;
-              const float px = __shfl_up_sync(0xffffffffu, cx, 1);
-              const int pv = __shfl_up_sync(0xffffffffu, cv, 1);
-              const bool up = lane > 0 && xv > px;
-              if (lane < KC) {
-                cv = up ? pv : in ? id : cv;
-                cx = up ? px : in ? xv : cx;
-              }
-              worst = __shfl_sync(0xffffffffu, cx, KC - 1);
-              changed = true;
+            const unsigned m4 = __ballot_sync(0xffffffffu, x[q] > cut);
+            const int at = before + __popc(m4 & ((1u << lane) - 1)) - done;
+            if (x[q] > cut && at >= 0 && at < 32) {
+              ex[warp][at] = x[q];
+              ev[warp][at] = v0 + lane + 32 * q;
             }
+            before += __popc(m4);
           }
-          if (changed && lane < KC) {
-            lx[row][lane] = cx;
-            lv[row][lane] = cv;
+          const int cnt = min(32, hits - done);
+          done += 32;
+          __syncwarp();
+          const float nx = lane < cnt ? ex[warp][lane] : -INFINITY, ox = lane < KC ? lx[row][lane] : -INFINITY;
+          const int nv = lane < cnt ? ev[warp][lane] : 0x7fffffff, ov = lane < KC ? lv[row][lane] : 0x7fffffff;
+          int nr = 0, orank = lane;                    // the list is sorted
+          for (int i = 0; i < KC; ++i) nr += sc_better(lx[row][i], lv[row][i], nx, nv);
+          for (int i = 0; i < cnt; ++i) {
+            const float ix = ex[warp][i];
+            const int iv = ev[warp][i];
+            nr += sc_better(ix, iv, nx, nv);
+            orank += sc_better(ix, iv, ox, ov);
           }
+          __syncwarp();
+          if (lane < KC && orank < KC) {
+            lx[row][orank] = ox;
+            lv[row][orank] = ov;
+          }
+          if (lane < cnt && nr < KC) {
+            lx[row][nr] = nx;
+            lv[row][nr] = nv;
+          }
+          __syncwarp();
         }
       }
       asm volatile("bar.sync 1, 256;" ::: "memory");   // zb is free again
@@ -715,6 +754,8 @@ __global__ void __launch_bounds__(SM_THREADS, 3) score_merge_kernel(ScoreArgs a,
   __shared__ int n_cand;
   __shared__ double zs[kMaxCand + 1];
   __shared__ int ids[kMaxCand + 1];
+  __shared__ float fast[kMaxCand];          // the chosen ones' logits by pass 1
+  __shared__ double sums[2];                // log of the corrected sum, expected distance from the maximum
   const int row = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int slices = tc.slices;
   const float4* stat = tc.rec.stat + (size_t)row * slices;
@@ -729,7 +770,7 @@ __global__ void __launch_bounds__(SM_THREADS, 3) score_merge_kernel(ScoreArgs a,
   for (int u = 0; u < SM_PER; ++u) {
     const int i = tid + u * SM_THREADS;
     v[u] = i < slices ? stat[i] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
-    hx[u] = i < slices && kc > 0 ? gx[i] : -INFINITY;
+    hx[u] = i < slices ? gx[i] : -INFINITY;
   }
   for (int j = 4 * tid; j < a.d; j += 4 * SM_THREADS) {
     const float4 f = *reinterpret_cast<const float4*>(yr + j);
@@ -751,7 +792,7 @@ __global__ void __launch_bounds__(SM_THREADS, 3) score_merge_kernel(ScoreArgs a,
   if (lane == 0) wred[0][warp] = M;
   if (tid == 0) n_cand = 0;
   bad = __syncthreads_or(bad);
-  if (warp == 0 && kc > 0) {
+  if (warp == 0) {
     float g = gmax[0][lane];
 #pragma unroll
     for (int w = 1; w < SM_WARPS; ++w) g = fmaxf(g, gmax[w][lane]);
@@ -803,7 +844,7 @@ __global__ void __launch_bounds__(SM_THREADS, 3) score_merge_kernel(ScoreArgs a,
 #pragma unroll
   for (int u = 0; u < SM_PER; ++u) {
     const int i = tid + u * SM_THREADS;
-    if (kc == 0 || i >= slices || !(hx[u] >= bound)) continue;
+    if (i >= slices || !(hx[u] >= bound)) continue;
     bool more = true;
     for (int p0 = 0; p0 < kc && more; p0 += 4) {      // kc is a multiple of 4
       float x4[4];
@@ -824,7 +865,7 @@ __global__ void __launch_bounds__(SM_THREADS, 3) score_merge_kernel(ScoreArgs a,
       }
     }
   }
-  const int n_pick = min(kc == 0 ? 0 : a.k + kSpare, a.V);
+  const int n_pick = min(max(a.k, kSpare) + kSpare, a.V);
   if (tid == 0) ids[n_pick] = target;
   __syncthreads();
   // a candidate's rank: how many come before it (their order in memory is of no matter)
@@ -835,7 +876,10 @@ __global__ void __launch_bounds__(SM_THREADS, 3) score_merge_kernel(ScoreArgs a,
     int rank = 0;
     for (int j = lane; j < nc; j += 32) rank += sc_better(cand[j].x, cand[j].v, x, id);
     rank = __reduce_add_sync(0xffffffffu, rank);
-    if (lane == 0 && rank < n_pick) ids[rank] = id;
+    if (lane == 0 && rank < n_pick) {
+      ids[rank] = id;
+      fast[rank] = x;
+    }
   }
   __syncthreads();
   for (int p0 = warp; p0 <= n_pick; p0 += 2 * SM_WARPS) {
@@ -884,10 +928,35 @@ __global__ void __launch_bounds__(SM_THREADS, 3) score_merge_kernel(ScoreArgs a,
       if (lane == 0 && p0 + u * SM_WARPS <= n_pick) zs[p0 + u * SM_WARPS] = z;
     }
   }
-  constexpr double kLn2 = 0.693147180559945309;
-  const double log_l = log((double)L), lse = (double)M * kLn2 + log_l;
   __syncthreads();
-  if (tid == 0 && a.entropy) a.entropy[row] = (float)(log_l - (double)S / (double)L * kLn2);
+  constexpr double kLn2 = 0.693147180559945309;
+  if (warp == 0) {
+    // The tensor cores add towards zero, d / 8 times per logit: a logit z of pass 1 is
+    // off by up to d 2^-28 z, which matters where one token has most of the
+    // probability.  The chosen tokens' terms are replaced by those of their fp64
+    // logits; what is left are many small terms of small logits.
+    double dl = 0.0, ds = 0.0;
+    if (lane < n_pick) {
+      // t0 as pass 1 had it, by the fp32 log2(e)
+      const double t1 = zs[lane] / kLn2 - (double)M, t0 = (double)fast[lane] * (double)kLog2e - (double)M;
+      const double e1 = exp2(t1), e0 = exp2(t0);
+      dl = e1 - e0;
+      ds = e1 * t1 - e0 * t0;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      dl += __shfl_xor_sync(0xffffffffu, dl, o);
+      ds += __shfl_xor_sync(0xffffffffu, ds, o);
+    }
+    if (lane == 0) {
+      const double l = (double)L + dl;
+      sums[0] = log(l);
+      sums[1] = ((double)S + ds) / l * kLn2;
+    }
+  }
+  __syncthreads();
+  const double lse = (double)M * kLn2 + sums[0];
+  if (tid == 0 && a.entropy) a.entropy[row] = (float)(sums[0] - sums[1]);
   if (tid == 0 && a.logp)
     a.logp[row] = target < 0 ? 0.f : target >= a.V ? CUDART_NAN_F : (float)(zs[n_pick] - lse);
   // the chosen ones' final order: a warp per token, a lane per rival
@@ -905,12 +974,13 @@ __global__ void __launch_bounds__(SM_THREADS, 3) score_merge_kernel(ScoreArgs a,
 
 size_t score_merge_smem(int slices, int kc, int d) { return (size_t)d * 8 + (size_t)slices * kc * sizeof(ScoreCand); }
 
-// candidates a slice keeps: k + kSpare, in the sizes that are instantiated
-int score_cand(int k) { return k == 0 ? 0 : k + kSpare <= 8 ? 8 : k + kSpare <= 12 ? 12 : 20; }
+// candidates a slice keeps: k + kSpare (at least 2 kSpare, for the sum's sake), in the
+// sizes that are instantiated
+int score_cand(int k) { return k + kSpare <= 4 ? 4 : k + kSpare <= 8 ? 8 : k + kSpare <= 12 ? 12 : 20; }
 
 constexpr int kScoreChunk = 37 * 128;  // rows per sweep over the embedding: bounds the workspace; 37 row
                                        // tiles share 148 SMs evenly
-constexpr size_t kVocabSmem = 215 * 1024;   // beside up to 11 KB of static shared memory
+constexpr size_t kVocabSmem = 213 * 1024;   // beside up to 13 KB of static shared memory
 constexpr size_t kRowsSmem = 226 * 1024;
 
 struct ScorePlan {
@@ -1037,9 +1107,9 @@ tl_status launch_score_head(const ScoreArgs& a0, cudaStream_t s) {
                      CU_TENSOR_MAP_SWIZZLE_128B));
     TL_LAUNCH_PDL(score_split_kernel, t.pad, 256, 0, s, a.y, a.y_stride, a.n, a.d, t.pad, parts, scale, t.flag);
     const int kc = score_cand(a.k);
-    TL_TRY(kc == 0 ? launch_score_pass1<0>(p, my, me, s)
+    TL_TRY(kc == 4   ? launch_score_pass1<4>(p, my, me, s)
                    : kc == 8 ? launch_score_pass1<8>(p, my, me, s)
-                             : kc == 12 ? launch_score_pass1<12>(p, my, me, s) : launch_score_pass1<20>(p, my, me, s));
+                   : kc == 12 ? launch_score_pass1<12>(p, my, me, s) : launch_score_pass1<20>(p, my, me, s));
     TL_LAUNCH_PDL(score_merge_kernel, a.n, SM_THREADS, score_merge_smem(t.slices, kc, a.d), s, a, kc, t);
   }
   return ok();
