@@ -217,7 +217,7 @@ tl_status tl_kv_read_int4(const tl_kv_int4* cache, uint16_t* k, uint16_t* v, lon
  *   out    device fp16 [n_lanes * n_q][out_stride] (must not overlap q)
  *   workspace  device scratch of tl_attention_int4_workspace_bytes bytes, 16-byte
  *          aligned, for this call's use until it completes on the stream; may be
- *          NULL when that size is 0, as it is for max_ctx < 4096
+ *          NULL when that size is 0, as it is for max_ctx < 8192
  * Requirements: 0 <= n_q <= 8, q_heads a multiple of n_heads (at most 1024), q and
  * out 16-byte aligned, strides multiples of 8 and at least q_heads * head_dim. */
 tl_status tl_attention_int4_workspace_bytes(const tl_kv_int4* cache, int n_q, int q_heads,
@@ -428,7 +428,7 @@ tl_status tl_kv_layer_bytes(int n_heads, int head_dim, int max_ctx, tl_kv_dtype 
 /* Bytes of the cache buffer for n_lanes lanes of max_ctx positions each, lane
  * b running L_per_lane[b] loop iterations: the 4 KiB header, every lane's
  * n_pre + L_b slots (tl_kv_layer_bytes each) and, for TL_KV_H, the rebuild
- * workspace or, for TL_KV_INT4 with max_ctx >= 4096, the attention's.  Host-only.  Errors: TL_ERR_INVALID_ARG for a NULL model,
+ * workspace or, for TL_KV_INT4 with max_ctx >= 8192, the attention's.  Host-only.  Errors: TL_ERR_INVALID_ARG for a NULL model,
  * L_per_lane or bytes, n_lanes outside [1, 8], max_ctx outside [1, the
  * model's max_ctx], an L outside [1, max_L] or an unknown dtype. */
 tl_status tl_kv_bytes(const tl_model* model, int n_lanes, int max_ctx,

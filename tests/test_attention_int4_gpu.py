@@ -97,18 +97,18 @@ def test_windows_beyond_the_context_are_no_windows(window):
 
 
 @pytest.mark.parametrize("lanes,H,group,hd,ctx,n_q,window", [
-    (1, 2, 1, 128, 4095, 1, 0), (1, 2, 1, 128, 4096, 1, 0), (1, 1, 8, 64, 4097, 3, 0), (2, 3, 2, 128, 5000, 5, 700),
+    (1, 2, 1, 128, 8191, 1, 0), (1, 2, 1, 128, 8192, 1, 0), (1, 1, 8, 64, 8193, 3, 0), (2, 3, 2, 128, 9000, 5, 700),
     (1, 1, 1, 64, 40001, 1, 0),
 ])
 def test_long_contexts_go_through_a_workspace(lanes, H, group, hd, ctx, n_q, window):
-    """From 4096 positions a split may be wider than a cluster; lengths from none to
+    """From 8192 positions a split may be wider than a cluster; lengths from none to
     all of the cache, a workspace given and one allocated by the binding."""
     k, v = _kv(1, H, ctx, hd, 25)
     cache = Cache(np.repeat(k, lanes, 0), np.repeat(v, lanes, 0))
     q = _q(lanes * n_q, H * group, hd, 26, 2.0)
     need = tl.tl_attention_int4_workspace_bytes(*cache.t, n_q, H * group)
-    assert (need > 0) == (ctx >= 4096)
-    for lens in ([ctx] * lanes, [ctx - 1, 4000][:lanes], [1, 0][:lanes], [33, 5][:lanes]):
+    assert (need > 0) == (ctx >= 8192)
+    for lens in ([ctx] * lanes, [ctx - 1, 7000][:lanes], [1, 0][:lanes], [33, 5][:lanes]):
         got = _run(q, cache, lens, n_q, window)
         _check(got, q, cache, lens, n_q, window)
         ws = torch.full((max(need, 1) + 64,), 0xFF, dtype=torch.uint8, device="cuda")

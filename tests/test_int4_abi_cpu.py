@@ -76,7 +76,7 @@ def test_attention_workspace():
         c = _cache(code_stride=1 << 40, param_stride=1 << 40, **kw)
         assert tl.lib.tl_attention_int4_workspace_bytes(ctypes.byref(c), n_q, heads, ctypes.byref(b)) == tl.TL_OK
         return b.value
-    assert need(max_ctx=4095) == 0 and need(max_ctx=4096) > 0       # two lanes of two heads: the split is wide
+    assert need(max_ctx=8191) == 0 and need(max_ctx=8192) > 0       # two lanes of two heads: the split is wide
     assert need(max_ctx=1 << 20, n_q=0) == 0 and need(max_ctx=1 << 20, n_lanes=0) == 0
     assert need(max_ctx=65536, n_lanes=512) == 0                     # enough lanes fill the GPU without it
     big = need(max_ctx=1 << 20)

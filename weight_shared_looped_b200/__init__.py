@@ -322,7 +322,7 @@ def tl_kv_read_int4(k_codes, k_params, v_codes, v_params, pos, k, v, cu=None, st
                   v_params, pos, cu, stream)
 
 
-_INT4_SPLIT_CTX = 4096   # caches below this many positions need no workspace
+_INT4_SPLIT_CTX = 8192   # caches below this many positions need no workspace
 
 
 def tl_attention_int4_workspace_bytes(k_codes, k_params, v_codes, v_params, n_q: int,

@@ -596,9 +596,9 @@ size_t a4_smem_bytes() {
 int a4_split(int max_ctx, int pairs, bool* through_ws) {
   const int tiles = (max_ctx + A4_TILE - 1) / A4_TILE;
   // as many CTAs as fill the GPU once (four per SM), a tile per warp at least.  More
-  // than a cluster's eight cost a second launch: 16 heads at 2112 positions 10.3 us
-  // in a cluster and 8.2 through the workspace, 32 heads 10.3 and 10.3; at 4096
-  // positions 12.3 and 10.3, 12.3 and 13.3; at 16384 the cluster takes 26 against 18
+  // than a cluster's eight cost a second launch and a workspace: one lane of 16
+  // heads takes 12.3 us in a cluster and 10.3 through the workspace at 4096
+  // positions (12.3 and 13.3 with two lanes), 16.4 and 13.2 at 8192
   int c = std::min((tiles + A4_WARPS - 1) / A4_WARPS, std::max(1, 148 * 4 / pairs));
   *through_ws = max_ctx >= kInt4SplitCtx && c > A4_MAX_CLUSTER;
   if (*through_ws) return std::min(c, A4_MAX_SPLIT);

@@ -303,7 +303,7 @@ struct AttnInt4Args {
   float* ws;                       // attn_int4_workspace bytes; null where that is 0
   int col_tiles;                   // set by the launcher
 };
-constexpr int kInt4SplitCtx = 4096;   // caches below this many positions need no workspace
+constexpr int kInt4SplitCtx = 8192;   // caches below this many positions need no workspace
 size_t attn_int4_workspace(int n_rows, int H, int hd, int cols, int max_ctx, int split_pairs);
 tl_status launch_attn_int4(const AttnInt4Args& a, cudaStream_t s);
 
