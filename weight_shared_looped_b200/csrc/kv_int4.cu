@@ -76,41 +76,59 @@ __global__ void __launch_bounds__(KV4_THREADS) kv4_rows_kernel(Kv4RowsArgs a) {
         w[z][u] = at[u].y >= 0 ? *reinterpret_cast<const uint4*>((z ? a.v_in : a.k_in) + elem)
                                : make_uint4(0u, 0u, 0u, 0u);
     }
+    // Group extremes, least in the low half and largest (negated) in the high: one
+    // reduction over the four neighbours that share a group.
+    __half2 ext[2 * U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
+    for (int i = 0; i < 2 * U; ++i) {
+      const uint4 q = w[i % 2][i / 2];
+      // NaN stays NaN
+      const __half2 mn = __hmin2_nan(__hmin2_nan(kv_bits_h2(q.x), kv_bits_h2(q.y)), __hmin2_nan(kv_bits_h2(q.z), kv_bits_h2(q.w)));
+      const __half2 mx = __hmax2_nan(__hmax2_nan(kv_bits_h2(q.x), kv_bits_h2(q.y)), __hmax2_nan(kv_bits_h2(q.z), kv_bits_h2(q.w)));
+      ext[i] = __halves2half2(__hmin_nan(__low2half(mn), __high2half(mn)), __hneg(__hmax_nan(__low2half(mx), __high2half(mx))));
 #pragma unroll
-      for (int z = 0; z < 2; ++z) {
-        const uint32_t ws[4] = {w[z][u].x, w[z][u].y, w[z][u].z, w[z][u].w};
-        __half2 mn = kv_bits_h2(ws[0]), mx = mn;
+      for (int o = 1; o < 4; o <<= 1)
+        ext[i] = __hmin2_nan(ext[i], kv_bits_h2(__shfl_xor_sync(0xffffffffu, kv_h2_bits(ext[i]), o)));
+    }
+    // Scale, zero point and reciprocal take as many instructions as a third of a
+    // row's codes: the four neighbours share them out, group i to neighbour i mod 4.
+    constexpr int OWN = (2 * U + 3) / 4;
+    uint32_t own_param[OWN];
+    float own_inv[OWN];
+    const int me = threadIdx.x & 3;
 #pragma unroll
-        for (int i = 1; i < 4; ++i) {                  // NaN stays NaN
-          mn = __hmin2_nan(mn, kv_bits_h2(ws[i]));
-          mx = __hmax2_nan(mx, kv_bits_h2(ws[i]));
-        }
-        // least in the low half, largest (negated) in the high: one reduction over
-        // the four neighbours that share the group
-        __half2 e = __halves2half2(__hmin_nan(__low2half(mn), __high2half(mn)),
-                                   __hneg(__hmax_nan(__low2half(mx), __high2half(mx))));
+    for (int j = 0; j < OWN; ++j) {
+      __half2 e = ext[4 * j];
 #pragma unroll
-        for (int o = 1; o < 4; o <<= 1)
-          e = __hmin2_nan(e, kv_bits_h2(__shfl_xor_sync(0xffffffffu, kv_h2_bits(e), o)));
-        const Int4Group g = kv_int4_group(__low2float(e), -__high2float(e));
-        // the eight biased codes shifted and added; their biases add up to a constant
-        uint32_t word = 0, bias = 0;
+      for (int i = 1; i < 4; ++i)
+        if (4 * j + i < 2 * U && me == i) e = ext[4 * j + i];
+      const Int4Group g = kv_int4_group(__low2float(e), -__high2float(e));
+      own_param[j] = g.param;
+      own_inv[j] = g.inv;
+    }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 f = __half22float2(kv_bits_h2(ws[i]));
-          word += kv_int4_biased(f.x, g) << (8 * i);
-          word += kv_int4_biased(f.y, g) << (8 * i + 4);
-          bias += (kInt4CodeBias << (8 * i)) + (kInt4CodeBias << (8 * i + 4));
-        }
-        word = kv_int4_marked(g) ? 0u : word - bias;
-        if (at[u].y >= 0) {
-          const size_t slot = (size_t)head * a.max_ctx + at[u].y;
-          ((z ? a.v_codes : a.k_codes) + (size_t)at[u].x * a.code_stride)[slot * PARTS + part] = word;
-          if (part % 4 == 0)
-            ((z ? a.v_params : a.k_params) + (size_t)at[u].x * a.param_stride)[slot * RP + part / 4] = g.param;
-        }
+    for (int i = 0; i < 2 * U; ++i) {
+      const int u = i / 2, z = i % 2;
+      Int4Group g;
+      g.param = __shfl_sync(0xffffffffu, own_param[i / 4], i % 4, 4);
+      g.inv = __shfl_sync(0xffffffffu, own_inv[i / 4], i % 4, 4);
+      g.lo = __low2float(ext[i]);
+      // the eight biased codes shifted and added; their biases add up to a constant
+      const uint32_t ws[4] = {w[z][u].x, w[z][u].y, w[z][u].z, w[z][u].w};
+      uint32_t word = 0, bias = 0;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float2 f = __half22float2(kv_bits_h2(ws[q]));
+        word += kv_int4_biased(f.x, g) << (8 * q);
+        word += kv_int4_biased(f.y, g) << (8 * q + 4);
+        bias += (kInt4CodeBias << (8 * q)) + (kInt4CodeBias << (8 * q + 4));
+      }
+      word = kv_int4_marked(g) ? 0u : word - bias;
+      if (at[u].y >= 0) {
+        const size_t slot = (size_t)head * a.max_ctx + at[u].y;
+        ((z ? a.v_codes : a.k_codes) + (size_t)at[u].x * a.code_stride)[slot * PARTS + part] = word;
+        if (part % 4 == 0)
+          ((z ? a.v_params : a.k_params) + (size_t)at[u].x * a.param_stride)[slot * RP + part / 4] = g.param;
       }
     }
   } else {
