@@ -113,6 +113,15 @@ def test_write_and_read_back_bit_exact(counts, pos, behind, H, hd, ctx):
                 assert np.array_equal(got[r], exact), r
 
 
+@pytest.mark.parametrize("counts,pos,behind,H,hd,ctx", [
+    ([1201, 0, 700, 3, 500], [0, 5, 611, 1310, 100], 2, 16, 128, 1311),   # a lane ends at the cache's end
+    ([2400, 1400, 1001], [0, 1001, 1400], 0, 16, 64, 2403),
+])
+def test_many_rows(counts, pos, behind, H, hd, ctx):
+    """Batches large enough for two rows a thread; the last CTA's rows are cut off."""
+    test_write_and_read_back_bit_exact(counts, pos, behind, H, hd, ctx)
+
+
 @pytest.mark.parametrize("hd", [64, 128])
 def test_equal_shares_and_column_slices(hd):
     """Without cu every lane takes n / lanes rows; k and v are column slices of

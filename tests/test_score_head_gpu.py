@@ -94,6 +94,14 @@ def test_matches_fp64(n, V, d, k):
     _check(E, y, t, k)
 
 
+@pytest.mark.parametrize("n,V", [
+    (131, 700), (65, 5003), (131, 7001), (300, 5003), (131, 20011), (1021, 3001), (131, 15001), (300, 12007),
+])
+def test_every_tile_width(n, V):
+    """Vocabulary tiles of 32, 64, .. 256 entries; none of the vocabularies is a multiple of its tile."""
+    test_matches_fp64(n, V, 192, 6)
+
+
 def test_ties_go_to_the_lowest_id():
     """Equal rows of the embedding give equal logits."""
     E, y, t = _inputs(40, 3000, 256, 50)

@@ -10,29 +10,34 @@
 // Codes become fp16 values in registers (three half2 operations a pair: the
 // nibble under the exponent of 1024, less the bias, times the scale plus the
 // zero point; the one rounding of the value to fp16 is the read-back's own), so
-// the cache is read once, as it is stored: each warp copies its tiles of 16 keys
-// (2.5 KB for head_dim 128) through a ring of its own in shared memory, three tiles
-// ahead (loads into registers one tile ahead left a warp waiting for memory at
-// every tile: 1.3 us a tile against 0.2 of work).  From the K tile lane (g, t)
-// takes a whole 32-code group of two keys, from the V tile the same 16 head_dim
-// elements of four keys; the k order inside an MMA is free as long as both
-// operands agree, and is chosen so that no read has a bank conflict.
+// the cache is read once, as it is stored: each warp copies its tiles of 32 keys
+// (5 KB for head_dim 128) through a ring of its own in shared memory, one tile
+// ahead of the one it works on (loads into registers instead left a warp waiting
+// for memory at every tile: 1.3 us per 16 keys against 0.2 of work).  Sixteen
+// warps per SM keep 80 KB on the way, which covers the memory's latency; rings of
+// three and four tiles measured the same or slower, and tiles of 16 keys 48 us
+// where 32 take 41.  From the K tile lane (g, t) takes a whole 32-code group of
+// two keys, from the V tile the same 16 head_dim elements of four keys; the k
+// order inside an MMA is free as long as both operands agree, and is chosen so
+// that no read has a bank conflict.
 //
-// Bound by memory (head_dim 128: 160 bytes per key and head); about 280
-// instructions per 16 keys keep the issue slots about two thirds busy at that
-// rate.
+// Memory sets the floor (head_dim 128: 160 bytes per key and head), the issue
+// slots the pace: about 340 instructions per 16 keys, 63 % of the slots busy.
+// Two lanes of up to 65536 positions, 8 cache heads, 4 queries per head: 147 MB in
+// 41 us, 3.6 TB/s.  Many short lanes are bound by their launch, the merge and the tail.
 //
-// Work split: the context is cut into tiles of 16 keys; tile i belongs to warp
-// slot i mod (CTAs of the cluster x warps), whatever the lane's length, so the
+// Work split: the context is cut into tiles of 32 keys; tile i belongs to warp
+// slot i mod (CTAs of the split x warps), whatever the lane's length, so the
 // work is even for every length and a query's arithmetic does not depend on
 // the other queries of its launch: a query alone and the same query among
 // several give the same bits.  Each warp keeps a running maximum and sum per
 // query (base 2); the maximum is raised only when a score exceeds it by more
 // than 2^8, which spares the cross-lane maximum on most tiles (weights stay
-// below 2^8, well inside fp16).  The warps merge in warp order through shared
-// memory, the CTAs of the cluster in rank order through distributed shared
+// at or below 2^8, well inside fp16).  The warps merge in warp order through
+// shared memory, up to eight CTAs in rank order through distributed shared
 // memory, every CTA finishing its share of the outputs: one launch, no
-// workspace, the same bits at every run.
+// workspace.  Longer contexts are split further (a4_split), their records joined
+// in order by a second launch.  The bits are the same at every run.
 //
 // Masked places never reach a sum: scores are selected, not multiplied, and
 // where a key's value is not finite and some query of the tile does not see
@@ -51,9 +56,7 @@ namespace {
 constexpr int A4_COLS = 8;          // queries per CTA (MMA N)
 constexpr int A4_TILE = 32;         // keys per warp tile: two sub-tiles of 16 (MMA M)
 constexpr int A4_WARPS = 4;          // warps per CTA
-#ifndef A4_MINB
-#define A4_MINB 4
-#endif
+constexpr int A4_MINB = 4;           // CTAs per SM
 constexpr int A4_MAX_CLUSTER = 8;
 constexpr int A4_MAX_SPLIT = 64;
 constexpr int A4_STAGES = 2;         // tiles of a warp's ring
@@ -351,7 +354,7 @@ __global__ void __launch_bounds__(32 * A4_WARPS, A4_MINB) attn_int4_kernel(AttnI
       }
     }
     const int base = tile * A4_TILE;
-    const bool edge = base < full_lo || base + A4_TILE - 1 > full_hi;   // uniform over the CTA
+    const bool edge = base < full_lo || base + A4_TILE - 1 > full_hi;   // uniform over the warp
     if (edge) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {

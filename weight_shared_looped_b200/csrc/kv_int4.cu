@@ -10,8 +10,11 @@
 // one head, so its code and parameter accesses are contiguous and its fp16
 // accesses are whole head rows.
 //
-// Bound by memory: written, 4 * H * hd bytes in and 1.25 * H * hd out per
-// token; read back, the reverse.
+// Memory sets the floor: written, 4 * H * hd bytes in and 1.25 * H * hd out per
+// token; read back, the reverse.  16384 tokens of 16 heads of 128 (172 MB each way)
+// are written in 42 us, 4.1 TB/s (issue slots: about 150 instructions per eight
+// values of K and of V, for the group's extremes and the rounding of each code), and
+// read back in 31 us, 5.6 TB/s.  One token per lane takes 2 us, a launch.
 #include "kv_int4.cuh"
 #include "tl_launch.cuh"
 
@@ -171,9 +174,13 @@ __global__ void __launch_bounds__(KV4_THREADS) kv4_rows_kernel(Kv4RowsArgs a) {
 template <int HD, bool WRITE>
 tl_status launch_kv4(const Kv4RowsArgs& a, cudaStream_t s) {
   constexpr int rows = KV4_THREADS / (HD / 8);
-  // four rows a thread once that leaves at least two CTAs per SM
-  if ((long)a.n_rows * a.H >= (long)rows * 4 * 148 * 2)
-    TL_LAUNCH_PDL((kv4_rows_kernel<HD, WRITE, 4>), dim3((a.n_rows + 4 * rows - 1) / (4 * rows), a.H), KV4_THREADS, 0, s, a);
+  // Two rows a thread once eight CTAs per SM are left of them (a full SM), one below.
+  // Written / read, us, one and two rows a thread, 16 heads of 128:  600 rows 4.6 / 3.3
+  // and 4.5 / 3.2, 1200 rows 6.2 / 4.7 and 6.6 / 4.7, 2400 rows 9.4 / 7.0 and 9.2 / 6.3,
+  // 16384 rows 46.3 / 34.6 and 42.2 / 30.9.  Four rows: 8.1 / 4.6 at 1200, 43.2 / 31.6
+  // at 16384.
+  if ((long)a.n_rows * a.H >= (long)rows * 2 * 148 * 8)
+    TL_LAUNCH_PDL((kv4_rows_kernel<HD, WRITE, 2>), dim3((a.n_rows + 2 * rows - 1) / (2 * rows), a.H), KV4_THREADS, 0, s, a);
   else
     TL_LAUNCH_PDL((kv4_rows_kernel<HD, WRITE, 1>), dim3((a.n_rows + rows - 1) / rows, a.H), KV4_THREADS, 0, s, a);
   return ok();

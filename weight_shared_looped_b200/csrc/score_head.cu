@@ -20,6 +20,12 @@
 // lowest token id; equal embedding rows tie in pass 1 already, and for another
 // token to be missed, three logits would have to lie within pass 1's error of the
 // k-th).
+//
+// Bounds (vocabulary 50257, d 2048): few rows by the embedding's 206 MB, 31 us; one row
+// with k 5 takes 47 us (passes 0 and 2 and the fill and tail of pass 1 are 12 of
+// them).  Many rows by the matrix work, twice 2 n V d; 1024 rows in 310 us with k 0,
+// 1.36 PFLOP/s, 333 with k 5 (candidates).  In between the epilogue of the last tiles
+// shows: 128 rows with k 8 take 80 us.
 #include <math_constants.h>
 
 #include <algorithm>
@@ -990,8 +996,10 @@ struct ScorePlan {
   size_t smem, parts_off, scale_off, flag_off, stat_off, top_x_off, top_v_off, bytes;
 };
 
-// Up to 64 rows the embedding streams as the M side (its bytes are the bound);
-// above, the rows are (the matrix work is).
+// Up to 64 rows the embedding streams as the M side (its bytes are the bound); above,
+// the rows are (the matrix work is).  Vocabulary 50257, d 2048, k 5, vocabulary-major
+// and row-major:  8 rows 52 and 69 us, 32 rows 56 and 71, 64 rows 69 and 73 (128
+// columns, the accumulator's size; 128 rows row-major 76).
 ScorePlan score_plan(int n, int V, int d, int k) {
   ScorePlan p;
   memset(&p, 0, sizeof(p));
@@ -1008,23 +1016,30 @@ ScorePlan score_plan(int n, int V, int d, int k) {
     t.vt = (V + t.bn - 1) / t.bn;
     p.grid = std::min(kScoreSms, t.vt);
     t.slices = p.grid;
-    // two k blocks per stage while four stages of them fit: a stage costs its copying
-    // thread about 0.25 us however small, as long as a k block's rows take from HBM
-    t.kbs = t.pad <= 32 ? 2 : 1;
-    t.stage_bytes = (uint32_t)t.kbs * (16384 + (uint32_t)(2 * t.pad * 128 + 1023) / 1024 * 1024);
+    // Two k blocks per stage while three such stages fit: a stage costs its copying
+    // thread about 0.25 us however small, as long as a k block's rows take from HBM.
+    // One and two blocks: 1 row 49 and 47 us, 32 rows 60 and 56, 56 rows 66 and 65; at 64
+    // rows two stages of two lose, 69 and 71.
     const size_t zb = (size_t)t.pad * 132 * 4;
+    const uint32_t block = 16384 + (uint32_t)(2 * t.pad * 128 + 1023) / 1024 * 1024;
+    t.kbs = 3 * 2 * (size_t)block + zb + 1024 <= kVocabSmem ? 2 : 1;
+    t.stage_bytes = (uint32_t)t.kbs * block;
     t.stages = (int)std::min<size_t>(12, (kVocabSmem - zb - 1024) / t.stage_bytes);
     p.smem = 1024 + (size_t)t.stages * t.stage_bytes + zb;
   } else {
     t.pad = (n + 127) / 128 * 128;
     t.mt = t.pad / 128;
     t.groups = kScoreSms / t.mt;
-    // the tile width (a multiple of 32) with the least work on the busiest CTA,
-    // counting a tile's fixed cost as 16 columns
+    // The tile width (a multiple of 32) with the least work on the busiest CTA, counting
+    // a tile's fixed cost (its activations' copies, the first k blocks' latency) as 48
+    // columns.  Measured at every width: 50257 entries take 128 rows 93 us by 96, 76 by
+    // 192, 83 by 256, and 512 rows 212 by 160 and 189 by 256; 2000 entries take 128 rows
+    // 38 by 32 and 52 by 256.  The rule is within 5 % of the best width in all of 40
+    // combinations of 5 vocabularies and 8 batches, 0.2 % on average.
     long best = -1;
-    for (int bn = 256; bn >= 128; bn -= 32) {
+    for (int bn = 256; bn >= 32; bn -= 32) {
       const int vt = (V + bn - 1) / bn;
-      const long cost = (long)((vt + t.groups - 1) / t.groups) * (bn + 16);
+      const long cost = (long)((vt + t.groups - 1) / t.groups) * (bn + 48);
       if (best < 0 || cost < best) {
         best = cost;
         t.bn = bn;
