@@ -178,6 +178,34 @@ def test_a_seen_nan_reaches_only_its_lane_and_head():
     assert np.array_equal(got, want)
 
 
+@pytest.mark.parametrize("ctx,lanes,H,group,hd,n_q", [
+    (100, 80, 2, 1, 64, 1), (200, 90, 1, 2, 128, 3), (130, 40, 1, 1, 128, 1), (512, 100, 1, 1, 128, 1),
+    (700, 80, 1, 4, 128, 1), (2112, 75, 1, 1, 64, 1), (2112, 37, 4, 1, 128, 2), (2112, 90, 1, 8, 128, 1),
+    (2112, 25, 2, 3, 64, 1), (2112, 19, 2, 8, 128, 1), (1100, 300, 2, 1, 128, 1), (1100, 150, 2, 8, 64, 1),
+    (8200, 80, 1, 1, 128, 1), (9000, 20, 1, 1, 64, 1), (16500, 38, 1, 16, 64, 1),
+])
+def test_any_number_of_lanes(ctx, lanes, H, group, hd, n_q):
+    """However the work is spread (one CTA a lane and head, clusters, a workspace),
+    lanes of the same cache and length give the same bits, and the right ones."""
+    two = Cache(*_kv(2, H, ctx, hd, 27))
+    pick = np.arange(lanes) % 2
+    at = torch.from_numpy(pick).cuda()
+    cache = [t[at] for t in two.t]
+    base = _q(6 * n_q, H * group, hd, 28, 2.0).reshape(6, n_q, H * group, hd)
+    kind = np.arange(lanes) % 6                        # lanes b and b + 6 are alike
+    q = base[kind].reshape(lanes * n_q, H * group, hd)
+    lens = np.array([ctx, 1, 0, ctx - 37, ctx // 2, ctx - 1], np.int32)[kind]
+    x = torch.from_numpy(q.reshape(lanes * n_q, -1)).cuda()
+    out = torch.full_like(x, 9.0)
+    tl.tl_attention_int4(x, *cache, torch.from_numpy(lens).cuda(), out, n_q=n_q)
+    got = out.cpu().numpy().reshape(lanes, n_q, H * group, hd)
+    for b in range(6, lanes):
+        assert np.array_equal(got[b], got[b % 6]), b
+    for b in range(0, 6, 2):
+        six = slice(b * n_q, (b + 2) * n_q)
+        _check(got[b:b + 2].reshape(2 * n_q, H * group, hd), q[six], two, lens[b:b + 2].tolist(), n_q, 0)
+
+
 def test_a_query_alone_and_among_others_gives_the_same_bits():
     """A query's arithmetic does not depend on the lane's other queries, its
     neighbours' contents, or the run."""

@@ -127,6 +127,52 @@ def test_lanes_are_independent():
     m.close()
 
 
+@pytest.mark.parametrize("ctx", [1000, 8200])
+def test_any_number_of_lanes_of_sixteen_heads(ctx):
+    """The work is spread differently for 1, 3 and 8 lanes (8200 positions: through a
+    workspace), and over one query and several: the same bits."""
+    w, L, steps = syn.WORKLOADS["prefill407m"], 2, 2
+    H, hd = w.shape.n_heads, w.shape.head_dim
+    m = device_model("prefill407m", max_tokens=16, max_lanes=8, max_ctx=ctx)
+    pos = [ctx - 9, 7, ctx // 2, 129, 0, ctx - steps, 64, 31]
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(5)
+    codes = torch.randint(-2 ** 31, 2 ** 31 - 1, (2, H, ctx, hd // 8), dtype=torch.int32, device="cuda", generator=gen)
+    scale = 0.2 * torch.rand(2, H, ctx, hd // 32, device="cuda", generator=gen)
+    params = torch.stack((scale, torch.randn(scale.shape, device="cuda", generator=gen) - 7.5 * scale), -1).half()
+    ids = torch.from_numpy(syn.token_ids(8 * steps, 71, "int4.lanes").reshape(steps, 8)).cuda()
+
+    def new(lanes):
+        kv = m.new_kv([L] * len(lanes), max_ctx=ctx, dtype="int4")
+        for at, b in enumerate(lanes):
+            for layer in range(w.n_pre + L):
+                p = kv.layer_ptrs(at, layer)
+                for i in range(2):                     # lanes and layers differ by a rotation of the positions
+                    turn = 13 * b + 5 * layer
+                    _raw(kv, p[i], (H, ctx, hd // 8), torch.int32).copy_(codes[i].roll(turn, 1))
+                    _raw(kv, p[2 + i], (H, ctx, hd // 32, 2), torch.float16).copy_(params[i].roll(turn, 1))
+            kv.set_position(at, pos[b])
+        return kv
+
+    def run(lanes):
+        kv = new(lanes)
+        ys = [m.decode(kv, ids[s][lanes].contiguous(), L_per_lane=[L] * len(lanes)).cpu().numpy() for s in range(steps)]
+        kv.close()
+        return np.stack(ys, 1)
+    batch = run(list(range(8)))
+    assert np.isfinite(batch).all()
+    for lanes in ([0], [2], [5], [4], [0, 5, 2]):
+        assert np.array_equal(run(lanes), batch[lanes]), lanes
+    a, b = new([0]), new([0])
+    x = ids.flatten()[:8].contiguous()
+    together = m.extend(a, x, lane=0, L=L).cpu().numpy()
+    alone = np.concatenate([m.extend(b, x[i:i + 1], lane=0, L=L).cpu().numpy() for i in range(8)])
+    assert np.array_equal(together, alone)
+    a.close()
+    b.close()
+    m.close()
+
+
 @pytest.mark.parametrize("start", [0, 1, 13, 16, 60])
 def test_extend_equals_decode_steps(start):
     n, L = 8, 2

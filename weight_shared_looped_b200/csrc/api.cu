@@ -287,10 +287,17 @@ tl_status check_attn4(const tl_kv_int4* cache, int n_q, int q_heads) {
   return ok();
 }
 
-// the units the work split of a caller's attention is chosen for
-int attn4_pairs(const tl_kv_int4* c, int n_q, int q_heads) {
-  const long cols = (long)n_q * (q_heads / c->n_heads);
-  return (int)std::min<long>((long)c->n_lanes * c->n_heads * ((cols + 7) / 8), 1 << 20);
+// the arguments that set the work split of a caller's attention
+AttnInt4Args attn4_sizes(const tl_kv_int4* c, int n_q, int q_heads) {
+  AttnInt4Args a;
+  memset(&a, 0, sizeof(a));
+  a.n_rows = c->n_lanes;
+  a.n_q = n_q;
+  a.H = c->n_heads;
+  a.group = q_heads / c->n_heads;
+  a.hd = c->head_dim;
+  a.max_ctx = c->max_ctx;
+  return a;
 }
 
 }  // namespace
@@ -298,11 +305,7 @@ int attn4_pairs(const tl_kv_int4* c, int n_q, int q_heads) {
 TL_API tl_status tl_attention_int4_workspace_bytes(const tl_kv_int4* cache, int n_q, int q_heads, size_t* bytes) {
   TL_CHECK_ARG(bytes, "bytes is NULL");
   TL_TRY(check_attn4(cache, n_q, q_heads));
-  *bytes = n_q == 0 || cache->n_lanes == 0
-               ? 0
-               : attn_int4_workspace(cache->n_lanes, cache->n_heads, cache->head_dim,
-                                     n_q * (q_heads / cache->n_heads), cache->max_ctx,
-                                     attn4_pairs(cache, n_q, q_heads));
+  *bytes = n_q == 0 || cache->n_lanes == 0 ? 0 : attn_int4_workspace(attn4_sizes(cache, n_q, q_heads));
   return ok();
 }
 
@@ -319,9 +322,7 @@ TL_API tl_status tl_attention_int4(const tl_kv_int4* cache, const uint16_t* q, l
   TL_CHECK_ARG(q && out && lens, "NULL device pointer");
   TL_CHECK_ARG((((uintptr_t)q | (uintptr_t)out) & 15) == 0, "q and out must be 16-byte aligned");
   TL_CHECK_ARG(((uintptr_t)lens & 3) == 0, "lens must be 4-byte aligned");
-  AttnInt4Args a;
-  memset(&a, 0, sizeof(a));
-  a.split_pairs = attn4_pairs(cache, n_q, q_heads);
+  AttnInt4Args a = attn4_sizes(cache, n_q, q_heads);
   if (cache->max_ctx >= kInt4SplitCtx) {
     size_t need;
     TL_TRY(tl_attention_int4_workspace_bytes(cache, n_q, q_heads, &need));
@@ -333,12 +334,6 @@ TL_API tl_status tl_attention_int4(const tl_kv_int4* cache, const uint16_t* q, l
   a.out = (__half*)out;
   a.q_stride = q_stride;
   a.out_stride = out_stride;
-  a.n_rows = cache->n_lanes;
-  a.n_q = n_q;
-  a.H = cache->n_heads;
-  a.group = q_heads / cache->n_heads;
-  a.hd = cache->head_dim;
-  a.max_ctx = cache->max_ctx;
   a.window = window > cache->max_ctx ? 0 : window;   // at least the whole context
   a.k_codes = cache->k_codes;
   a.v_codes = cache->v_codes;
@@ -762,13 +757,18 @@ size_t h_workspace_bytes(const tl_model* m, int n_lanes, int max_ctx, size_t* la
   return *part_off + align256(part * 2 * m->d * sizeof(float));
 }
 
-// 4-bit caches: the units the attention's split is chosen for.  A lane's split must
-// not depend on how many lanes run, so it is that of four lanes.
-int int4_split_pairs(const tl_model* m) { return 4 * m->H; }
-
-// The attention's workspace for up to 8 rows (decode) or 8 queries of a row (extend).
+// 4-bit caches: the attention's workspace for up to 8 rows (decode) or 8 queries of a
+// row (extend).
 size_t int4_workspace_bytes(const tl_model* m, int max_ctx) {
-  return align256(attn_int4_workspace(kMaxLanes, m->H, m->hd, 1, max_ctx, int4_split_pairs(m)));
+  AttnInt4Args a;
+  memset(&a, 0, sizeof(a));
+  a.n_rows = kMaxLanes;
+  a.n_q = a.group = 1;
+  a.H = m->H;
+  a.hd = m->hd;
+  a.max_ctx = max_ctx;
+  a.lane_split = true;
+  return align256(attn_int4_workspace(a));
 }
 
 bool known_kv_dtype(int dtype) {
@@ -1201,7 +1201,7 @@ tl_status enqueue_int4_attention(tl_model* m, int layer, int rows, tl_kv* kv, co
     a.row_lane[i] = rm->lane[i];
     a.row_cum[i] = rm->cum[i];
   }
-  a.split_pairs = int4_split_pairs(m);
+  a.lane_split = true;
   a.ws = kv->int4_ws;
   return launch_attn_int4(a, s);
 }

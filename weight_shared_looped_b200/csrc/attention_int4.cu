@@ -55,10 +55,11 @@ namespace {
 
 constexpr int A4_COLS = 8;          // queries per CTA (MMA N)
 constexpr int A4_TILE = 32;         // keys per warp tile: two sub-tiles of 16 (MMA M)
-constexpr int A4_WARPS = 4;          // warps per CTA
-constexpr int A4_MINB = 4;           // CTAs per SM
+constexpr int A4_GROUP = 4;          // slots whose records are joined first
+constexpr int A4_WIDE = 12;          // warps of a CTA that has an SM to itself; others have 4
 constexpr int A4_MAX_CLUSTER = 8;
 constexpr int A4_MAX_SPLIT = 64;
+constexpr int A4_MAX_SMEM = 227 * 1024;
 constexpr int A4_STAGES = 2;         // tiles of a warp's ring
 constexpr float A4_SLACK = 8.f;     // the running maximum may lag by 2^8
 constexpr float A4_NONE = -1e30f;   // below every score: no key yet
@@ -147,12 +148,11 @@ __device__ __forceinline__ void a4_copy4(uint32_t* dst, const uint32_t* src) {
                : "memory");
 }
 
-template <int HD>
-__global__ void __launch_bounds__(32 * A4_WARPS, A4_MINB) attn_int4_kernel(AttnInt4Args a) {
+template <int HD, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS, WARPS == A4_WIDE ? 1 : 4) attn_int4_kernel(AttnInt4Args a) {
   using C = A4<HD>;
   pdl_enter();
   extern __shared__ __align__(128) float a4_smem[];
-  constexpr int nw = A4_WARPS;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const int cls = gridDim.x, rank = blockIdx.x;
@@ -207,21 +207,21 @@ __global__ void __launch_bounds__(32 * A4_WARPS, A4_MINB) attn_int4_kernel(AttnI
     }
   }
   const float csc = rsqrtf((float)HD) * 1.4426950408889634f;   // 1/sqrt(hd) in base 2
-  float m[2] = {A4_NONE, A4_NONE}, l[2] = {0.f, 0.f};
-  float o[C::MT][4];
-#pragma unroll
-  for (int i = 0; i < C::MT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+  float m[2], l[2], o[C::MT][4];
 
   // MMA row r stands for key kr(r) of the tile: a lane's V pairs are then the keys
   // kr(2t), kr(2t + 1) and those + 8, and the reads of a quarter (half) warp fall on
   // distinct banks
   const int kr = g ^ ((g >> 1) & 1);
   const int vk[4] = {2 * t ^ (t & 1), (2 * t + 1) ^ (t & 1), (2 * t ^ (t & 1)) + 8, ((2 * t + 1) ^ (t & 1)) + 8};
-  const int slots = cls * nw;
-  const int slot = rank * nw + warp;
+  // slot s takes tiles s, s + slots, ..; this warp takes `passes` slots in turn
+  const int passes = WARPS == A4_WIDE ? a.passes : 1;
+  const int stride = cls * WARPS, slots = stride * passes;
   const int tile_lo = lo_all / A4_TILE;
   const int tile_hi = hi_all < 0 ? -1 : hi_all / A4_TILE;      // last tile with a key
-  int tile = tile_lo + (slot - tile_lo % slots + slots) % slots;
+  auto first_tile = [&](int pass) {
+    return tile_lo + (pass * stride + rank * WARPS + warp - tile_lo % slots + slots) % slots;
+  };
   uint32_t* ring = reinterpret_cast<uint32_t*>(a4_smem) + (size_t)warp * A4_STAGES * C::WORDS;
   // head_dim 64 with an odd max_ctx, or a caller's strides, leave parameters on 4 bytes
   const bool par16 = (((uintptr_t)kp | (uintptr_t)vp) & 15) == 0;
@@ -307,8 +307,21 @@ __global__ void __launch_bounds__(32 * A4_WARPS, A4_MINB) attn_int4_kernel(AttnI
     }
   };
 
-  int ahead = tile, in_slot = 0, out_slot = 0;
+  // records of the slots [passes][WARPS][cols][HD] (over the rings when there is one
+  // pass), their maxima and sums, the groups', the CTA's record
+  const int my_slots = passes * WARPS, my_groups = my_slots / A4_GROUP, elems = cols * HD;
+  float* rec = a4_smem + (passes > 1 ? WARPS * A4_STAGES * C::WORDS : 0);
+  float* rm = rec + (size_t)my_slots * elems;
+  float* rl = rm + my_slots * cols;
+  float* gm = rl + my_slots * cols;
+  float* gl = gm + my_groups * cols;
+  float* go = gl + my_groups * cols;
+  float* cm = go + elems;
+  float* cl = cm + cols;
+
+  int pass = 0, tile = first_tile(0), ahead_pass = 0, ahead = tile, in_slot = 0, out_slot = 0;
   auto request = [&]() {                           // one group per tile, empty behind the last
+    while (ahead > tile_hi && ahead_pass + 1 < passes) ahead = first_tile(++ahead_pass);
     if (ahead <= tile_hi) fetch(ahead, in_slot);
     asm volatile("cp.async.commit_group;" ::: "memory");
     ahead += slots;
@@ -317,182 +330,234 @@ __global__ void __launch_bounds__(32 * A4_WARPS, A4_MINB) attn_int4_kernel(AttnI
 #pragma unroll
   for (int i = 0; i < A4_STAGES - 1; ++i) request();
 #pragma unroll 1
-  for (; tile <= tile_hi; tile += slots) {
-    asm volatile("cp.async.wait_group %0;" ::"n"(A4_STAGES - 2) : "memory");
-    __syncwarp();                                  // every lane's copies of this tile; the slot before is free
-    request();
-    const uint32_t* tw = ring + out_slot * C::WORDS;
-    out_slot = out_slot + 1 == A4_STAGES ? 0 : out_slot + 1;
-    // S^T = K q^T: lane (g, t) gets keys kr and kr + 8 of each sub-tile, columns 2t and 2t + 1
-    float s[2][4];
+  while (true) {
+    m[0] = m[1] = A4_NONE;
+    l[0] = l[1] = 0.f;
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      s[u][0] = s[u][1] = s[u][2] = s[u][3] = 0.f;
-      const int r0 = 16 * u + kr, r1 = r0 + 8;
-      uint32_t k0[C::KW], k1[C::KW];
-      a4_lds<C::KW>(k0, tw + r0 * C::RW + C::KW * t);
-      a4_lds<C::KW>(k1, tw + r1 * C::RW + C::KW * t);
-      const __half2 p0 = kv_bits_h2(tw[C::KP0 + r0 * C::RP + (HD == 128 ? t : t >> 1)]);
-      const __half2 p1 = kv_bits_h2(tw[C::KP0 + r1 * C::RP + (HD == 128 ? t : t >> 1)]);
-      const __half2 s0 = __low2half2(p0), z0 = __high2half2(p0), s1 = __low2half2(p1), z1 = __high2half2(p1);
+    for (int i = 0; i < C::MT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+#pragma unroll 1
+    for (; tile <= tile_hi; tile += slots) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(A4_STAGES - 2) : "memory");
+      __syncwarp();                                  // every lane's copies of this tile; the slot before is free
+      request();
+      const uint32_t* tw = ring + out_slot * C::WORDS;
+      out_slot = out_slot + 1 == A4_STAGES ? 0 : out_slot + 1;
+      // S^T = K q^T: lane (g, t) gets keys kr and kr + 8 of each sub-tile, columns 2t and 2t + 1
+      float s[2][4];
 #pragma unroll
-      for (int jj = 0; jj < C::KW; ++jj) {
-        uint32_t x0 = k0[jj], x1 = k1[jj];
+      for (int u = 0; u < 2; ++u) {
+        s[u][0] = s[u][1] = s[u][2] = s[u][3] = 0.f;
+        const int r0 = 16 * u + kr, r1 = r0 + 8;
+        uint32_t k0[C::KW], k1[C::KW];
+        a4_lds<C::KW>(k0, tw + r0 * C::RW + C::KW * t);
+        a4_lds<C::KW>(k1, tw + r1 * C::RW + C::KW * t);
+        const __half2 p0 = kv_bits_h2(tw[C::KP0 + r0 * C::RP + (HD == 128 ? t : t >> 1)]);
+        const __half2 p1 = kv_bits_h2(tw[C::KP0 + r1 * C::RP + (HD == 128 ? t : t >> 1)]);
+        const __half2 s0 = __low2half2(p0), z0 = __high2half2(p0), s1 = __low2half2(p1), z1 = __high2half2(p1);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t af[4];
-          af[0] = kv_h2_bits(__hfma2(kv_int4_pair<true>(x0), s0, z0));
-          af[1] = kv_h2_bits(__hfma2(kv_int4_pair<true>(x1), s1, z1));
-          af[2] = kv_h2_bits(__hfma2(kv_int4_pair<false>(x0), s0, z0));
-          af[3] = kv_h2_bits(__hfma2(kv_int4_pair<false>(x1), s1, z1));
-          a4_mma(s[u], af, qb[2 * jj + h][0], qb[2 * jj + h][1]);
-          if (h == 0) {
-            x0 >>= 8;
-            x1 >>= 8;
+        for (int jj = 0; jj < C::KW; ++jj) {
+          uint32_t x0 = k0[jj], x1 = k1[jj];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t af[4];
+            af[0] = kv_h2_bits(__hfma2(kv_int4_pair<true>(x0), s0, z0));
+            af[1] = kv_h2_bits(__hfma2(kv_int4_pair<true>(x1), s1, z1));
+            af[2] = kv_h2_bits(__hfma2(kv_int4_pair<false>(x0), s0, z0));
+            af[3] = kv_h2_bits(__hfma2(kv_int4_pair<false>(x1), s1, z1));
+            a4_mma(s[u], af, qb[2 * jj + h][0], qb[2 * jj + h][1]);
+            if (h == 0) {
+              x0 >>= 8;
+              x1 >>= 8;
+            }
           }
         }
       }
-    }
-    const int base = tile * A4_TILE;
-    const bool edge = base < full_lo || base + A4_TILE - 1 > full_hi;   // uniform over the warp
-    if (edge) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int hi = last_of(c0 + min(2 * t + (e & 1), cols - 1)), lo = first_of(hi);
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int key = base + 16 * u + kr + 8 * (e >> 1);
-          if (key > hi || key < lo) s[u][e] = -INFINITY;
-        }
-      }
-    }
-    const float mx0 = fmaxf(fmaxf(s[0][0], s[0][2]), fmaxf(s[1][0], s[1][2]));
-    const float mx1 = fmaxf(fmaxf(s[0][1], s[0][3]), fmaxf(s[1][1], s[1][3]));
-    if (__any_sync(0xffffffffu, mx0 * csc > m[0] + A4_SLACK || mx1 * csc > m[1] + A4_SLACK)) {
-      // raise the maxima that are due, each column by its own scores alone
-      float mx[2] = {mx0, mx1}, al[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-#pragma unroll
-        for (int w = 4; w < 32; w <<= 1) mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], w));
-        mx[e] *= csc;
-        const bool up = mx[e] > m[e] + A4_SLACK;
-        al[e] = up ? a4_ex2(m[e] - mx[e]) : 1.f;
-        if (up) m[e] = mx[e];
-        l[e] *= al[e];
-      }
-#pragma unroll
-      for (int i = 0; i < C::MT; ++i) {
-        o[i][0] *= al[0];
-        o[i][1] *= al[1];
-        o[i][2] *= al[0];
-        o[i][3] *= al[1];
-      }
-    }
-    // weights as fp16 (a rounding of 2^-11 each, of values the sum has in fp32),
-    // key pairs of column g
-    uint32_t pb[2][2];
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const float p0 = a4_ex2(fmaf(s[u][0], csc, -m[0])), p1 = a4_ex2(fmaf(s[u][1], csc, -m[1]));
-      const float p2 = a4_ex2(fmaf(s[u][2], csc, -m[0])), p3 = a4_ex2(fmaf(s[u][3], csc, -m[1]));
-      l[0] += p0 + p2;
-      l[1] += p1 + p3;
-      pb[u][0] = a4_transpose(a4_pack(p0, p1));
-      pb[u][1] = a4_transpose(a4_pack(p2, p3));
-    }
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      uint32_t prm[4];
-#pragma unroll
-      for (int h = 0; h < 4; ++h) prm[h] = tw[C::VP0 + (16 * u + vk[h]) * C::RP + (HD == 128 ? g >> 1 : g >> 2)];
-      // keys that no query sees may hold anything: they count as zero
-      bool odd = false;
+      const int base = tile * A4_TILE;
+      const bool edge = base < full_lo || base + A4_TILE - 1 > full_hi;   // uniform over the warp
       if (edge) {
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {
-          const int key = base + 16 * u + vk[h];
-          if (key > hi_all || key < lo_all) prm[h] = 0u;
-          odd |= a4_odd(prm[h]);
+        for (int e = 0; e < 4; ++e) {
+          const int hi = last_of(c0 + min(2 * t + (e & 1), cols - 1)), lo = first_of(hi);
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const int key = base + 16 * u + kr + 8 * (e >> 1);
+            if (key > hi || key < lo) s[u][e] = -INFINITY;
+          }
         }
-        odd = __any_sync(0xffffffffu, odd);
       }
-      if (!odd) {
-        pv(tw, u, prm, pb[u][0], pb[u][1], -1);
-      } else {
-        // some value may not be finite and some query may not see it: column by
-        // column, the keys it does not see zeroed, the same arithmetic otherwise
-#pragma unroll 1
-        for (int c = 0; c < cols; ++c) {
-          uint32_t own[4];
-          const int hi = last_of(c0 + c), lo = first_of(hi);
+      const float mx0 = fmaxf(fmaxf(s[0][0], s[0][2]), fmaxf(s[1][0], s[1][2]));
+      const float mx1 = fmaxf(fmaxf(s[0][1], s[0][3]), fmaxf(s[1][1], s[1][3]));
+      if (__any_sync(0xffffffffu, mx0 * csc > m[0] + A4_SLACK || mx1 * csc > m[1] + A4_SLACK)) {
+        // raise the maxima that are due, each column by its own scores alone
+        float mx[2] = {mx0, mx1}, al[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+          for (int w = 4; w < 32; w <<= 1) mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], w));
+          mx[e] *= csc;
+          const bool up = mx[e] > m[e] + A4_SLACK;
+          al[e] = up ? a4_ex2(m[e] - mx[e]) : 1.f;
+          if (up) m[e] = mx[e];
+          l[e] *= al[e];
+        }
+#pragma unroll
+        for (int i = 0; i < C::MT; ++i) {
+          o[i][0] *= al[0];
+          o[i][1] *= al[1];
+          o[i][2] *= al[0];
+          o[i][3] *= al[1];
+        }
+      }
+      // weights as fp16 (a rounding of 2^-11 each, of values the sum has in fp32),
+      // key pairs of column g
+      uint32_t pb[2][2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const float p0 = a4_ex2(fmaf(s[u][0], csc, -m[0])), p1 = a4_ex2(fmaf(s[u][1], csc, -m[1]));
+        const float p2 = a4_ex2(fmaf(s[u][2], csc, -m[0])), p3 = a4_ex2(fmaf(s[u][3], csc, -m[1]));
+        l[0] += p0 + p2;
+        l[1] += p1 + p3;
+        pb[u][0] = a4_transpose(a4_pack(p0, p1));
+        pb[u][1] = a4_transpose(a4_pack(p2, p3));
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        uint32_t prm[4];
+#pragma unroll
+        for (int h = 0; h < 4; ++h) prm[h] = tw[C::VP0 + (16 * u + vk[h]) * C::RP + (HD == 128 ? g >> 1 : g >> 2)];
+        // keys that no query sees may hold anything: they count as zero
+        bool odd = false;
+        if (edge) {
 #pragma unroll
           for (int h = 0; h < 4; ++h) {
             const int key = base + 16 * u + vk[h];
-            own[h] = key <= hi && key >= lo ? prm[h] : 0u;
+            if (key > hi_all || key < lo_all) prm[h] = 0u;
+            odd |= a4_odd(prm[h]);
           }
-          pv(tw, u, own, pb[u][0], pb[u][1], c);
+          odd = __any_sync(0xffffffffu, odd);
+        }
+        if (!odd) {
+          pv(tw, u, prm, pb[u][0], pb[u][1], -1);
+        } else {
+          // some value may not be finite and some query may not see it: column by
+          // column, the keys it does not see zeroed, the same arithmetic otherwise
+#pragma unroll 1
+          for (int c = 0; c < cols; ++c) {
+            uint32_t own[4];
+            const int hi = last_of(c0 + c), lo = first_of(hi);
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+              const int key = base + 16 * u + vk[h];
+              own[h] = key <= hi && key >= lo ? prm[h] : 0u;
+            }
+            pv(tw, u, own, pb[u][0], pb[u][1], c);
+          }
         }
       }
     }
+    if (passes == 1) __syncthreads();              // the rings' memory holds the records from here on
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+#pragma unroll
+      for (int w = 4; w < 32; w <<= 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], w);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int c = 2 * t + e;
+      if (c < cols) {
+        const int r = (pass * WARPS + warp) * cols + c;
+        float* dst = rec + (size_t)r * HD + (HD / 8) * g;
+#pragma unroll
+        for (int i = 0; i < C::MT; ++i) *reinterpret_cast<float2*>(dst + 2 * i) = make_float2(o[i][e], o[i][e + 2]);
+        if (g == 0) {
+          rm[r] = m[e];
+          rl[r] = l[e];
+        }
+      }
+    }
+    if (++pass == passes) break;
+    tile = first_tile(pass);
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
-  __syncthreads();                                 // the rings' memory holds the merge from here on
-
-  // ---- merge: warps (in warp order), then the cluster's CTAs (in rank order)
-#pragma unroll
-  for (int e = 0; e < 2; ++e)
-#pragma unroll
-    for (int w = 4; w < 32; w <<= 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], w);
-  // per warp [cols][HD], then per warp [cols] maxima and sums
-  float* wo = a4_smem;
-  float* wm = wo + (size_t)nw * cols * HD;
-  float* wl = wm + nw * A4_COLS;
-  float* go = wl + nw * A4_COLS;          // the CTA's record: [cols][HD], maxima, sums
-  float* gm = go + cols * HD;
-  float* gl = gm + A4_COLS;
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const int c = 2 * t + e;
-    if (c < cols) {
-      float* dst = wo + (size_t)(warp * cols + c) * HD + (HD / 8) * g;
-#pragma unroll
-      for (int i = 0; i < C::MT; ++i) *reinterpret_cast<float2*>(dst + 2 * i) = make_float2(o[i][e], o[i][e + 2]);
-      if (g == 0) {
-        wm[warp * A4_COLS + c] = m[e];
-        wl[warp * A4_COLS + c] = l[e];
-      }
-    }
-  }
   __syncthreads();
-  for (int i = threadIdx.x; i < cols * HD; i += blockDim.x) {
+
+  // ---- join: the slots of a group in their order, the groups, the cluster's CTAs.
+  // The join of one record has its bits, so a group per CTA and all groups in one CTA
+  // give the same.
+  auto group_record = [&](int r0, int i, float* M, float* acc, float* L) {
     const int c = i / HD;
-    float M = A4_NONE;
-    for (int w = 0; w < nw; ++w) M = fmaxf(M, wm[w * A4_COLS + c]);
-    float acc = 0.f, L = 0.f;
-    for (int w = 0; w < nw; ++w) {
-      const float f = exp2f(wm[w * A4_COLS + c] - M);
-      acc = fmaf(wo[(size_t)w * cols * HD + i], f, acc);
-      L = fmaf(wl[w * A4_COLS + c], f, L);
+    *M = A4_NONE;
+    *acc = *L = 0.f;
+#pragma unroll
+    for (int w = 0; w < A4_GROUP; ++w) *M = fmaxf(*M, rm[(r0 + w) * cols + c]);
+#pragma unroll
+    for (int w = 0; w < A4_GROUP; ++w) {
+      const float f = exp2f(rm[(r0 + w) * cols + c] - *M);
+      *acc = fmaf(rec[(size_t)(r0 + w) * elems + i], f, *acc);
+      *L = fmaf(rl[(r0 + w) * cols + c], f, *L);
     }
-    if (cls == 1) {
-      const int cc = c0 + c, qi = cc / a.group, hq = head * a.group + cc % a.group;
-      a.out[(size_t)(row * a.n_q + qi) * a.out_stride + (size_t)hq * HD + i % HD] =
-          __float2half_rn(L == 0.f ? 0.f : acc / L);
-    } else if (a.ws != nullptr) {
-      // a split beyond a cluster: the record goes to the merge kernel
-      float* rec = a.ws + (((size_t)row * gridDim.y + blockIdx.y) * cls + rank) * (A4_COLS * (HD + 2));
-      rec[i] = acc;
-      if (i % HD == 0) {
-        rec[A4_COLS * HD + c] = M;
-        rec[A4_COLS * HD + A4_COLS + c] = L;
+  };
+  auto to_output = [&](int i, float acc, float L) {
+    const int cc = c0 + i / HD, qi = cc / a.group, hq = head * a.group + cc % a.group;
+    a.out[(size_t)(row * a.n_q + qi) * a.out_stride + (size_t)hq * HD + i % HD] =
+        __float2half_rn(L == 0.f ? 0.f : acc / L);
+  };
+  // a split beyond a cluster: record `all` of `of` goes to the merge kernel
+  auto to_workspace = [&](int all, int of, int i, float M, float acc, float L) {
+    const int c = i / HD;
+    float* to = a.ws + (((size_t)row * gridDim.y + blockIdx.y) * of + all) * (A4_COLS * (HD + 2));
+    to[i] = acc;
+    if (i % HD == 0) {
+      to[A4_COLS * HD + c] = M;
+      to[A4_COLS * HD + A4_COLS + c] = L;
+    }
+  };
+  auto to_cluster = [&](int i, float M, float acc, float L) {
+    go[i] = acc;
+    if (i % HD == 0) {
+      cm[i / HD] = M;
+      cl[i / HD] = L;
+    }
+  };
+  if constexpr (WARPS == A4_GROUP) {
+    for (int i = threadIdx.x; i < elems; i += blockDim.x) {
+      float M, acc, L;
+      group_record(0, i, &M, &acc, &L);
+      if (cls == 1) to_output(i, acc, L);
+      else if (a.ws != nullptr) to_workspace(rank, cls, i, M, acc, L);
+      else to_cluster(i, M, acc, L);
+    }
+  } else {
+    constexpr int WG = WARPS / A4_GROUP;           // groups of a pass
+    for (int gg = warp / A4_GROUP; gg < my_groups; gg += WG) {
+      for (int i = threadIdx.x % (32 * A4_GROUP); i < elems; i += 32 * A4_GROUP) {
+        float M, acc, L;
+        group_record(gg * A4_GROUP, i, &M, &acc, &L);
+        if (a.ws != nullptr) {
+          to_workspace(gg / WG * (cls * WG) + rank * WG + gg % WG, cls * my_groups, i, M, acc, L);
+          continue;
+        }
+        rec[(size_t)gg * A4_GROUP * elems + i] = acc;   // over the group's first, which this thread alone reads
+        if (i % HD == 0) {
+          gm[gg * cols + i / HD] = M;
+          gl[gg * cols + i / HD] = L;
+        }
       }
-    } else {
-      go[i] = acc;
-      if (i % HD == 0) {
-        gm[c] = M;
-        gl[c] = L;
+    }
+    if (a.ws != nullptr) return;
+    __syncthreads();
+    for (int i = threadIdx.x; i < elems; i += blockDim.x) {
+      const int c = i / HD;
+      float M = A4_NONE, acc = 0.f, L = 0.f;
+#pragma unroll 3
+      for (int gg = 0; gg < my_groups; ++gg) M = fmaxf(M, gm[gg * cols + c]);
+#pragma unroll 3
+      for (int gg = 0; gg < my_groups; ++gg) {
+        const float f = exp2f(gm[gg * cols + c] - M);
+        acc = fmaf(rec[(size_t)gg * A4_GROUP * elems + i], f, acc);
+        L = fmaf(gl[gg * cols + c], f, L);
       }
+      if (cls == 1) to_output(i, acc, L);
+      else to_cluster(i, M, acc, L);
     }
   }
   if (cls == 1 || a.ws != nullptr) return;
@@ -508,8 +573,8 @@ __global__ void __launch_bounds__(32 * A4_WARPS, A4_MINB) attn_int4_kernel(AttnI
 #pragma unroll
     for (int r = 0; r < A4_MAX_CLUSTER; ++r) {
       if (r < cls) {
-        mr[r] = a4_remote(gm + c, r);
-        lr[r] = a4_remote(gl + c, r);
+        mr[r] = a4_remote(cm + c, r);
+        lr[r] = a4_remote(cl + c, r);
         ar[r] = a4_remote(go + i, r);
       }
     }
@@ -525,9 +590,7 @@ __global__ void __launch_bounds__(32 * A4_WARPS, A4_MINB) attn_int4_kernel(AttnI
         L = fmaf(lr[r], f, L);
       }
     }
-    const int cc = c0 + c, qi = cc / a.group, hq = head * a.group + cc % a.group;
-    a.out[(size_t)(row * a.n_q + qi) * a.out_stride + (size_t)hq * HD + i % HD] =
-        __float2half_rn(L == 0.f ? 0.f : acc / L);
+    to_output(i, acc, L);
   }
   a4_cluster_sync();   // no CTA leaves while another reads its shared memory
 }
@@ -586,60 +649,109 @@ __global__ void __launch_bounds__(2 * HD) attn_int4_merge_kernel(AttnInt4Args a,
   }
 }
 
+// How the launch is cut up: CTAs per (row, cache head, column tile), their warps, the
+// slots a warp takes in turn, and the records that go through the workspace.
+struct A4Split {
+  int ctas, warps, passes, records;
+};
+
 template <int HD>
-size_t a4_smem_bytes() {
-  const size_t ring = (size_t)A4_WARPS * A4_STAGES * A4<HD>::WORDS * 4;
-  const size_t merge =
-      ((size_t)(A4_WARPS + 1) * A4_COLS * HD + 2 * (size_t)(A4_WARPS + 1) * A4_COLS) * sizeof(float);
-  return std::max(ring, merge);
+size_t a4_smem_bytes(const A4Split& p, int cols) {
+  const size_t slots = (size_t)p.warps * p.passes, c = std::min(cols, A4_COLS);
+  const size_t ring = (size_t)p.warps * A4_STAGES * A4<HD>::WORDS * 4;
+  const size_t records = (slots * (HD + 2) + slots / A4_GROUP * 2 + HD + 2) * c * sizeof(float);
+  return p.passes > 1 ? ring + records : std::max(ring, records);
 }
 
-// CTAs per (row, cache head, column tile) for `pairs` of those over a cache of
-// max_ctx positions, and whether they merge in a cluster or through the workspace.
-int a4_split(int max_ctx, int pairs, bool* through_ws) {
+// The split of a caller's attention, for n (row, cache head, column tile) units.
+//
+// One CTA of 12 warps per SM leaves a cluster's join out, or needs one of two CTAs only.
+// 16 heads of 128, us with four warps (as many CTAs as are resident) and with 12:  4
+// lanes of 2112 positions 11.5 and 10.2; 8 lanes of 512 positions 7.7 and 6.5, of 2112
+// 16.0 and 13.7, of 4200 26.8 and 23.2; two lanes 8.6 and (three CTAs) 8.3, 16 lanes 25.5
+// and (two rounds of CTAs) 26.2.
+//
+// Four warps: four CTAs per SM.  More than a cluster's eight cost a second launch and a
+// workspace: one lane of 16 heads takes 12.3 us in a cluster and 10.3 through the
+// workspace at 4096 positions (12.3 and 13.3 with two lanes), 16.4 and 13.2 at 8192.
+A4Split a4_split(int max_ctx, long n) {
   const int tiles = (max_ctx + A4_TILE - 1) / A4_TILE;
-  // as many CTAs as fill the GPU once (four per SM), a tile per warp at least.  More
-  // than a cluster's eight cost a second launch and a workspace: one lane of 16
-  // heads takes 12.3 us in a cluster and 10.3 through the workspace at 4096
-  // positions (12.3 and 13.3 with two lanes), 16.4 and 13.2 at 8192
-  int c = std::min((tiles + A4_WARPS - 1) / A4_WARPS, std::max(1, 148 * 4 / pairs));
-  *through_ws = max_ctx >= kInt4SplitCtx && c > A4_MAX_CLUSTER;
-  if (*through_ws) return std::min(c, A4_MAX_SPLIT);
-  return std::min(c, A4_MAX_CLUSTER);
+  if (n > 37 && n <= 148 && tiles > A4_GROUP)
+    return {std::min((tiles + A4_WIDE - 1) / A4_WIDE, n <= 74 ? 2 : 1), A4_WIDE, 1, 0};
+  const int c = (int)std::min<long>((tiles + A4_GROUP - 1) / A4_GROUP, std::max(1L, 148 * 4 / n));
+  if (max_ctx < kInt4SplitCtx || c <= A4_MAX_CLUSTER) return {std::min(c, A4_MAX_CLUSTER), A4_GROUP, 1, 0};
+  return {std::min(c, A4_MAX_SPLIT), A4_GROUP, 1, std::min(c, A4_MAX_SPLIT)};
+}
+
+// The split of a model's attention, whose results must not depend on how many lanes
+// run: the groups of four slots, and the way they are joined, follow from max_ctx.
+// Below kInt4SplitCtx six groups, in a CTA each or all in one; from there on 24,
+// through the workspace.
+template <int HD>
+A4Split a4_lane_split(int max_ctx, long n, int cols) {
+  const int tiles = (max_ctx + A4_TILE - 1) / A4_TILE;
+  constexpr int wide = A4_WIDE / A4_GROUP;
+  if (max_ctx < kInt4SplitCtx) {
+    const int groups = std::min((tiles + A4_GROUP - 1) / A4_GROUP, 2 * wide);
+    if (n > 74 && groups == 2 * wide) return {1, A4_WIDE, 2, 0};
+    return {groups, A4_GROUP, 1, 0};
+  }
+  constexpr int groups = 8 * wide;
+  if (n * groups <= 148 * 4) return {groups, A4_GROUP, 1, groups};
+  A4Split p = {8, A4_WIDE, 1, groups};
+  while (p.ctas > 1 && n * p.ctas > 148) {
+    const A4Split q = {p.ctas / 2, A4_WIDE, p.passes * 2, groups};
+    if (a4_smem_bytes<HD>(q, cols) > A4_MAX_SMEM) break;
+    p = q;
+  }
+  return p;
+}
+
+template <int HD, int WARPS>
+tl_status launch_a4_warps(const AttnInt4Args& a, const A4Split& p, size_t smem, cudaStream_t s) {
+  static std::atomic<uint64_t> attr_done{0};
+  TL_TRY(once_per_device(attr_done, []() -> tl_status {
+    TL_CUDA(cudaFuncSetAttribute(attn_int4_kernel<HD, WARPS>, cudaFuncAttributeMaxDynamicSharedMemorySize, A4_MAX_SMEM));
+    return ok();
+  }));
+  const dim3 grid(p.ctas, a.H * a.col_tiles, a.n_rows);
+  const cudaError_t e = launch_pdl_cluster(attn_int4_kernel<HD, WARPS>, grid, dim3(32 * WARPS), smem, s,
+                                           p.records ? 1u : (unsigned)p.ctas, a);
+  if (e != cudaSuccess)
+    return set_error(TL_ERR_CUDA, "launch of attn_int4_kernel failed: %s", cudaGetErrorString(e));
+  return ok();
+}
+
+template <int HD>
+A4Split a4_split_of(const AttnInt4Args& a, int cols) {
+  const long n = (long)a.n_rows * a.H * ((cols + A4_COLS - 1) / A4_COLS);
+  return a.lane_split ? a4_lane_split<HD>(a.max_ctx, n, cols) : a4_split(a.max_ctx, n);
 }
 
 template <int HD>
 tl_status launch_a4(const AttnInt4Args& a0, cudaStream_t s) {
-  static std::atomic<uint64_t> attr_done{0};
-  TL_TRY(once_per_device(attr_done, []() -> tl_status {
-    TL_CUDA(cudaFuncSetAttribute(attn_int4_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)a4_smem_bytes<HD>()));
-    return ok();
-  }));
   AttnInt4Args a = a0;
-  a.col_tiles = (a.n_q * a.group + A4_COLS - 1) / A4_COLS;
-  bool through_ws;
-  const int c = a4_split(a.max_ctx, a.split_pairs, &through_ws);
-  if (!through_ws) a.ws = nullptr;
+  const int cols = a.n_q * a.group;
+  a.col_tiles = (cols + A4_COLS - 1) / A4_COLS;
+  const A4Split p = a4_split_of<HD>(a, cols);
+  a.passes = p.passes;
+  if (!p.records) a.ws = nullptr;
   else if (!a.ws) return set_error(TL_ERR_INVALID_ARG, "4-bit attention: a context of %d needs a workspace", a.max_ctx);
-  const dim3 grid(c, a.H * a.col_tiles, a.n_rows);
-  const cudaError_t e = launch_pdl_cluster(attn_int4_kernel<HD>, grid, dim3(32 * A4_WARPS), a4_smem_bytes<HD>(), s,
-                                           through_ws ? 1u : (unsigned)c, a);
-  if (e != cudaSuccess)
-    return set_error(TL_ERR_CUDA, "launch of attn_int4_kernel failed: %s", cudaGetErrorString(e));
-  if (through_ws)
-    TL_LAUNCH_PDL(attn_int4_merge_kernel<HD>, dim3(a.H * a.n_q * a.group, a.n_rows), 2 * HD, 0, s, a, c);
+  const size_t smem = a4_smem_bytes<HD>(p, cols);
+  if (p.warps == A4_WIDE) TL_TRY((launch_a4_warps<HD, A4_WIDE>(a, p, smem, s)));
+  else TL_TRY((launch_a4_warps<HD, A4_GROUP>(a, p, smem, s)));
+  if (p.records)
+    TL_LAUNCH_PDL(attn_int4_merge_kernel<HD>, dim3(a.H * cols, a.n_rows), 2 * HD, 0, s, a, p.records);
   return ok();
 }
 
 }  // namespace
 
-// Workspace of a call: n_rows rows of n_q * group queries per cache head.
-size_t attn_int4_workspace(int n_rows, int H, int hd, int cols, int max_ctx, int split_pairs) {
-  bool through_ws;
-  const int c = a4_split(max_ctx, split_pairs, &through_ws);
-  if (!through_ws) return 0;
-  return (size_t)n_rows * H * ((cols + A4_COLS - 1) / A4_COLS) * c * A4_COLS * (hd + 2) * sizeof(float);
+// Workspace of a call with these sizes (the arguments that set the split).
+size_t attn_int4_workspace(const AttnInt4Args& a) {
+  const int cols = a.n_q * a.group;
+  const A4Split p = a.hd == 128 ? a4_split_of<128>(a, cols) : a4_split_of<64>(a, cols);
+  return (size_t)a.n_rows * a.H * ((cols + A4_COLS - 1) / A4_COLS) * p.records * A4_COLS * (a.hd + 2) * sizeof(float);
 }
 
 tl_status launch_attn_int4(const AttnInt4Args& a, cudaStream_t s) {

@@ -299,12 +299,12 @@ struct AttnInt4Args {
   size_t layer_bytes, region_bytes;
   int layer;
   int row_lane[kMaxLanes], row_cum[kMaxLanes];
-  int split_pairs;                 // (lane, cache head, 8 queries) units the work split is chosen for
+  bool lane_split;                 // a lane's bits must not depend on n_rows
   float* ws;                       // attn_int4_workspace bytes; null where that is 0
-  int col_tiles;                   // set by the launcher
+  int col_tiles, passes;           // set by the launcher
 };
 constexpr int kInt4SplitCtx = 8192;   // caches below this many positions need no workspace
-size_t attn_int4_workspace(int n_rows, int H, int hd, int cols, int max_ctx, int split_pairs);
+size_t attn_int4_workspace(const AttnInt4Args& a);
 tl_status launch_attn_int4(const AttnInt4Args& a, cudaStream_t s);
 
 // scoring head (score_head.cu): log probabilities under logits y . E
