@@ -1155,32 +1155,34 @@ tl_status rebuild_kv(tl_model* m, const tl_block_desc& bd, int layer, int rows, 
   return ok();
 }
 
-// Decode attention of a 4-bit cache: RoPE and the append of every row's entry,
-// then the attention over the stored entries.  split_attn: the rows are
-// consecutive tokens of one lane, which its cache is read once for.
+// Decode attention of a 4-bit cache.  split_attn: the rows are consecutive tokens of
+// one lane, which its cache is read once for; RoPE and the append of all their
+// entries come first.  Otherwise the attention makes each row's entry itself.
 tl_status enqueue_int4_attention(tl_model* m, int layer, int rows, tl_kv* kv, const RowMap* rm,
                                  const int32_t* lane_of_row, bool split_attn, cudaStream_t s) {
-  RopeKvArgs r;
-  memset(&r, 0, sizeof(r));
-  r.part = m->part;
-  r.S = 1;
-  r.rows = rows;
-  r.d = m->d;
-  r.H = m->H;
-  r.hd = m->hd;
-  r.rope_cs = m->rope;
-  r.q = m->q;
-  r.kv_base = kv->buffer + kKvHeaderBytes;
-  r.hdr = (const KvHeader*)kv->buffer;
-  r.layer_bytes = kv->layer_bytes;
-  r.kv_region_bytes = kv->region_bytes;
-  r.layer = layer;
-  r.max_ctx = kv->max_ctx;
-  r.kv_int4 = 1;
-  r.lane_of_row = lane_of_row;
-  r.lane = rm->lane[0];
-  r.decode = split_attn ? 2 : 1;
-  TL_TRY(launch_rope_kv(r, s));
+  if (split_attn) {
+    RopeKvArgs r;
+    memset(&r, 0, sizeof(r));
+    r.part = m->part;
+    r.S = 1;
+    r.rows = rows;
+    r.d = m->d;
+    r.H = m->H;
+    r.hd = m->hd;
+    r.rope_cs = m->rope;
+    r.q = m->q;
+    r.kv_base = kv->buffer + kKvHeaderBytes;
+    r.hdr = (const KvHeader*)kv->buffer;
+    r.layer_bytes = kv->layer_bytes;
+    r.kv_region_bytes = kv->region_bytes;
+    r.layer = layer;
+    r.max_ctx = kv->max_ctx;
+    r.kv_int4 = 1;
+    r.lane_of_row = lane_of_row;
+    r.lane = rm->lane[0];
+    r.decode = 2;
+    TL_TRY(launch_rope_kv(r, s));
+  }
   AttnInt4Args a;
   memset(&a, 0, sizeof(a));
   a.q = m->q;
@@ -1192,14 +1194,18 @@ tl_status enqueue_int4_attention(tl_model* m, int layer, int rows, tl_kv* kv, co
   a.group = 1;
   a.hd = m->hd;
   a.max_ctx = kv->max_ctx;
-  a.hdr = r.hdr;
-  a.kv_base = r.kv_base;
+  a.hdr = (const KvHeader*)kv->buffer;
+  a.kv_base = kv->buffer + kKvHeaderBytes;
   a.layer_bytes = kv->layer_bytes;
   a.region_bytes = kv->region_bytes;
   a.layer = layer;
   for (int i = 0; i < kMaxLanes; ++i) {
     a.row_lane[i] = rm->lane[i];
     a.row_cum[i] = rm->cum[i];
+  }
+  if (!split_attn) {
+    a.qkv = m->part;
+    a.rope_cs = m->rope;
   }
   a.lane_split = true;
   a.ws = kv->int4_ws;

@@ -26,18 +26,21 @@
 // Two lanes of up to 65536 positions, 8 cache heads, 4 queries per head: 147 MB in
 // 41 us, 3.6 TB/s.  Many short lanes are bound by their launch, the merge and the tail.
 //
-// Work split: the context is cut into tiles of 32 keys; tile i belongs to warp
-// slot i mod (CTAs of the split x warps), whatever the lane's length, so the
-// work is even for every length and a query's arithmetic does not depend on
-// the other queries of its launch: a query alone and the same query among
-// several give the same bits.  Each warp keeps a running maximum and sum per
-// query (base 2); the maximum is raised only when a score exceeds it by more
-// than 2^8, which spares the cross-lane maximum on most tiles (weights stay
-// at or below 2^8, well inside fp16).  The warps merge in warp order through
-// shared memory, up to eight CTAs in rank order through distributed shared
-// memory, every CTA finishing its share of the outputs: one launch, no
-// workspace.  Longer contexts are split further (a4_split), their records joined
-// in order by a second launch.  The bits are the same at every run.
+// Work split: the context is cut into tiles of 32 keys; tile i belongs to slot i mod
+// slots, whatever the lane's length, so the work is even for every length and the
+// other queries of a launch do not change a query's arithmetic.  A warp takes a slot,
+// or some in turn, and keeps a running maximum and sum per query (base 2); the maximum
+// is raised only when a score exceeds it by more than 2^8, which spares the cross-lane
+// maximum on most tiles (weights stay at or below 2^8, well inside fp16).  The slots'
+// records are joined in a fixed order through shared memory, the CTAs of a cluster
+// through distributed shared memory, every CTA finishing its share of the outputs: one
+// launch, no workspace.  The longest contexts are split over more CTAs, whose records
+// a second launch joins.  The bits are the same at every run.
+//
+// A model's decode step makes its new entry here (FUSED): RoPE of q in every CTA, of k
+// in the one that reads the entry's tile, which quantises and appends it, while the
+// other tiles are on their way: a launch less per layer (one lane of 384 positions, 10
+// layer applications: 309 -> 284 us per step).
 //
 // Masked places never reach a sum: scores are selected, not multiplied, and
 // where a key's value is not finite and some query of the tile does not see
@@ -59,7 +62,7 @@ constexpr int A4_GROUP = 4;          // slots whose records are joined first
 constexpr int A4_WIDE = 12;          // warps of a CTA that has an SM to itself; others have 4
 constexpr int A4_MAX_CLUSTER = 8;
 constexpr int A4_MAX_SPLIT = 64;
-constexpr int A4_MAX_SMEM = 227 * 1024;
+constexpr int A4_MAX_SMEM = 226 * 1024;   // beside the static array
 constexpr int A4_STAGES = 2;         // tiles of a warp's ring
 constexpr float A4_SLACK = 8.f;     // the running maximum may lag by 2^8
 constexpr float A4_NONE = -1e30f;   // below every score: no key yet
@@ -148,11 +151,14 @@ __device__ __forceinline__ void a4_copy4(uint32_t* dst, const uint32_t* src) {
                : "memory");
 }
 
-template <int HD, int WARPS>
+template <int HD, int WARPS, bool FUSED>
 __global__ void __launch_bounds__(32 * WARPS, WARPS == A4_WIDE ? 1 : 4) attn_int4_kernel(AttnInt4Args a) {
   using C = A4<HD>;
-  pdl_enter();
+  // What a model's decode reads before pdl_enter() (positions, the cache) was written
+  // before the QKV projection it waits for there, which has itself waited for that.
+  if (!FUSED) pdl_enter();
   extern __shared__ __align__(128) float a4_smem[];
+  __shared__ __align__(16) __half a4_q[FUSED ? HD : 8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const int cls = gridDim.x, rank = blockIdx.x;
@@ -190,22 +196,6 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == A4_WIDE ? 1 : 4) attn_int
   const int lo_all = first_of(last_of(c0)), hi_all = last_of(c0 + cols - 1);
   const int full_lo = first_of(hi_all), full_hi = last_of(c0);   // seen by every column
 
-  // q as the B operand: column g, k step s = 2 jj + h covers the pairs (i, i + 4)
-  // of word KW * t + jj with i = 2h (k indices 2t, 2t + 1) and 2h + 1 (+ 8)
-  uint32_t qb[C::KSTEPS][2];
-  {
-    const int c = c0 + g, qi = c / a.group, hq = head * a.group + c % a.group;
-    const bool ok = g < cols;
-    const __half* q = a.q + (size_t)(row * a.n_q + (ok ? qi : 0)) * a.q_stride + (size_t)(ok ? hq : 0) * HD;
-#pragma unroll
-    for (int jj = 0; jj < C::KW; ++jj) {
-      const uint4 w = ok ? *reinterpret_cast<const uint4*>(q + 8 * (C::KW * t + jj)) : make_uint4(0u, 0u, 0u, 0u);
-      qb[2 * jj][0] = __byte_perm(w.x, w.z, 0x5410);       // elements 0, 4
-      qb[2 * jj][1] = __byte_perm(w.x, w.z, 0x7632);       // 1, 5
-      qb[2 * jj + 1][0] = __byte_perm(w.y, w.w, 0x5410);   // 2, 6
-      qb[2 * jj + 1][1] = __byte_perm(w.y, w.w, 0x7632);   // 3, 7
-    }
-  }
   const float csc = rsqrtf((float)HD) * 1.4426950408889634f;   // 1/sqrt(hd) in base 2
   float m[2], l[2], o[C::MT][4];
 
@@ -327,8 +317,71 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == A4_WIDE ? 1 : 4) attn_int
     ahead += slots;
     in_slot = in_slot + 1 == A4_STAGES ? 0 : in_slot + 1;
   };
+  // the tile that takes the new entry waits for it, the others' first copies do not
+  const bool holds_new = FUSED && ahead == tile_hi;
+  if (!holds_new)
 #pragma unroll
-  for (int i = 0; i < A4_STAGES - 1; ++i) request();
+    for (int i = 0; i < A4_STAGES - 1; ++i) request();
+  if constexpr (FUSED) {
+    const int pos = hi_all;
+    float2 cs[HD / 64];
+#pragma unroll
+    for (int p = 0; p < HD / 64; ++p) cs[p] = a.rope_cs[(size_t)pos * (HD / 2) + lane + 32 * p];
+    pdl_enter();
+    // rotate-half pairs (i, i + HD / 2), i = lane + 32 p, of q (every CTA, warp 0) and of
+    // k, with v (warp 1 of the CTA that reads the new entry's tile)
+    const float* x = a.qkv + (size_t)row * 3 * a.H * HD + (size_t)head * HD + lane;
+    if (warp == 0) {
+#pragma unroll
+      for (int p = 0; p < HD / 64; ++p) {
+        const float x0 = __ldcg(x + 32 * p), x1 = __ldcg(x + 32 * p + HD / 2);
+        a4_q[lane + 32 * p] = __float2half_rn(x0 * cs[p].x - x1 * cs[p].y);
+        a4_q[lane + 32 * p + HD / 2] = __float2half_rn(x1 * cs[p].x + x0 * cs[p].y);
+      }
+    } else if (warp == 1 && tile_hi % slots % stride / WARPS == rank) {
+      const float *k = x + (size_t)a.H * HD, *v = k + (size_t)a.H * HD;
+      __half kh[HD / 64][2], vh[HD / 64][2];
+#pragma unroll
+      for (int p = 0; p < HD / 64; ++p) {
+        const float x0 = __ldcg(k + 32 * p), x1 = __ldcg(k + 32 * p + HD / 2);
+        kh[p][0] = __float2half_rn(x0 * cs[p].x - x1 * cs[p].y);
+        kh[p][1] = __float2half_rn(x1 * cs[p].x + x0 * cs[p].y);
+        vh[p][0] = __float2half_rn(__ldcg(v + 32 * p));
+        vh[p][1] = __float2half_rn(__ldcg(v + 32 * p + HD / 2));
+      }
+      // the cache is const to the rest of the kernel: this row is read behind the barrier only
+      uint32_t *ck = const_cast<uint32_t*>(kc) + (size_t)pos * C::RW, *cv = const_cast<uint32_t*>(vc) + (size_t)pos * C::RW;
+      uint32_t *pk = const_cast<uint32_t*>(kp) + (size_t)pos * C::RP, *pv_ = const_cast<uint32_t*>(vp) + (size_t)pos * C::RP;
+#pragma unroll
+      for (int p = 0; p < HD / 64; ++p)
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          const int grp = p + hh * (HD / 64);
+          kv_int4_append_group(kh[p][hh], vh[p][hh], ck + 4 * grp, cv + 4 * grp, pk + grp, pv_ + grp);
+        }
+      __threadfence_block();
+    }
+    __syncthreads();
+    if (holds_new)
+#pragma unroll
+      for (int i = 0; i < A4_STAGES - 1; ++i) request();
+  }
+  // q as the B operand: column g, k step s = 2 jj + h covers the pairs (i, i + 4)
+  // of word KW * t + jj with i = 2h (k indices 2t, 2t + 1) and 2h + 1 (+ 8)
+  uint32_t qb[C::KSTEPS][2];
+  {
+    const int c = c0 + g, qi = c / a.group, hq = head * a.group + c % a.group;
+    const bool ok = g < cols;
+    const __half* q = FUSED ? a4_q : a.q + (size_t)(row * a.n_q + (ok ? qi : 0)) * a.q_stride + (size_t)(ok ? hq : 0) * HD;
+#pragma unroll
+    for (int jj = 0; jj < C::KW; ++jj) {
+      const uint4 w = ok ? *reinterpret_cast<const uint4*>(q + 8 * (C::KW * t + jj)) : make_uint4(0u, 0u, 0u, 0u);
+      qb[2 * jj][0] = __byte_perm(w.x, w.z, 0x5410);       // elements 0, 4
+      qb[2 * jj][1] = __byte_perm(w.x, w.z, 0x7632);       // 1, 5
+      qb[2 * jj + 1][0] = __byte_perm(w.y, w.w, 0x5410);   // 2, 6
+      qb[2 * jj + 1][1] = __byte_perm(w.y, w.w, 0x7632);   // 3, 7
+    }
+  }
 #pragma unroll 1
   while (true) {
     m[0] = m[1] = A4_NONE;
@@ -707,19 +760,24 @@ A4Split a4_lane_split(int max_ctx, long n, int cols) {
   return p;
 }
 
-template <int HD, int WARPS>
-tl_status launch_a4_warps(const AttnInt4Args& a, const A4Split& p, size_t smem, cudaStream_t s) {
+template <int HD, int WARPS, bool FUSED>
+tl_status launch_a4_kernel(const AttnInt4Args& a, const A4Split& p, size_t smem, cudaStream_t s) {
   static std::atomic<uint64_t> attr_done{0};
   TL_TRY(once_per_device(attr_done, []() -> tl_status {
-    TL_CUDA(cudaFuncSetAttribute(attn_int4_kernel<HD, WARPS>, cudaFuncAttributeMaxDynamicSharedMemorySize, A4_MAX_SMEM));
+    TL_CUDA(cudaFuncSetAttribute(attn_int4_kernel<HD, WARPS, FUSED>, cudaFuncAttributeMaxDynamicSharedMemorySize, A4_MAX_SMEM));
     return ok();
   }));
   const dim3 grid(p.ctas, a.H * a.col_tiles, a.n_rows);
-  const cudaError_t e = launch_pdl_cluster(attn_int4_kernel<HD, WARPS>, grid, dim3(32 * WARPS), smem, s,
+  const cudaError_t e = launch_pdl_cluster(attn_int4_kernel<HD, WARPS, FUSED>, grid, dim3(32 * WARPS), smem, s,
                                            p.records ? 1u : (unsigned)p.ctas, a);
   if (e != cudaSuccess)
     return set_error(TL_ERR_CUDA, "launch of attn_int4_kernel failed: %s", cudaGetErrorString(e));
   return ok();
+}
+
+template <int HD, int WARPS>
+tl_status launch_a4_warps(const AttnInt4Args& a, const A4Split& p, size_t smem, cudaStream_t s) {
+  return a.qkv ? launch_a4_kernel<HD, WARPS, true>(a, p, smem, s) : launch_a4_kernel<HD, WARPS, false>(a, p, smem, s);
 }
 
 template <int HD>

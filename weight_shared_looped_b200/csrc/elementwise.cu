@@ -298,30 +298,7 @@ __global__ void rope_kv_kernel(RopeKvArgs a) {
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
           const int grp = p + hh * npair;
-          const __half2 kv = __halves2half2(kh[p][hh], vh[p][hh]);   // K and V reduced together
-          __half2 mn = kv, mx = kv;
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) {
-            mn = __hmin2_nan(mn, kv_bits_h2(__shfl_xor_sync(0xffffffffu, kv_h2_bits(mn), o)));
-            mx = __hmax2_nan(mx, kv_bits_h2(__shfl_xor_sync(0xffffffffu, kv_h2_bits(mx), o)));
-          }
-          const Int4Group gk = kv_int4_group(__low2float(mn), __low2float(mx));
-          const Int4Group gv = kv_int4_group(__high2float(mn), __high2float(mx));
-          uint32_t wk = kv_int4_code(__low2float(kv), gk) << (4 * (lane & 7));
-          uint32_t wv = kv_int4_code(__high2float(kv), gv) << (4 * (lane & 7));
-#pragma unroll
-          for (int o = 1; o < 8; o <<= 1) {
-            wk |= __shfl_xor_sync(0xffffffffu, wk, o);
-            wv |= __shfl_xor_sync(0xffffffffu, wv, o);
-          }
-          if ((lane & 7) == 0) {
-            kc[4 * grp + (lane >> 3)] = wk;
-            vc[4 * grp + (lane >> 3)] = wv;
-          }
-          if (lane == 0) {
-            kp[grp] = gk.param;
-            vp[grp] = gv.param;
-          }
+          kv_int4_append_group(kh[p][hh], vh[p][hh], kc + 4 * grp, vc + 4 * grp, kp + grp, vp + grp);
         }
       }
     }

@@ -85,4 +85,35 @@ __device__ __forceinline__ __half2 kv_int4_pair(uint32_t x) {
   return __hfma2(kv_bits_h2(v), __float2half2_rn(0.0625f), __float2half2_rn(-64.f));
 }
 
+// A warp appends one group of a K row and of a V row, lane l holding element l of
+// each: eight code words (kc, vc: the group's four) and a parameter pair each.
+__device__ __forceinline__ void kv_int4_append_group(__half k, __half v, uint32_t* kc, uint32_t* vc, uint32_t* kp,
+                                                     uint32_t* vp) {
+  const int lane = threadIdx.x & 31;
+  const __half2 kv = __halves2half2(k, v);   // K and V reduced together
+  __half2 mn = kv, mx = kv;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    mn = __hmin2_nan(mn, kv_bits_h2(__shfl_xor_sync(0xffffffffu, kv_h2_bits(mn), o)));
+    mx = __hmax2_nan(mx, kv_bits_h2(__shfl_xor_sync(0xffffffffu, kv_h2_bits(mx), o)));
+  }
+  const Int4Group gk = kv_int4_group(__low2float(mn), __low2float(mx));
+  const Int4Group gv = kv_int4_group(__high2float(mn), __high2float(mx));
+  uint32_t wk = kv_int4_code(__low2float(kv), gk) << (4 * (lane & 7));
+  uint32_t wv = kv_int4_code(__high2float(kv), gv) << (4 * (lane & 7));
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) {
+    wk |= __shfl_xor_sync(0xffffffffu, wk, o);
+    wv |= __shfl_xor_sync(0xffffffffu, wv, o);
+  }
+  if ((lane & 7) == 0) {
+    kc[lane >> 3] = wk;
+    vc[lane >> 3] = wv;
+  }
+  if (lane == 0) {
+    *kp = gk.param;
+    *vp = gv.param;
+  }
+}
+
 }  // namespace tl

@@ -299,6 +299,11 @@ struct AttnInt4Args {
   size_t layer_bytes, region_bytes;
   int layer;
   int row_lane[kMaxLanes], row_cum[kMaxLanes];
+  // decode (n_q = 1, group = 1): the rows' new entries are made here, from the QKV
+  // projection's sums [n_rows][3 H hd] and the RoPE table [max_ctx][hd / 2], and
+  // appended; q is not read.  Null: q and the cache hold them.
+  const float* qkv;
+  const float2* rope_cs;
   bool lane_split;                 // a lane's bits must not depend on n_rows
   float* ws;                       // attn_int4_workspace bytes; null where that is 0
   int col_tiles, passes;           // set by the launcher
