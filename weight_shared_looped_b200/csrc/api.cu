@@ -1159,7 +1159,7 @@ tl_status rebuild_kv(tl_model* m, const tl_block_desc& bd, int layer, int rows, 
 // one lane, which its cache is read once for; RoPE and the append of all their
 // entries come first.  Otherwise the attention makes each row's entry itself.
 tl_status enqueue_int4_attention(tl_model* m, int layer, int rows, tl_kv* kv, const RowMap* rm,
-                                 const int32_t* lane_of_row, bool split_attn, cudaStream_t s) {
+                                 bool split_attn, cudaStream_t s) {
   if (split_attn) {
     RopeKvArgs r;
     memset(&r, 0, sizeof(r));
@@ -1178,9 +1178,8 @@ tl_status enqueue_int4_attention(tl_model* m, int layer, int rows, tl_kv* kv, co
     r.layer = layer;
     r.max_ctx = kv->max_ctx;
     r.kv_int4 = 1;
-    r.lane_of_row = lane_of_row;
     r.lane = rm->lane[0];
-    r.decode = 2;
+    r.decode = 1;
     TL_TRY(launch_rope_kv(r, s));
   }
   AttnInt4Args a;
@@ -1251,7 +1250,7 @@ tl_status enqueue_decode_layer(tl_model* m, const tl_block* b, int layer, int ro
   p.ex = exit_args(m, layer, 0);
   p.x_out = nullptr;
   if (store_h) TL_TRY(rebuild_kv(m, bd, layer, rows, kv, rm, odd, s));
-  if (kv->dtype == TL_KV_INT4) TL_TRY(enqueue_int4_attention(m, layer, rows, kv, rm, lane_of_row, split_attn, s));
+  if (kv->dtype == TL_KV_INT4) TL_TRY(enqueue_int4_attention(m, layer, rows, kv, rm, split_attn, s));
   // RoPE, KV append, split attention and merge in one launch
   DecodeAttnArgs da;
   memset(&da, 0, sizeof(da));

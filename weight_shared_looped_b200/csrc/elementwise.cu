@@ -188,7 +188,8 @@ __global__ void rope_kv_kernel(RopeKvArgs a) {
   const int row = wid / a.H, head = wid % a.H;
   const int half = a.hd / 2;
   const int npair = half / 32;   // 1 or 2
-  int kv_lane = a.lane, pos = a.pos0 + row;
+  const int kv_lane = a.lane;
+  int pos = a.pos0 + row;
   // prefill: the positions are the row indices, and the RoPE table and the
   // cache's layer offsets are constants: read them before waiting for the QKV
   // projection
@@ -203,12 +204,7 @@ __global__ void rope_kv_kernel(RopeKvArgs a) {
   pdl_enter();
   if (!active) return;
   if (a.decode) {
-    if (a.decode == 1) {
-      kv_lane = a.lane_of_row[row];
-      pos = a.hdr->pos[kv_lane];
-    } else {
-      pos = a.hdr->pos[kv_lane] + row;
-    }
+    pos = a.hdr->pos[kv_lane] + row;
 #pragma unroll
     for (int p = 0; p < 2; ++p)
       if (p < npair) csp[p] = a.rope_cs[(size_t)pos * half + lane + 32 * p];

@@ -209,10 +209,8 @@ struct RopeKvArgs {
   size_t layer_bytes, kv_region_bytes;   // region = K or V array bytes (256-aligned)
   int layer, max_ctx, kv_int8;
   int kv_int4;
-  const int32_t* lane_of_row;  // decode: lane of each row; null = prefill of `lane`
   int lane;
-  int decode;                  // 1: position = hdr->pos[lane]; 0: position = row index;
-                               // 2: position = hdr->pos[lane] + row index (rows of one lane)
+  int decode;                  // 1: position = hdr->pos[lane] + row index; 0: position = row index
   int kv_only;                 // 1: part holds [S][rows][2d] K|V sums only; no q is written
   int pos0;                    // decode == 0: position = pos0 + row index
 };
