@@ -237,6 +237,29 @@ def test_strides():
     assert (got[:, :w] == 5).all() and np.array_equal(got[:, w:].reshape(want.shape), want)
 
 
+@pytest.mark.parametrize("raw", [False, True])
+def test_a_workspace_for_another_stream(raw):
+    """The workspace that the binding allocates for a call on another stream is none of
+    the current stream's blocks: work queued there may still use them."""
+    H, hd, ctx = 1, 64, 8192
+    cache = Cache(*_kv(1, H, ctx, hd, 40))
+    q = _q(1, H, hd, 41)
+    want = _run(q, cache, [ctx], 1, 0)
+    need = tl.tl_attention_int4_workspace_bytes(*cache.t, 1, H)
+    tq = torch.from_numpy(q.reshape(1, -1)).cuda()
+    out, lens = torch.zeros_like(tq), torch.tensor([ctx], dtype=torch.int32, device="cuda")
+    block = torch.full((need,), 0xAB, dtype=torch.uint8, device="cuda")
+    ptr = block.data_ptr()
+    torch.cuda.synchronize()
+    del block
+    s = torch.cuda.Stream()
+    tl.tl_attention_int4(tq, *cache.t, lens, out, stream=s.cuda_stream if raw else s)
+    torch.cuda.synchronize()
+    again = torch.empty(need, dtype=torch.uint8, device="cuda")
+    assert again.data_ptr() == ptr and (again == 0xAB).all()
+    assert np.array_equal(out.cpu().numpy().reshape(want.shape), want)
+
+
 def test_streams_graphs_and_growing_lengths():
     """Two calls at once on two streams; a captured write and attention replayed
     while the lane grows."""

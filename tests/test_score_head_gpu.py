@@ -8,12 +8,16 @@ logits do, plus the rounding of the exponentials and their sum (2^-20 covers
 2^-22 of the fast exponential, its argument's rounding 2^-24 |z - m| <= 2^-19 on
 weights e^-(m - z), and the sum of V terms held in many parts).  The given
 token's logit and the order of the best come from fp64 sums."""
+from types import SimpleNamespace
+
 import numpy as np
 import pytest
 import torch
 
 import synthetic as syn
 import weight_shared_looped_b200 as tl
+
+from weight_shared_looped_b200.model import DeviceModel
 
 from gpu_util import device_model
 
@@ -238,6 +242,28 @@ def test_streams_and_graphs(n):
             want = _run(E, yy, t, k)
             for g, w in zip((r["lp"], r["h"], r["ids"], r["top"]), want):
                 assert np.array_equal(g.cpu().numpy(), w)
+
+
+def test_scores_on_another_stream():
+    """Outputs and workspace of a model's scores on another stream are none of the
+    current stream's blocks: work queued there may still use them."""
+    n, V, d, k = 70, 900, 128, 4
+    E, y, t = _inputs(n, V, d, 90)
+    want = _run(E, y, t, k)
+    model = SimpleNamespace(embed=torch.from_numpy(E).cuda(), d=d)
+    ty, tt = torch.from_numpy(y).cuda(), torch.from_numpy(t.astype(np.int32)).cuda()
+    sizes = [n * 4, n * 4, n * k * 4, n * k * 4, tl.tl_score_head_workspace_bytes(n, V, d, k)]
+    blocks = [torch.full((b,), 0xAB, dtype=torch.uint8, device="cuda") for b in sizes]
+    torch.cuda.synchronize()
+    ptrs = sorted(b.data_ptr() for b in blocks)
+    del blocks
+    s = torch.cuda.Stream()
+    got = DeviceModel.score(model, ty, tt, k=k, stream=s)
+    torch.cuda.synchronize()
+    again = [torch.empty(b, dtype=torch.uint8, device="cuda") for b in sizes]
+    assert sorted(b.data_ptr() for b in again) == ptrs and all((b == 0xAB).all() for b in again)
+    for a, b in zip((got["logp"], got["entropy"], got["ids"], got["top"]), want):
+        assert np.array_equal(a.cpu().numpy(), b)
 
 
 def test_model_scores_a_prompt():

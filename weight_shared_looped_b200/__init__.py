@@ -8,6 +8,7 @@ import fails.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional, Sequence
@@ -140,6 +141,18 @@ def _stream(stream) -> Optional[int]:
     if isinstance(stream, int):
         return stream or None
     return stream.cuda_stream or None
+
+
+def _allocating_on(stream, device):
+    """A context in which tensors are allocated for use on `stream` (None: the current one).
+    A block that the allocator hands out may still be in use on the stream it is for, and
+    is handed out again in that stream's order."""
+    if stream is None:
+        return contextlib.nullcontext()
+    import torch
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_stream(stream) or 0, device=device)
+    return torch.cuda.stream(stream)
 
 
 # --------------------------------------------------------------------- packing
@@ -371,9 +384,8 @@ def tl_attention_int4(q, k_codes, k_params, v_codes, v_params, lens, out, n_q: i
             b = SZ()
             _check(lib.tl_attention_int4_workspace_bytes(d, n_q, width // d.head_dim, b))
             if b.value:
-                workspace = n["torch"].empty(b.value, dtype=n["u8"], device=q.device)
-                if stream is not None and not isinstance(stream, int):
-                    workspace.record_stream(stream)   # freed at return, used until the stream gets there
+                with _allocating_on(stream, q.device):
+                    workspace = n["torch"].empty(b.value, dtype=n["u8"], device=q.device)
         elif workspace.dtype is not n["u8"] or workspace.get_device() != dev or not workspace.is_contiguous():
             _fail(f"{what}: workspace is not a contiguous uint8 tensor on {q.device}")
         if workspace is not None:

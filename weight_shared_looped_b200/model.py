@@ -15,7 +15,7 @@ from . import (TL_KV_FP16, TL_KV_INT4, TL_KV_INT8, TL_KV_H, tl_block_create, tl_
                tl_model_device_bytes, tl_model_set_decode_chunks, tl_model_set_graphs,
                tl_pack_weights, tl_packed_bytes, tl_prefill, tl_sync_status, tl_extend,
                tl_greedy_head, tl_spec_step, tl_model_set_exit_threshold, tl_loops_used,
-               tl_score_head, tl_score_head_workspace_bytes,
+               tl_score_head, tl_score_head_workspace_bytes, _allocating_on,
                tl_sign_bits_bytes, tl_pack_sign_bits, tl_model_set_cross_iter,
                tl_model_set_iteration_blocks)
 
@@ -153,20 +153,19 @@ class DeviceModel:
     def score(self, y, targets=None, k: int = 0, stream=None) -> Dict[str, torch.Tensor]:
         """Log probabilities under the tied embedding of final-norm outputs y fp32 [n, d]:
         "logp" of the given tokens (targets int32 [n], -1: none), the distributions' "entropy",
-        and the k most probable tokens, "ids" and "top"."""
+        and the k most probable tokens, "ids" and "top" (allocated for use on `stream`)."""
         if self.embed is None:
             raise ValueError("the model has no embedding to use as its head")
         n, dev = y.shape[0], y.device
-        out = {"entropy": torch.empty(n, dtype=torch.float32, device=dev)}
-        if targets is not None:
-            out["logp"] = torch.empty(n, dtype=torch.float32, device=dev)
-        if k:
-            out["ids"] = torch.empty(n, k, dtype=torch.int32, device=dev)
-            out["top"] = torch.empty(n, k, dtype=torch.float32, device=dev)
-        ws = torch.empty(tl_score_head_workspace_bytes(n, self.embed.shape[0], self.d, k),
-                         dtype=torch.uint8, device=dev)
-        if stream is not None and not isinstance(stream, int):
-            ws.record_stream(stream)   # freed at return, used until the stream gets there
+        with _allocating_on(stream, dev):
+            out = {"entropy": torch.empty(n, dtype=torch.float32, device=dev)}
+            if targets is not None:
+                out["logp"] = torch.empty(n, dtype=torch.float32, device=dev)
+            if k:
+                out["ids"] = torch.empty(n, k, dtype=torch.int32, device=dev)
+                out["top"] = torch.empty(n, k, dtype=torch.float32, device=dev)
+            ws = torch.empty(tl_score_head_workspace_bytes(n, self.embed.shape[0], self.d, k),
+                             dtype=torch.uint8, device=dev)
         tl_score_head(self.embed, y, targets, out.get("logp"), out["entropy"], out.get("ids"),
                       out.get("top"), ws, stream=stream)
         return out
