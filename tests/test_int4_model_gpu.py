@@ -168,8 +168,14 @@ def test_any_number_of_lanes_of_sixteen_heads(ctx):
     together = m.extend(a, x, lane=0, L=L).cpu().numpy()
     alone = np.concatenate([m.extend(b, x[i:i + 1], lane=0, L=L).cpu().numpy() for i in range(8)])
     assert np.array_equal(together, alone)
-    a.close()
-    b.close()
+    c = new([0])
+    steps_ = np.concatenate([m.decode(c, x[i:i + 1], L_per_lane=[L]).cpu().numpy() for i in range(8)])
+    assert np.array_equal(together, steps_)
+    for layer in range(w.n_pre + L):                   # and the same entries
+        for pa, pc, words in zip(a.layer_ptrs(0, layer), c.layer_ptrs(0, layer), (hd // 8, hd // 8, hd // 32, hd // 32)):
+            assert torch.equal(_raw(a, pa, (H, ctx, words), torch.int32), _raw(c, pc, (H, ctx, words), torch.int32))
+    for kv in (a, b, c):
+        kv.close()
     m.close()
 
 
