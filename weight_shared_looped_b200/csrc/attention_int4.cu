@@ -334,18 +334,18 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == A4_WIDE ? 1 : 4) attn_int
     if (warp == 0) {
 #pragma unroll
       for (int p = 0; p < HD / 64; ++p) {
-        const float x0 = __ldcg(x + 32 * p), x1 = __ldcg(x + 32 * p + HD / 2);
-        a4_q[lane + 32 * p] = __float2half_rn(x0 * cs[p].x - x1 * cs[p].y);
-        a4_q[lane + 32 * p + HD / 2] = __float2half_rn(x1 * cs[p].x + x0 * cs[p].y);
+        const float2 r = kv_rope(__ldcg(x + 32 * p), __ldcg(x + 32 * p + HD / 2), cs[p]);
+        a4_q[lane + 32 * p] = __float2half_rn(r.x);
+        a4_q[lane + 32 * p + HD / 2] = __float2half_rn(r.y);
       }
     } else if (warp == 1 && tile_hi % slots % stride / WARPS == rank) {
       const float *k = x + (size_t)a.H * HD, *v = k + (size_t)a.H * HD;
       __half kh[HD / 64][2], vh[HD / 64][2];
 #pragma unroll
       for (int p = 0; p < HD / 64; ++p) {
-        const float x0 = __ldcg(k + 32 * p), x1 = __ldcg(k + 32 * p + HD / 2);
-        kh[p][0] = __float2half_rn(x0 * cs[p].x - x1 * cs[p].y);
-        kh[p][1] = __float2half_rn(x1 * cs[p].x + x0 * cs[p].y);
+        const float2 r = kv_rope(__ldcg(k + 32 * p), __ldcg(k + 32 * p + HD / 2), cs[p]);
+        kh[p][0] = __float2half_rn(r.x);
+        kh[p][1] = __float2half_rn(r.y);
         vh[p][0] = __float2half_rn(__ldcg(v + 32 * p));
         vh[p][1] = __float2half_rn(__ldcg(v + 32 * p + HD / 2));
       }

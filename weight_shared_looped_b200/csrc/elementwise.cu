@@ -250,12 +250,11 @@ __global__ void rope_kv_kernel(RopeKvArgs a) {
 #pragma unroll
   for (int p = 0; p < 2; ++p) {
     if (p < npair) {
-      const float2 cs = csp[p];
-      float q0 = q[p][0], q1 = q[p][1], k0 = k[p][0], k1 = k[p][1];
-      q[p][0] = q0 * cs.x - q1 * cs.y;
-      q[p][1] = q1 * cs.x + q0 * cs.y;
-      k[p][0] = k0 * cs.x - k1 * cs.y;
-      k[p][1] = k1 * cs.x + k0 * cs.y;
+      const float2 qr = kv_rope(q[p][0], q[p][1], csp[p]), kr = kv_rope(k[p][0], k[p][1], csp[p]);
+      q[p][0] = qr.x;
+      q[p][1] = qr.y;
+      k[p][0] = kr.x;
+      k[p][1] = kr.y;
     }
   }
   __half kh[2][2], vh[2][2];

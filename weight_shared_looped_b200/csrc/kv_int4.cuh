@@ -85,6 +85,13 @@ __device__ __forceinline__ __half2 kv_int4_pair(uint32_t x) {
   return __hfma2(kv_bits_h2(v), __float2half2_rn(0.0625f), __float2half2_rn(-64.f));
 }
 
+// Rotate-half RoPE of the pair (x0, x1) by (cos, sin), with the roundings written out:
+// whoever makes a 4-bit entry must make the same one, and left to the compiler two
+// kernels fused different products of the second sum.
+__device__ __forceinline__ float2 kv_rope(float x0, float x1, float2 cs) {
+  return make_float2(__fmaf_rn(x0, cs.x, -__fmul_rn(x1, cs.y)), __fmaf_rn(x0, cs.y, __fmul_rn(x1, cs.x)));
+}
+
 // A warp appends one group of a K row and of a V row, lane l holding element l of
 // each: eight code words (kc, vc: the group's four) and a parameter pair each.
 __device__ __forceinline__ void kv_int4_append_group(__half k, __half v, uint32_t* kc, uint32_t* vc, uint32_t* kp,
