@@ -11,10 +11,10 @@
 // accesses are whole head rows.
 //
 // Memory sets the floor: written, 4 * H * hd bytes in and 1.25 * H * hd out per
-// token; read back, the reverse.  16384 tokens of 16 heads of 128 (172 MB each way)
-// are written in 42 us, 4.1 TB/s (issue slots: about 150 instructions per eight
-// values of K and of V, for the group's extremes and the rounding of each code), and
-// read back in 31 us, 5.6 TB/s.  One token per lane takes 2 us, a launch.
+// token; read back, the reverse.  16384 tokens of 16 heads of 128 (176 MB each way)
+// are written in 42 us, 4.2 TB/s (bound by issue slots: about 140 instructions per
+// eight values, for the group's extremes and parameters and the rounding of each
+// code), and read back in 31 us, 5.7 TB/s.  One token per lane takes 2 us, a launch.
 #include "kv_int4.cuh"
 #include "tl_launch.cuh"
 
