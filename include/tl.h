@@ -213,7 +213,7 @@ tl_status tl_kv_read_int4(const tl_kv_int4* cache, uint16_t* k, uint16_t* v, lon
  *   q      device fp16 [n_lanes * n_q][q_stride], row b * n_q + i, head h at
  *          column h * head_dim
  *   lens   device int32 [n_lanes]: positions that hold entries, the queries' own
- *          included; values above max_ctx count as max_ctx
+ *          included; values above max_ctx count as max_ctx, negative ones as 0
  *   out    device fp16 [n_lanes * n_q][out_stride] (must not overlap q)
  *   workspace  device scratch of tl_attention_int4_workspace_bytes bytes, 16-byte
  *          aligned, for this call's use until it completes on the stream; may be

@@ -204,6 +204,22 @@ def test_any_number_of_lanes(ctx, lanes, H, group, hd, n_q):
     for b in range(0, 6, 2):
         six = slice(b * n_q, (b + 2) * n_q)
         _check(got[b:b + 2].reshape(2 * n_q, H * group, hd), q[six], two, lens[b:b + 2].tolist(), n_q, 0)
+    # what lies behind a lane's last entry may be anything
+    behind = torch.arange(ctx, device="cuda") >= torch.from_numpy(lens).cuda()[:, None]
+    for i in (1, 3):
+        cache[i][behind[:, None].expand(-1, H, -1)] = float("nan")
+        cache[i - 1][behind[:, None].expand(-1, H, -1)] = -1
+    again = torch.full_like(x, 9.0)
+    tl.tl_attention_int4(x, *cache, torch.from_numpy(lens).cuda(), again, n_q=n_q)
+    assert torch.equal(again, out)
+
+
+def test_lengths_below_zero():
+    """A negative length is an empty lane, down to the least 32-bit value."""
+    cache = Cache(*_kv(1, 1, 70, 64, 42))
+    q = _q(5, 1, 64, 43)
+    for n in (-1, -6, -(1 << 31), -(1 << 31) + 3):
+        assert (_run(q, cache, [n], 5, 0) == 0).all() and (_run(q, cache, [n], 5, 3) == 0).all(), n
 
 
 def test_a_query_alone_and_among_others_gives_the_same_bits():

@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == A4_WIDE ? 1 : 4) attn_int
     vp = a.v_params + (size_t)row * a.param_stride;
     len = a.lens[row];
   }
-  len = min(len, a.max_ctx);
+  len = max(0, min(len, a.max_ctx));
   kc += (size_t)head * a.max_ctx * C::RW;
   vc += (size_t)head * a.max_ctx * C::RW;
   kp += (size_t)head * a.max_ctx * C::RP;
