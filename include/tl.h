@@ -428,8 +428,8 @@ tl_status tl_kv_layer_bytes(int n_heads, int head_dim, int max_ctx, tl_kv_dtype 
 /* Bytes of the cache buffer for n_lanes lanes of max_ctx positions each, lane
  * b running L_per_lane[b] loop iterations: the 4 KiB header, every lane's
  * n_pre + L_b slots (tl_kv_layer_bytes each) and, for TL_KV_H, the rebuild
- * workspace or, for TL_KV_INT4 with max_ctx >= 8192, the attention's.  Host-only.  Errors: TL_ERR_INVALID_ARG for a NULL model,
- * L_per_lane or bytes, n_lanes outside [1, 8], max_ctx outside [1, the
+ * workspace or, for TL_KV_INT4 with max_ctx >= 8192, the attention's.
+ * Host-only.  Errors: TL_ERR_INVALID_ARG for a NULL model, L_per_lane or bytes, n_lanes outside [1, 8], max_ctx outside [1, the
  * model's max_ctx], an L outside [1, max_L] or an unknown dtype. */
 tl_status tl_kv_bytes(const tl_model* model, int n_lanes, int max_ctx,
                       const int* L_per_lane /* host [n_lanes] */,

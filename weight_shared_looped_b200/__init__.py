@@ -250,28 +250,31 @@ def _explain(what: str, **named) -> None:
 
 def _launch(n, device: int, stream, call, *args) -> None:
     """The C call on `stream` (default: `device`'s current one) with `device` current."""
+    raw, current = n["stream"], n["device"]
     if stream is not None:
         s = _stream(stream)
-    elif n["stream"] is not None:
-        s = n["stream"](device)
+    elif raw is not None:
+        s = raw(device)
     else:
         s = n["torch"].cuda.current_stream(device).cuda_stream
-    now = n["device"]() if n["device"] is not None else n["torch"].cuda.current_device()
-    if now == device:
-        _check(call(*args, s))
+    if (current() if current is not None else n["torch"].cuda.current_device()) == device:
+        status = call(*args, s)
     else:
         with n["torch"].cuda.device(device):
-            _check(call(*args, s))
+            status = call(*args, s)
+    if status:
+        _check(status)
 
 
 def _kv_int4(what: str, k_codes, k_params, v_codes, v_params) -> KvInt4Desc:
     """The cache description of codes int32 [lanes, heads, ctx, hd / 8] and parameters fp16
-    [lanes, heads, ctx, hd / 32, 2]; only the lane stride is free."""
-    shape, pshape = k_codes.shape, k_params.shape
+    [lanes, heads, ctx, hd / 32, 2]; only the lane stride is free.  ValueError: k_codes does
+    not have four dimensions."""
+    shape = k_codes.shape
     lanes, heads, ctx, words = shape
-    if (v_codes.shape != shape or v_params.shape != pshape
-            or pshape != (lanes, heads, ctx, words // 4, 2)):
-        _fail(f"{what}: codes {tuple(shape)} and {tuple(v_codes.shape)}, parameters {tuple(pshape)} and "
+    pshape = (lanes, heads, ctx, words // 4, 2)
+    if v_codes.shape != shape or k_params.shape != pshape or v_params.shape != pshape:
+        _fail(f"{what}: codes {tuple(shape)} and {tuple(v_codes.shape)}, parameters {tuple(k_params.shape)} and "
               f"{tuple(v_params.shape)} do not have the shapes [lanes, heads, ctx, hd / 8] and "
               "[lanes, heads, ctx, hd / 32, 2]")
     if (k_codes.is_contiguous() and k_params.is_contiguous() and v_codes.is_contiguous()
@@ -294,29 +297,32 @@ def _kv_int4_rows(what, fn, k, v, k_codes, k_params, v_codes, v_params, pos, cu,
     n = _TORCH or _torch_names()
     f16, i32 = n["f16"], n["i32"]
     dev = k.get_device()
-    if not (dev >= 0 and k.dtype in f16 and v.dtype in f16 and k_codes.dtype is i32
-            and v_codes.dtype is i32 and k_params.dtype in f16 and v_params.dtype in f16
-            and pos.dtype is i32 and (cu is None or cu.dtype is i32)
-            and k.dim() == 2 == v.dim() and k_codes.dim() == 4 == v_codes.dim()
-            and k_params.dim() == 5 == v_params.dim() and pos.dim() == 1
-            and (cu is None or (cu.dim() == 1 and cu.get_device() == dev))
-            and v.get_device() == dev == k_codes.get_device() == v_codes.get_device()
-            and k_params.get_device() == dev == v_params.get_device() == pos.get_device()):
+    ok = (dev >= 0 and k.dtype in f16 and v.dtype in f16 and k_codes.dtype is i32
+          and v_codes.dtype is i32 and k_params.dtype in f16 and v_params.dtype in f16
+          and pos.dtype is i32 and (cu is None or (cu.dtype is i32 and cu.get_device() == dev))
+          and v.get_device() == dev == k_codes.get_device() == v_codes.get_device()
+          and k_params.get_device() == dev == v_params.get_device() == pos.get_device())
+    if ok:
+        try:   # what the cache description does not compare: the dimensions it unpacks
+            rows, width = shape = k.shape
+            d = _kv_int4(what, k_codes, k_params, v_codes, v_params)
+        except ValueError:
+            ok = False
+    if not ok:
         i = (i32,)
         _explain(what, k=(k, f16, 2), v=(v, f16, 2), k_codes=(k_codes, i, 4), k_params=(k_params, f16, 5),
                  v_codes=(v_codes, i, 4), v_params=(v_params, f16, 5), pos=(pos, i, 1), cu=(cu, i, 1))
-    d = _kv_int4(what, k_codes, k_params, v_codes, v_params)
-    rows, width = k.shape
-    if v.shape != k.shape or width != d.n_heads * d.head_dim:
+    lanes = d.n_lanes
+    if v.shape != shape or width != d.n_heads * d.head_dim:
         _fail(f"{what}: k {tuple(k.shape)} and v {tuple(v.shape)} are not rows of "
               f"{d.n_heads} x {d.head_dim} values")
-    stride, unit = k.stride()
-    if rows and (unit != 1 or v.stride() != (stride, 1)) and (rows > 1 or unit != 1 or v.stride(1) != 1):
+    stride, unit = strides = k.stride()
+    if rows and (unit != 1 or v.stride() != strides) and (rows > 1 or unit != 1 or v.stride(1) != 1):
         _fail(f"{what}: k and v need unit column stride and the same row stride")
-    if pos.shape[0] != d.n_lanes or not pos.is_contiguous():
-        _fail(f"{what}: pos is not a contiguous [{d.n_lanes}]")
-    if cu is not None and (cu.shape[0] != d.n_lanes + 1 or not cu.is_contiguous()):
-        _fail(f"{what}: cu is not a contiguous [{d.n_lanes + 1}]")
+    if pos.shape != (lanes,) or not pos.is_contiguous():
+        _fail(f"{what}: pos is not a contiguous [{lanes}]")
+    if cu is not None and (cu.shape != (lanes + 1,) or not cu.is_contiguous()):
+        _fail(f"{what}: cu is not a contiguous [{lanes + 1}]")
     _launch(n, dev, stream, fn, d, k.data_ptr(), v.data_ptr(), stride if rows > 1 else width,
             None if cu is None else cu.data_ptr(), pos.data_ptr(), rows)
 
@@ -355,34 +361,38 @@ def tl_attention_int4(q, k_codes, k_params, v_codes, v_params, lens, out, n_q: i
     f16, i32 = n["f16"], n["i32"]
     what = "tl_attention_int4"
     dev = q.get_device()
-    if not (dev >= 0 and q.dtype in f16 and out.dtype in f16 and k_codes.dtype is i32
-            and v_codes.dtype is i32 and k_params.dtype in f16 and v_params.dtype in f16
-            and lens.dtype is i32 and q.dim() == 2 == out.dim()
-            and k_codes.dim() == 4 == v_codes.dim() and k_params.dim() == 5 == v_params.dim()
-            and lens.dim() == 1 and out.get_device() == dev == k_codes.get_device()
-            and v_codes.get_device() == dev == k_params.get_device()
-            and v_params.get_device() == dev == lens.get_device()):
+    ok = (dev >= 0 and q.dtype in f16 and out.dtype in f16 and k_codes.dtype is i32
+          and v_codes.dtype is i32 and k_params.dtype in f16 and v_params.dtype in f16
+          and lens.dtype is i32 and out.get_device() == dev == k_codes.get_device()
+          and v_codes.get_device() == dev == k_params.get_device()
+          and v_params.get_device() == dev == lens.get_device())
+    if ok:
+        try:   # what the cache description does not compare: the dimensions it unpacks
+            rows, width = shape = q.shape
+            d = _kv_int4(what, k_codes, k_params, v_codes, v_params)
+        except ValueError:
+            ok = False
+    if not ok:
         i = (i32,)
         _explain(what, q=(q, f16, 2), k_codes=(k_codes, i, 4), k_params=(k_params, f16, 5),
                  v_codes=(v_codes, i, 4), v_params=(v_params, f16, 5), lens=(lens, i, 1), out=(out, f16, 2))
-    d = _kv_int4(what, k_codes, k_params, v_codes, v_params)
-    rows, width = q.shape
-    if rows != d.n_lanes * n_q or width % d.head_dim or out.shape != q.shape:
-        _fail(f"{what}: q {tuple(q.shape)} and out {tuple(out.shape)} are not {d.n_lanes} x {n_q} "
-              f"rows of heads of {d.head_dim}")
+    lanes, head_dim = d.n_lanes, d.head_dim
+    if rows != lanes * n_q or width % head_dim or out.shape != shape:
+        _fail(f"{what}: q {tuple(q.shape)} and out {tuple(out.shape)} are not {lanes} x {n_q} "
+              f"rows of heads of {head_dim}")
     qs, qu = q.stride()
     os_, ou = out.stride()
     if rows and (qu != 1 or ou != 1):
         _fail(f"{what}: q and out need unit column stride")
-    if lens.shape[0] != d.n_lanes or not lens.is_contiguous():
-        _fail(f"{what}: lens is not a contiguous [{d.n_lanes}]")
+    if lens.shape != (lanes,) or not lens.is_contiguous():
+        _fail(f"{what}: lens is not a contiguous [{lanes}]")
     if rows <= 1:
         qs = os_ = width
     ws, ws_bytes = None, 0
     if d.max_ctx >= _INT4_SPLIT_CTX and rows:
         if workspace is None:
             b = SZ()
-            _check(lib.tl_attention_int4_workspace_bytes(d, n_q, width // d.head_dim, b))
+            _check(lib.tl_attention_int4_workspace_bytes(d, n_q, width // head_dim, b))
             if b.value:
                 with _allocating_on(stream, q.device):
                     workspace = n["torch"].empty(b.value, dtype=n["u8"], device=q.device)
@@ -390,7 +400,7 @@ def tl_attention_int4(q, k_codes, k_params, v_codes, v_params, lens, out, n_q: i
             _fail(f"{what}: workspace is not a contiguous uint8 tensor on {q.device}")
         if workspace is not None:
             ws, ws_bytes = workspace.data_ptr(), workspace.numel()
-    _launch(n, dev, stream, lib.tl_attention_int4, d, q.data_ptr(), qs, n_q, width // d.head_dim,
+    _launch(n, dev, stream, lib.tl_attention_int4, d, q.data_ptr(), qs, n_q, width // head_dim,
             lens.data_ptr(), window, out.data_ptr(), os_, ws, ws_bytes)
 
 
