@@ -106,6 +106,27 @@ def test_every_tile_width(n, V):
     test_matches_fp64(n, V, 192, 6)
 
 
+@pytest.mark.parametrize("n", [40, 200, 500])
+def test_no_bias_of_the_sums(n):
+    """The tensor cores' additions round towards zero, which takes 0.29 d 2^-28 (row-major
+    0.57 d 2^-28) of an average logit and as much of lse as the mean logit is; the kernels
+    give that back.  What may be left of the mean over rows and runs: a fifth of the
+    smaller one, and the fp32 result's rounding, 2^-24 of it at most."""
+    d, V = 4096, 3000
+    bias, weight, size = [], [], []
+    for seed in range(3):
+        E, y, t = _inputs(n, V, d, 300 + seed, lean=0.0)
+        lp = _run(E, y, t, 0)[0]
+        z = torch.from_numpy(y).cuda().double() @ torch.from_numpy(E).cuda().double().t()
+        want = torch.log_softmax(z, 1)
+        bias.append(lp - want.gather(1, torch.from_numpy(np.asarray(t)).cuda().long()[:, None])[:, 0].cpu().numpy())
+        weight.append((want.exp() * z).sum(1).cpu().numpy())
+        size.append(np.abs(lp))
+    bias, weight, size = (np.concatenate(a).mean() for a in (bias, weight, size))
+    assert weight > 1                                  # so that the bias would show: 0.29 d 2^-28 = 4.4e-6
+    assert abs(bias) <= 0.2 * 0.29 * d * 2.0 ** -28 * weight + 2.0 ** -24 * size
+
+
 def test_ties_go_to_the_lowest_id():
     """Equal rows of the embedding give equal logits."""
     E, y, t = _inputs(40, 3000, 256, 50)
