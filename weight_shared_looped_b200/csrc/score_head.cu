@@ -14,7 +14,7 @@
 // Pass 1 streams the embedding through tcgen05 and keeps, per row and slice of
 // the vocabulary, the running maximum m, l = sum e^(z - m), s = sum e^(z - m) (z - m)
 // and the best candidates.
-// Pass 2, one CTA per row, merges the slices and decides the order of the best
+// Pass 2, a CTA per row (a warp per row where there are many), merges the slices and decides the order of the best
 // k + kSpare candidates, and the given token's logit, by fp64 dot products of the
 // inputs, so the ranking does not depend on pass 1's rounding (ties go to the
 // lowest token id; equal embedding rows tie in pass 1 already, and for another
@@ -24,7 +24,7 @@
 // Bounds (vocabulary 50257, d 2048): few rows by the embedding's 206 MB, 31 us; one row
 // with k 5 takes 47 us (passes 0 and 2 and the fill and tail of pass 1 are 12 of
 // them).  Many rows by the matrix work, twice 2 n V d; 1024 rows in 310 us with k 0,
-// 1.36 PFLOP/s, 333 with k 5 (candidates).  In between the epilogue of the last tiles
+// 1.36 PFLOP/s, 324 with k 5 (candidates, merge).  In between the epilogue of the last tiles
 // shows: 128 rows with k 8 take 80 us.
 #include <math_constants.h>
 
