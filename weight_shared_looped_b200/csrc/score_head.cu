@@ -30,6 +30,7 @@
 
 #include <algorithm>
 #include <cstring>
+#include <type_traits>
 
 #include "tc_util.cuh"
 
@@ -374,40 +375,46 @@ __global__ void __launch_bounds__(SR_THREADS, 1)
           if (c0 >= cols) break;
           sc_ld_wait(w[h]);
           if (c0 + 16 < cols) sc_ld16(w[h ^ 1], base + c0 + 16);
-          const int nv = valid - c0;                   // uniform over the warp
-          if (nv <= 0) continue;
-          float x[16];
-          float top = -INFINITY;
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            x[j] = __uint_as_float(w[h][j]);
-            if (j < nv) top = fmaxf(top, x[j]);
-          }
-          const float top2 = top * rs2;
-          if (top2 > m) {
-            const float f = sc_ex2(m - top2);
-            sx = l == 0.f ? 0.f : (sx + l * (m - top2)) * f;
-            l *= f;
-            m = top2;
-          }
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            if (j < nv) {
-              const float t = fmaf(x[j], rs2, -m), e = sc_ex2(t);
-              l += e;
-              sx = fmaf(e, t, sx);
-            }
-          }
-          if (__any_sync(0xffffffffu, top > cx[KC - 1])) {
+          // 16 logits, all of them entries of the vocabulary except at its end (a test per
+          // logit took 5 % of 1021 rows of d 256, where the epilogue is what counts)
+          auto take = [&](auto full, int nv) {
+            constexpr bool all = decltype(full)::value;
+            float x[16];
+            float top = -INFINITY;
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
-              if ((j & 3) == 0 && __any_sync(0xffffffffu, queued > SR_QUEUE - 4)) drain();
-              if (j < nv && x[j] > cx[KC - 1]) {
-                queue[queued * 256] = make_uint2(__float_as_uint(x[j]), (uint32_t)(v0 + c0 + j));
-                ++queued;
+              x[j] = __uint_as_float(w[h][j]);
+              if (all || j < nv) top = fmaxf(top, x[j]);
+            }
+            const float top2 = top * rs2;
+            if (top2 > m) {
+              const float f = sc_ex2(m - top2);
+              sx = l == 0.f ? 0.f : (sx + l * (m - top2)) * f;
+              l *= f;
+              m = top2;
+            }
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              if (all || j < nv) {
+                const float t = fmaf(x[j], rs2, -m), e = sc_ex2(t);
+                l += e;
+                sx = fmaf(e, t, sx);
               }
             }
-          }
+            if (__any_sync(0xffffffffu, top > cx[KC - 1])) {
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                if ((j & 3) == 0 && __any_sync(0xffffffffu, queued > SR_QUEUE - 4)) drain();
+                if ((all || j < nv) && x[j] > cx[KC - 1]) {
+                  queue[queued * 256] = make_uint2(__float_as_uint(x[j]), (uint32_t)(v0 + c0 + j));
+                  ++queued;
+                }
+              }
+            }
+          };
+          const int nv = valid - c0;                   // uniform over the warp
+          if (nv >= 16) take(std::true_type{}, 16);
+          else if (nv > 0) take(std::false_type{}, nv);
         }
       }
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
