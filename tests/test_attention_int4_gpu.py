@@ -34,6 +34,13 @@ def _run(q, cache, lens, n_q, window, out=None):
     return out.cpu().numpy().reshape(rows, heads, hd)
 
 
+class TwoByTurns:
+    """The lanes 0, 1, 0, 1, .. of a cache of two."""
+
+    def __init__(self, two):
+        self.K, self.V = lambda b: two.K(b % 2), lambda b: two.V(b % 2)
+
+
 def _check(got, q, cache, lens, n_q, window):
     for b, length in enumerate(lens):
         rows = slice(b * n_q, (b + 1) * n_q)
@@ -212,6 +219,13 @@ def test_any_number_of_lanes(ctx, lanes, H, group, hd, n_q):
     again = torch.full_like(x, 9.0)
     tl.tl_attention_int4(x, *cache, torch.from_numpy(lens).cuda(), again, n_q=n_q)
     assert torch.equal(again, out)
+    # a window: tiles in front of it are skipped, the first one is cut
+    window = max(1, ctx // 3)
+    tl.tl_attention_int4(x, *cache, torch.from_numpy(lens).cuda(), again, n_q=n_q, window=window)
+    got = again.cpu().numpy().reshape(lanes, n_q, H * group, hd)
+    for b in range(6, lanes):
+        assert np.array_equal(got[b], got[b % 6]), b
+    _check(got[:4].reshape(4 * n_q, H * group, hd), q[:4 * n_q], TwoByTurns(two), lens[:4].tolist(), n_q, window)
 
 
 def test_lengths_below_zero():

@@ -46,9 +46,6 @@
 // where a key's value is not finite and some query of the tile does not see
 // it, the tile's V product runs query by query with the unseen keys zeroed.
 #include <algorithm>
-#include <map>
-#include <mutex>
-#include <tuple>
 
 #include "kv_int4.cuh"
 #include "tl_launch.cuh"
