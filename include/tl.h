@@ -532,10 +532,14 @@ tl_status tl_greedy_head(tl_model* model, const float* y, int n, int32_t* ids,
  *   top_ids[r][i], top_logp[r][i] = the k most probable tokens, most probable
  *                   first, the lowest id first among equal logits, and their log
  *                   probabilities
- * The logits are not stored.  y enters the products as two fp16 parts (22 bits);
- * sums are fp32; the given token's logit and the order of the best are decided
- * by fp64 dot products of the inputs.  A row with a logit that is not finite gets
- * NaN and ids of -1.
+ * The logits are not stored.  y enters the products as two fp16 parts (22 bits).
+ * The tensor cores sum up 512 elements at a time, in 64 additions that round
+ * towards zero; those sums are added in fp32.  A logit of the sum over v is so
+ * off by at most (2^-22 + 2^-17 + d 2^-33) sum_i |y_i E_i[v]|; towards zero by half
+ * of the 2^-17 where it comes from few early elements, by less elsewhere.  The
+ * given token's logit, the order of the best and the largest terms of the sum are
+ * decided by fp64 dot products of the inputs.  A row with a logit that is not
+ * finite gets NaN and ids of -1.
  *   embed      device fp16 [vocab, d]
  *   y          device fp32 [n][y_stride]
  *   targets    device int32 [n], with logp; or both NULL

@@ -304,3 +304,92 @@ def test_model_scores_a_prompt():
     greedy = m.greedy_head(y[:8].contiguous())
     assert torch.equal(greedy, got["ids"][:8, 0])
     m.close()
+
+
+def _chunk_eps(A, d):
+    """A logit's error: activations of 22 bits; 512 elements of two parts in 64 additions
+    towards zero, 24 more for the sums of 16 products within them; the chunks' fp32 sums."""
+    return A * (2.0 ** -22 + (min(d, 512) / 8 + 24) * 2.0 ** -23 + d / 512 * 2.0 ** -24)
+
+
+def _errors(E, y, t, k=0):
+    """logp - its fp64 value, and the probable logits' mean size."""
+    lp = _run(E, y, t, k)[0]
+    z = torch.from_numpy(y).cuda().double() @ torch.from_numpy(E).cuda().double().t()
+    want = torch.log_softmax(z, 1)
+    at = torch.from_numpy(np.asarray(t)).cuda().long()[:, None]
+    return (lp - want.gather(1, at)[:, 0].cpu().numpy()), (want.exp() * z).sum(1).cpu().numpy()
+
+
+@pytest.mark.parametrize("n", [40, 57, 200])
+@pytest.mark.parametrize("d", [512, 2048, 8192])
+@pytest.mark.parametrize("at", [3, -3])
+def test_logits_from_one_channel(n, d, at):
+    """All activations zero but one: every sum has one term of each part, so only the split
+    (2^-22 of the logit) and the parts' sum (2^-23) round, whatever d is and wherever the
+    channel lies; beside them the exponentials and the result as above."""
+    V = 1500
+    E, y, t = _inputs(n, V, d, 110)
+    c = at % d
+    E[:, c] = 1 + np.abs(E[:, 0])
+    y[:] = 0
+    y[:, c] = np.linspace(20, 50, n)
+    err, z = _errors(E, y, t)
+    tol = z * (2.0 ** -22 + 2.0 ** -23) + 2.0 ** -20 + 2.0 ** -24 * np.log(V)
+    assert z.min() > 19
+    assert (np.abs(err) <= tol).all(), (np.abs(err) / tol).max()
+
+
+@pytest.mark.parametrize("n", [40, 57, 200])
+@pytest.mark.parametrize("d", [4096, 8192])
+def test_sparse_activations(n, d):
+    """Eight channels, far apart: sixteen terms, each added with a loss of 2^-23 at most."""
+    V = 1500
+    E, y, t = _inputs(n, V, d, 111)
+    cs = np.arange(8) * (d // 8) + 5
+    E[:, cs] = 1 + np.abs(E[:, :8])
+    y[:] = 0
+    y[:, cs] = np.linspace(3, 6, n)[:, None]
+    err, z = _errors(E, y, t)
+    tol = z * (2.0 ** -22 + 16 * 2.0 ** -23 + 8 * 2.0 ** -24) + 2.0 ** -20 + 2.0 ** -24 * np.log(V)
+    assert z.min() > 23
+    assert (np.abs(err) <= tol).all(), (np.abs(err) / tol).max()
+
+
+@pytest.mark.parametrize("n", [40, 57, 200])
+@pytest.mark.parametrize("d", [4096, 8192])
+@pytest.mark.parametrize("at", [3, -3])
+def test_one_channel_far_above_the_others(n, d, at):
+    """Flat rows whose logits come from one channel, early or late, the others adding noise.
+    Every addition of its chunk loses half of 2^-23 of the logit on average (64 of them:
+    2^-18), the other chunks' next to nothing; over the vocabulary that is an average."""
+    V = 1500
+    E, y, t = _inputs(n, V, d, 112, lean=0.0)
+    c = at % d
+    E[:, c] = 1 + np.abs(E[:, 0])
+    y[:, c] = np.linspace(20, 40, n)
+    err, z = _errors(E, y, t)
+    assert z.min() > 19
+    assert (np.abs(err) <= z * (2.0 ** -18 + 2.0 ** -22) + 2.0 ** -20 + 2.0 ** -24 * np.log(V)).all(), np.abs(err / z).max()
+
+
+CHUNKS = [
+    # n, V, d, k: lengths around one and several chunks of 512, both layouts
+    (3, 700, 448, 2), (56, 900, 512, 5), (57, 900, 512, 5), (9, 800, 576, 3), (64, 800, 576, 3), (1, 300, 1088, 1),
+    (130, 1100, 1088, 9), (17, 500, 2112, 4), (300, 600, 2112, 4), (56, 3000, 4096, 12), (140, 2000, 4160, 16),
+    (24, 400, 8128, 6), (70, 400, 8192, 0),
+]
+
+
+@pytest.mark.parametrize("n,V,d,k", CHUNKS)
+def test_chunks_of_the_sums(n, V, d, k):
+    E, y, t = _inputs(n, V, d, n + d)
+    lp, h, ids, top = _run(E, y, t, k)
+    rlp, rh, rids, rtop, _, _ = _reference(E, y, t, k)
+    A = (np.abs(y).astype(np.float64) @ np.abs(E).astype(np.float64).T).max(1)
+    eps = _chunk_eps(A, d) + 2.0 ** -20
+    assert (np.abs(lp - rlp) <= eps + 2.0 ** -24 * np.abs(rlp)).all()
+    assert (np.abs(h - rh) <= eps * (2 + 2 * np.abs(h)) + np.abs(h) * 2.0 ** -20).all()
+    if k:
+        assert np.array_equal(ids, rids)
+        assert (np.abs(top - rtop) <= eps[:, None] + 2.0 ** -24 * np.abs(rtop)).all()

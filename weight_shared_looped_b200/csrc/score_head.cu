@@ -8,9 +8,19 @@
 // Pass 0 splits the activations of each row, scaled by a power of two so that
 // the row's largest lies in [2^9, 2^10), into two fp16 parts, y = hi + lo: 22 bits
 // of each activation, and no row over- or underflows.  Both parts meet the same
-// embedding tile on the tensor cores, so a logit has fp32 accuracy for twice the
-// matrix work (one fp16 part alone would leave errors of 2^-12 per activation in
-// every probability).
+// embedding tile on the tensor cores, for twice the matrix work (one fp16 part alone
+// would leave errors of 2^-12 per activation in every probability).
+//
+// The tensor cores add towards zero.  An addition loses up to 2^-23 of the sum so far, half
+// of that on average, always to the same side, so the loss does not average out over the
+// vocabulary as an fp32 sum's roundings do, and it depends on where along d a logit comes
+// from, so no factor takes it back.  The accumulators therefore hold SC_CHUNK k blocks at a
+// time, and their sums are added in fp32.  Chunks of 2048, 1024, 512, 256 and 128 elements
+// leave rows of d 2048 whose logits of 32 come from one early channel off by 2.8e-4, 1.3e-4,
+// 6.6e-5, 3.1e-5 and 1.4e-5 (row-major; half of it vocabulary-major); 1021 rows with k 3 take
+// 303, 309, 312, 334 and 369 us, 56 rows with k 5 64, 65, 68, 75 and 81.  Chunks of 512 are
+// the shortest that the epilogue keeps up with.
+//
 // Pass 1 streams the embedding through tcgen05 and keeps, per row and slice of
 // the vocabulary, the running maximum m, l = sum e^(z - m), s = sum e^(z - m) (z - m)
 // and the best candidates.
@@ -22,15 +32,14 @@
 // k-th).
 //
 // Bounds (vocabulary 50257, d 2048): few rows by the embedding's 206 MB, 31 us; one row
-// with k 5 takes 47 us (passes 0 and 2 and the fill and tail of pass 1 are 12 of
-// them).  Many rows by the matrix work, twice 2 n V d; 1024 rows in 310 us with k 0,
-// 1.36 PFLOP/s, 324 with k 5 (candidates, merge).  In between the epilogue of the last tiles
-// shows: 128 rows with k 8 take 80 us.
+// with k 5 takes 46 us (passes 0 and 2 and the fill and tail of pass 1 are 12 of
+// them).  Many rows by the matrix work, twice 2 n V d; 1021 rows with k 3 in 311 us,
+// 1.35 PFLOP/s.  In between the epilogue of the last tiles shows: 128 rows with k 8 take
+// 82 us.
 #include <math_constants.h>
 
 #include <algorithm>
 #include <cstring>
-#include <type_traits>
 
 #include "tc_util.cuh"
 
@@ -40,6 +49,8 @@ namespace {
 constexpr int kSpare = 2;          // candidates scored in fp64 beyond k
 constexpr int kMaxCand = 20;       // candidates kept per slice, at most
 constexpr int SC_BK = 64;          // k per stage (one 128-byte swizzled row)
+constexpr int SC_CHUNK = 8;        // k blocks of one accumulator: see above
+static_assert(SC_CHUNK % 2 == 0, "whole stages of up to two k blocks");
 constexpr int kScoreSms = 148;
 
 __device__ __forceinline__ bool sc_better(float x, int v, float bx, int bv) {
@@ -172,6 +183,12 @@ __device__ __forceinline__ void sc_ld_wait(uint32_t* u) {
                :
                : "memory");
 }
+// keeps uses of registers that an earlier wait covers below it
+__device__ __forceinline__ void sc_pin16(uint32_t* u) {
+  asm volatile(""
+               : "+r"(u[0]), "+r"(u[1]), "+r"(u[2]), "+r"(u[3]), "+r"(u[4]), "+r"(u[5]), "+r"(u[6]), "+r"(u[7]),
+                 "+r"(u[8]), "+r"(u[9]), "+r"(u[10]), "+r"(u[11]), "+r"(u[12]), "+r"(u[13]), "+r"(u[14]), "+r"(u[15]));
+}
 // barrier 1 over the eight statistics warps; true for all when `bad` is for any
 __device__ __forceinline__ bool sc_barrier_or(bool bad) {
   uint32_t any;
@@ -192,16 +209,18 @@ struct ScoreTc {
   int mt, groups;         // row tiles; CTAs that share one row tile's vocabulary tiles
   int stages;
   uint32_t stage_bytes;
-  int kbs;                // vocabulary-major: k blocks per stage
   int slices;             // records per row
-  float log2e;            // of pass 1's logits: see score_plan
+  int slots;              // vocabulary-major: accumulators in TMEM
   const float* scale;
   ScoreRec rec;
   int* flag;              // set when a bounded wait ran out
 };
 
+constexpr int SC_SLOTS = 8;        // accumulators of a CTA, at most
+constexpr float kLog2e = 1.4426950408889634f;
+
 struct ScoreBars {
-  uint64_t full[12], empty[12], acc_full[2], acc_empty[2];
+  uint64_t full[12], empty[12], acc_full[SC_SLOTS], acc_empty[SC_SLOTS];
   uint32_t tmem;
   int abort;
 };
@@ -210,10 +229,27 @@ struct ScoreBars {
 // bn vocabulary entries its N side, so an epilogue thread owns one row and walks
 // its logits: the softmax statistics and the candidate list live in registers.
 // Warps 0-7 read the accumulators (warp w: TMEM quadrant w mod 4, column half
-// w / 4), warp 8 copies, warp 9 issues the MMAs; two accumulators of 256 columns
-// let the epilogue of one tile run under the next tile's MMAs.
-constexpr int SR_THREADS = 320;
-constexpr int SR_QUEUE = 12;       // newcomers a statistics thread can hold
+// w / 4) and add up a tile's chunks, warp 8 copies, warp 9 issues the MMAs; two
+// accumulators of 256 columns let the epilogue of one tile run under the next
+// tile's MMAs.
+constexpr int SR_THREADS = 384;    // three warpgroups; the last one's other two warps idle
+// A statistics thread holds the 128 logits of its half tile, so that an accumulator is free
+// again once it is read; its warpgroups take registers that the issuing one gives up.
+constexpr int SR_REGS = 168;       // a thread's registers at launch: the launch bounds' share of the SM
+constexpr int SR_REGS_STAT = 232, SR_REGS_ISSUE = 40;
+static_assert(2 * SR_REGS_STAT + SR_REGS_ISSUE <= 3 * SR_REGS, "no more than the block was launched with");
+constexpr int SR_QUEUE = 16;       // newcomers a statistics thread can hold
+
+// A logit above `bar` goes to the queue at `at`, whose entries are 256 threads apart.
+// (Written out: the compiler branches around the store.)
+__device__ __forceinline__ void sc_push(uint32_t& at, float x, float bar, int id) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.gt.f32 p, %1, %2;\n @p st.shared.v2.b32 [%0], {%3, %4};\n"
+      " @p add.u32 %0, %0, 2048;\n}\n"
+      : "+r"(at)
+      : "f"(x), "f"(bar), "r"(__float_as_uint(x)), "r"(id)
+      : "memory");
+}
 
 template <int KC>
 __global__ void __launch_bounds__(SR_THREADS, 1)
@@ -248,76 +284,82 @@ __global__ void __launch_bounds__(SR_THREADS, 1)
   const uint32_t tmem = bars.tmem;
   pdl_enter();
 
-  if (warp == 8) {
-    // ---------------------------------------------------------------- copies
-    if (lane == 0) {
-      int s = 0, ph = 1, issued = 0;
-      bool ok = true;
-      const int r0 = mt * 128;
-      for (int vt = group; vt < a.vt && ok; vt += a.groups) {
-        const int v0 = vt * a.bn;
-        for (int kb = 0; kb < a.nkb; ++kb) {
-          if (issued >= a.stages && !sc_wait(&bars.empty[s], ph, &bars.abort)) {
-            ok = false;
-            break;
-          }
-          uint8_t* st = smem + (size_t)s * a.stage_bytes;
-          sc_expect(&bars.full[s], a.stage_bytes);
-          sc_copy(&bars.full[s], st, &map_y, kb * SC_BK, r0);
-          sc_copy(&bars.full[s], st + 16384, &map_y, kb * SC_BK, a.pad + r0);
-          sc_copy(&bars.full[s], st + 32768, &map_e, kb * SC_BK, v0);
-          ++issued;
-          if (++s == a.stages) {
-            s = 0;
-            ph ^= 1;
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(SR_REGS_ISSUE));
+    if (warp == 8) {
+      // ---------------------------------------------------------------- copies
+      if (lane == 0) {
+        int s = 0, ph = 1, issued = 0;
+        bool ok = true;
+        const int r0 = mt * 128;
+        for (int vt = group; vt < a.vt && ok; vt += a.groups) {
+          const int v0 = vt * a.bn;
+          for (int kb = 0; kb < a.nkb; ++kb) {
+            if (issued >= a.stages && !sc_wait(&bars.empty[s], ph, &bars.abort)) {
+              ok = false;
+              break;
+            }
+            uint8_t* st = smem + (size_t)s * a.stage_bytes;
+            sc_expect(&bars.full[s], a.stage_bytes);
+            sc_copy(&bars.full[s], st, &map_y, kb * SC_BK, r0);
+            sc_copy(&bars.full[s], st + 16384, &map_y, kb * SC_BK, a.pad + r0);
+            sc_copy(&bars.full[s], st + 32768, &map_e, kb * SC_BK, v0);
+            ++issued;
+            if (++s == a.stages) {
+              s = 0;
+              ph ^= 1;
+            }
           }
         }
+        if (!ok) atomicExch(&bars.abort, 1);
+        if (*(volatile int*)&bars.abort)               // the copies still in flight land before the CTA leaves
+          for (int i = max(0, issued - a.stages); i < issued; ++i) mbar_wait(&bars.full[i % a.stages], (i / a.stages) & 1);
       }
-      if (!ok) atomicExch(&bars.abort, 1);
-      if (*(volatile int*)&bars.abort)               // the copies still in flight land before the CTA leaves
-        for (int i = max(0, issued - a.stages); i < issued; ++i) mbar_wait(&bars.full[i % a.stages], (i / a.stages) & 1);
-    }
-    __syncwarp();
-  } else if (warp == 9) {
-    // ---------------------------------------------------------------- MMAs
-    if (lane == 0) {
-      const uint32_t idesc = (1u << 4) | ((uint32_t)(a.bn >> 3) << 17) | (8u << 24);
-      const uint64_t desc0 = smem_desc_sw128(smem_u32(smem));   // + stage bytes / 16 per stage: stays below 2^14
-      int s = 0, ph = 0, i = 0;
-      bool ok = true;
-      for (int vt = group; vt < a.vt && ok; vt += a.groups, ++i) {
-        const int buf = i & 1, use = i >> 1;
-        if (use > 0) ok = sc_wait(&bars.acc_empty[buf], (use & 1) ^ 1, &bars.abort);
-        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        const uint32_t acc = tmem + buf * 256;
-        for (int kb = 0; kb < a.nkb && ok; ++kb) {
-          ok = sc_wait(&bars.full[s], ph, &bars.abort);
-          if (!ok) break;
-          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-          const uint64_t hi = desc0 + (uint64_t)(s * (a.stage_bytes >> 4)), lo = hi + (16384 >> 4), e = hi + (32768 >> 4);
+      __syncwarp();
+    } else if (warp == 9) {
+      // ---------------------------------------------------------------- MMAs
+      if (lane == 0) {
+        const uint32_t idesc = (1u << 4) | ((uint32_t)(a.bn >> 3) << 17) | (8u << 24);
+        const uint64_t desc0 = smem_desc_sw128(smem_u32(smem));   // + stage bytes / 16 per stage: stays below 2^14
+        int s = 0, ph = 0, i = 0;
+        bool ok = true;
+        for (int vt = group; vt < a.vt && ok; vt += a.groups) {
+          for (int k0 = 0; k0 < a.nkb && ok; k0 += SC_CHUNK, ++i) {
+            const int buf = i & 1, use = i >> 1;
+            if (use > 0) ok = sc_wait(&bars.acc_empty[buf], (use & 1) ^ 1, &bars.abort);
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            const uint32_t acc = tmem + buf * 256;
+            for (int kb = k0; kb < min(k0 + SC_CHUNK, a.nkb) && ok; ++kb) {
+              ok = sc_wait(&bars.full[s], ph, &bars.abort);
+              if (!ok) break;
+              asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+              const uint64_t hi = desc0 + (uint64_t)(s * (a.stage_bytes >> 4)), lo = hi + (16384 >> 4), e = hi + (32768 >> 4);
+              // the small parts first: their additions lose next to nothing in an empty accumulator
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks) {
-            sc_mma(acc, hi + 2 * ks, e + 2 * ks, idesc, (kb | ks) != 0);
-            sc_mma(acc, lo + 2 * ks, e + 2 * ks, idesc, true);
-          }
-          sc_commit(&bars.empty[s]);
-          if (++s == a.stages) {
-            s = 0;
-            ph ^= 1;
+              for (int ks = 0; ks < 4; ++ks) sc_mma(acc, lo + 2 * ks, e + 2 * ks, idesc, kb != k0 || ks != 0);
+#pragma unroll
+              for (int ks = 0; ks < 4; ++ks) sc_mma(acc, hi + 2 * ks, e + 2 * ks, idesc, true);
+              sc_commit(&bars.empty[s]);
+              if (++s == a.stages) {
+                s = 0;
+                ph ^= 1;
+              }
+            }
+            if (ok) sc_commit(&bars.acc_full[buf]);
           }
         }
-        if (ok) sc_commit(&bars.acc_full[buf]);
+        if (!ok) atomicExch(&bars.abort, 1);
       }
-      if (!ok) atomicExch(&bars.abort, 1);
+      __syncwarp();
     }
-    __syncwarp();
   } else {
     // ---------------------------------------------------------------- statistics
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(SR_REGS_STAT));
     const int half = warp >> 2, r = (warp & 3) * 32 + lane;
     const uint32_t laddr = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const int cols = a.bn / 2;                         // a multiple of 16
     const int row = mt * 128 + r;
-    const float rs = row < a.n ? a.scale[row] : 1.f, rs2 = rs * a.log2e;
+    const float rs = row < a.n ? a.scale[row] : 1.f, rs2 = rs * kLog2e;
     float m = -INFINITY, l = 0.f, sx = 0.f;            // in log2 units
     // the row's best so far, and a queue of newcomers in shared memory: logits
     // above the list's last are queued (a predicated store each) and inserted when
@@ -330,96 +372,125 @@ __global__ void __launch_bounds__(SR_THREADS, 1)
       cx[p] = -INFINITY;
       cv[p] = 0x7fffffff;
     }
-    uint2* queue = reinterpret_cast<uint2*>(smem + (size_t)a.stages * a.stage_bytes) + threadIdx.x;   // [SR_QUEUE][256]
-    int queued = 0;
+    const uint32_t queue = smem_u32(smem + (size_t)a.stages * a.stage_bytes) + 8 * threadIdx.x;   // [SR_QUEUE][256]
+    uint32_t at = queue;
     auto drain = [&]() {
-      const int most = __reduce_max_sync(0xffffffffu, queued);
-      for (int q = 0; q < most; ++q) {
-        const uint2 w = q < queued ? queue[q * 256] : make_uint2(0xff800000u, 0u);
-        const float xv = __uint_as_float(w.x);
-        const int id = (int)w.y;
+      const uint32_t end = __reduce_max_sync(0xffffffffu, at - queue) + queue;
+#pragma unroll 1
+      for (uint32_t q = queue; q < end; q += 2048) {
+        uint32_t xb, id;
+        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(xb), "=r"(id) : "r"(q) : "memory");
+        const float xv = q < at ? __uint_as_float(xb) : -INFINITY;
         // an equal entry seen earlier (a lower id) stays before
 #pragma unroll
         for (int p = KC - 1; p > 0; --p) {
           const bool up = xv > cx[p - 1], in = xv > cx[p];
-          cv[p] = up ? cv[p - 1] : in ? id : cv[p];
+          cv[p] = up ? cv[p - 1] : in ? (int)id : cv[p];
           cx[p] = up ? cx[p - 1] : in ? xv : cx[p];
         }
         if (xv > cx[0]) {
           cx[0] = xv;
-          cv[0] = id;
+          cv[0] = (int)id;
         }
       }
-      queued = 0;
+      at = queue;
     };
     bool ok = true;
     int i = 0;
-    for (int vt = group; vt < a.vt; vt += a.groups, ++i) {
-      const int buf = i & 1, use = i >> 1;
-      if (!warp_wait(&bars.acc_full[buf], use & 1, &bars.abort, true)) {
-        if (lane == 0) atomicExch(&bars.abort, 1);
-        ok = false;
-        break;
+    uint32_t z[128];                                   // the tile's logits (fp32)
+    for (int vt = group; vt < a.vt && ok; vt += a.groups) {
+      for (int k0 = 0; k0 < a.nkb; k0 += SC_CHUNK, ++i) {
+        const int buf = i & 1, use = i >> 1;
+        if (!warp_wait(&bars.acc_full[buf], use & 1, &bars.abort, true)) {
+          if (lane == 0) atomicExch(&bars.abort, 1);
+          ok = false;
+          break;
+        }
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        const uint32_t base = laddr + buf * 256 + half * cols;
+        if (k0 == 0) {
+#pragma unroll
+          for (int b = 0; b < 8; ++b)
+            if (16 * b < cols) sc_ld16(z + 16 * b, base + 16 * b);
+          sc_ld_wait(z);
+#pragma unroll
+          for (int b = 1; b < 8; ++b) sc_pin16(z + 16 * b);
+        } else {
+          uint32_t w[2][16];
+          sc_ld16(w[0], base);
+#pragma unroll
+          for (int b = 0; b < 8; ++b) {
+            if (16 * b < cols) {
+              sc_ld_wait(w[b & 1]);
+              if (16 * b + 16 < cols) sc_ld16(w[(b & 1) ^ 1], base + 16 * b + 16);
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                z[16 * b + j] = __float_as_uint(__uint_as_float(z[16 * b + j]) + __uint_as_float(w[b & 1][j]));
+            }
+          }
+        }
+        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.acc_empty[buf]);
       }
-      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      if (!ok) break;
       const int v0 = vt * a.bn + half * cols;
       const int valid = min(cols, a.V - v0);           // may be <= 0 in the last tile
-      uint32_t w[2][16];
-      const uint32_t base = laddr + buf * 256 + half * cols;
-      sc_ld16(w[0], base);
-#pragma unroll 1
-      for (int c = 0; c < cols; c += 32) {
+      // 32 logits, z[z0] and on; two chains of sums, so that they wait less for each other
+      auto take = [&](int c, int z0) {
+        const int nv = min(cols, valid) - c;           // uniform over the warp
+        if (nv <= 0) return;
+        if (nv < 32)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int c0 = c + 16 * h;
-          if (c0 >= cols) break;
-          sc_ld_wait(w[h]);
-          if (c0 + 16 < cols) sc_ld16(w[h ^ 1], base + c0 + 16);
-          // 16 logits, all of them entries of the vocabulary except at its end (a test per
-          // logit took 5 % of 1021 rows of d 256, where the epilogue is what counts)
-          auto take = [&](auto full, int nv) {
-            constexpr bool all = decltype(full)::value;
-            float x[16];
-            float top = -INFINITY;
+          for (int j = 0; j < 32; ++j)
+            if (j >= nv) z[z0 + j] = 0xff800000u;           // below every logit
+        auto x = [&](int j) { return __uint_as_float(z[z0 + j]); };
+        float top4[4] = {x(0), x(1), x(2), x(3)};
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              x[j] = __uint_as_float(w[h][j]);
-              if (all || j < nv) top = fmaxf(top, x[j]);
-            }
-            const float top2 = top * rs2;
-            if (top2 > m) {
-              const float f = sc_ex2(m - top2);
-              sx = l == 0.f ? 0.f : (sx + l * (m - top2)) * f;
-              l *= f;
-              m = top2;
-            }
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              if (all || j < nv) {
-                const float t = fmaf(x[j], rs2, -m), e = sc_ex2(t);
-                l += e;
-                sx = fmaf(e, t, sx);
-              }
-            }
-            if (__any_sync(0xffffffffu, top > cx[KC - 1])) {
-#pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                if ((j & 3) == 0 && __any_sync(0xffffffffu, queued > SR_QUEUE - 4)) drain();
-                if ((all || j < nv) && x[j] > cx[KC - 1]) {
-                  queue[queued * 256] = make_uint2(__float_as_uint(x[j]), (uint32_t)(v0 + c0 + j));
-                  ++queued;
-                }
-              }
-            }
-          };
-          const int nv = valid - c0;                   // uniform over the warp
-          if (nv >= 16) take(std::true_type{}, 16);
-          else if (nv > 0) take(std::false_type{}, nv);
+        for (int j = 4; j < 32; ++j) top4[j & 3] = fmaxf(top4[j & 3], x(j));
+        const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
+        const float top2 = top * rs2;
+        if (top2 > m) {
+          const float f = sc_ex2(m - top2);
+          sx = l == 0.f ? 0.f : (sx + l * (m - top2)) * f;
+          l *= f;
+          m = top2;
         }
+        float l2[2] = {0.f, 0.f}, s2[2] = {0.f, 0.f};
+        if (nv >= 32) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const float t = fmaf(x(j), rs2, -m), e = sc_ex2(t);
+            l2[j & 1] += e;
+            s2[j & 1] = fmaf(e, t, s2[j & 1]);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {               // e = 0 where there is no logit
+            const float t = j < nv ? fmaf(x(j), rs2, -m) : -1e4f, e = sc_ex2(t);
+            l2[j & 1] += e;
+            s2[j & 1] = fmaf(e, t, s2[j & 1]);
+          }
+        }
+        l += l2[0] + l2[1];
+        sx += s2[0] + s2[1];
+        if (__any_sync(0xffffffffu, top > cx[KC - 1])) {
+          const int id = v0 + c;
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            if (__any_sync(0xffffffffu, at > queue + 2048 * (SR_QUEUE - 8))) drain();
+#pragma unroll
+            for (int j = 8 * g; j < 8 * g + 8; ++j) sc_push(at, x(j), cx[KC - 1], id + j);
+          }
+        }
+      };
+#pragma unroll 1
+      for (int c = 0; c < cols; c += 64) {
+        take(c, 0);
+        take(c + 32, 32);
+#pragma unroll
+        for (int j = 0; j < 64; ++j) z[j] = z[j + 64];   // the other half to the front
       }
-      asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars.acc_empty[buf]);
     }
     drain();
     if (row < a.n) {
@@ -448,7 +519,8 @@ __global__ void __launch_bounds__(SR_THREADS, 1)
 // embedding once.  The epilogue adds the two parts, transposes the logits
 // through shared memory and gives each row to a warp.
 constexpr int SV_THREADS = 320;
-constexpr int SV_MAX_ROWS = 64;
+constexpr int SV_MAX_ROWS = 56;
+constexpr int SV_KBS = 2;          // k blocks per stage
 
 template <int KC>
 __global__ void __launch_bounds__(SV_THREADS, 1)
@@ -470,7 +542,7 @@ __global__ void __launch_bounds__(SV_THREADS, 1)
       mbar_init(&bars.full[s], 1);
       mbar_init(&bars.empty[s], 1);
     }
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < a.slots; ++s) {
       mbar_init(&bars.acc_full[s], 1);
       mbar_init(&bars.acc_empty[s], 4);
     }
@@ -479,7 +551,7 @@ __global__ void __launch_bounds__(SV_THREADS, 1)
   }
   __syncwarp();
   if (warp == 9) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 256;" ::"r"(smem_u32(&bars.tmem)));
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&bars.tmem)));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
   for (int i = threadIdx.x; i < SV_MAX_ROWS; i += SV_THREADS) {
@@ -495,18 +567,19 @@ __global__ void __launch_bounds__(SV_THREADS, 1)
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = bars.tmem;
   const uint32_t ybytes = (uint32_t)(2 * tp) * 128, ebytes = (uint32_t)a.bn * 128;
+  const uint32_t slot_cols = (uint32_t)(2 * tp + 31) & ~31u;
 
-  // A stage holds up to kbs k blocks: their embedding rows (16 KB each), then their
+  // A stage holds up to two k blocks: their embedding rows (16 KB each), then their
   // activations.
-  const uint32_t ybase = (uint32_t)a.kbs * 16384, ystep = (ybytes + 1023) & ~1023u;
-  const int spt = (a.nkb + a.kbs - 1) / a.kbs;       // stages per tile
+  const uint32_t ybase = SV_KBS * 16384, ystep = (ybytes + 1023) & ~1023u;
+  const int spt = (a.nkb + SV_KBS - 1) / SV_KBS;       // stages per tile
   if (warp == 8) {
     if (lane == 0) {
       const int total = (a.vt - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x * spt;
       const int v_step = (int)gridDim.x * a.bn;
       auto copy_e = [&](int s, int k0, int v0) {     // expect the stage, request its embedding rows
         uint8_t* sp = smem + (size_t)s * a.stage_bytes;
-        const bool two = a.kbs == 2 && k0 + 1 < a.nkb;
+        const bool two = k0 + 1 < a.nkb;
         sc_expect(&bars.full[s], two ? 2 * (ybytes + ebytes) : ybytes + ebytes);
         sc_copy(&bars.full[s], sp, &map_e, k0 * SC_BK, v0);
         if (two) sc_copy(&bars.full[s], sp + 16384, &map_e, (k0 + 1) * SC_BK, v0);
@@ -517,7 +590,7 @@ __global__ void __launch_bounds__(SV_THREADS, 1)
       int k0 = 0, v0 = (int)blockIdx.x * a.bn;
       for (int i = 0; i < ahead; ++i) {
         copy_e(i, k0, v0);
-        if ((k0 += a.kbs) >= a.nkb) {
+        if ((k0 += SV_KBS) >= a.nkb) {
           k0 = 0;
           v0 += v_step;
         }
@@ -531,15 +604,15 @@ __global__ void __launch_bounds__(SV_THREADS, 1)
             break;
           }
           copy_e(s, k0, v0);
-          if ((k0 += a.kbs) >= a.nkb) {
+          if ((k0 += SV_KBS) >= a.nkb) {
             k0 = 0;
             v0 += v_step;
           }
         }
         uint8_t* sp = smem + (size_t)s * a.stage_bytes + ybase;
         sc_copy(&bars.full[s], sp, &map_y, ky * SC_BK, 0);
-        if (a.kbs == 2 && ky + 1 < a.nkb) sc_copy(&bars.full[s], sp + ystep, &map_y, (ky + 1) * SC_BK, 0);
-        if ((ky += a.kbs) >= a.nkb) ky = 0;
+        if (ky + 1 < a.nkb) sc_copy(&bars.full[s], sp + ystep, &map_y, (ky + 1) * SC_BK, 0);
+        if ((ky += SV_KBS) >= a.nkb) ky = 0;
         if (++s == a.stages) {
           s = 0;
           ph ^= 1;
@@ -554,31 +627,38 @@ __global__ void __launch_bounds__(SV_THREADS, 1)
       pdl_enter();
       const uint32_t idesc = (1u << 4) | ((uint32_t)(2 * tp >> 3) << 17) | (8u << 24);
       const uint64_t desc0 = smem_desc_sw128(smem_u32(smem));
-      int s = 0, ph = 0, j = 0;
+      int s = 0, ph = 0, slot = 0, slot_ph = 1, used = 0;
       bool ok = true;
-      for (int t = blockIdx.x; t < a.vt && ok; t += gridDim.x, ++j) {
-        const int buf = j & 1, use = j >> 1;
-        if (use > 0) ok = sc_wait(&bars.acc_empty[buf], (use & 1) ^ 1, &bars.abort);
-        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        for (int k0 = 0; k0 < a.nkb && ok; k0 += a.kbs) {
-          ok = sc_wait(&bars.full[s], ph, &bars.abort);
-          if (!ok) break;
+      for (int t = blockIdx.x; t < a.vt && ok; t += gridDim.x) {
+        for (int c0 = 0; c0 < a.nkb && ok; c0 += SC_CHUNK) {
+          if (used >= a.slots) ok = sc_wait(&bars.acc_empty[slot], slot_ph, &bars.abort);
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-          const uint64_t e0 = desc0 + (uint64_t)(s * (a.stage_bytes >> 4)), y0 = e0 + (ybase >> 4);
+          const uint32_t acc = tmem + slot * slot_cols;
+          for (int k0 = c0; k0 < min(c0 + SC_CHUNK, a.nkb) && ok; k0 += SV_KBS) {
+            ok = sc_wait(&bars.full[s], ph, &bars.abort);
+            if (!ok) break;
+            asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+            const uint64_t e0 = desc0 + (uint64_t)(s * (a.stage_bytes >> 4)), y0 = e0 + (ybase >> 4);
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks) sc_mma(tmem + buf * 128, e0 + 2 * ks, y0 + 2 * ks, idesc, (k0 | ks) != 0);
-          if (a.kbs == 2 && k0 + 1 < a.nkb) {
-            const uint64_t e1 = e0 + (16384 >> 4), y1 = y0 + (ystep >> 4);
+            for (int ks = 0; ks < 4; ++ks) sc_mma(acc, e0 + 2 * ks, y0 + 2 * ks, idesc, k0 != c0 || ks != 0);
+            if (k0 + 1 < a.nkb) {
+              const uint64_t e1 = e0 + (16384 >> 4), y1 = y0 + (ystep >> 4);
 #pragma unroll
-            for (int ks = 0; ks < 4; ++ks) sc_mma(tmem + buf * 128, e1 + 2 * ks, y1 + 2 * ks, idesc, true);
+              for (int ks = 0; ks < 4; ++ks) sc_mma(acc, e1 + 2 * ks, y1 + 2 * ks, idesc, true);
+            }
+            sc_commit(&bars.empty[s]);
+            if (++s == a.stages) {
+              s = 0;
+              ph ^= 1;
+            }
           }
-          sc_commit(&bars.empty[s]);
-          if (++s == a.stages) {
-            s = 0;
-            ph ^= 1;
+          if (ok) sc_commit(&bars.acc_full[slot]);
+          ++used;
+          if (++slot == a.slots) {
+            slot = 0;
+            slot_ph ^= 1;
           }
         }
-        if (ok) sc_commit(&bars.acc_full[buf]);
       }
       if (!ok) atomicExch(&bars.abort, 1);
     }
@@ -587,31 +667,41 @@ __global__ void __launch_bounds__(SV_THREADS, 1)
     pdl_enter();
     const uint32_t laddr = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     bool ok = true;
-    int j = 0;
-    for (int t = blockIdx.x; t < a.vt; t += gridDim.x, ++j) {
-      const int buf = j & 1, use = j >> 1;
+    int slot = 0, slot_ph = 0;
+    for (int t = blockIdx.x; t < a.vt; t += gridDim.x) {
       if (warp < 4) {
-        ok = warp_wait(&bars.acc_full[buf], use & 1, &bars.abort, true);
-        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        if (ok) {
-          for (int c = 0; c < tp; c += 8) {
-            uint32_t hl[16];                             // hi, then lo
+        float z[64];                                     // an entry's logits
+        for (int c0 = 0; c0 < a.nkb; c0 += SC_CHUNK) {
+          ok = warp_wait(&bars.acc_full[slot], slot_ph, &bars.abort, true);
+          if (!ok) break;
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              uint32_t* d = hl + 8 * q;
-              asm volatile(
-                  "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                  : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3]), "=r"(d[4]), "=r"(d[5]), "=r"(d[6]), "=r"(d[7])
-                  : "r"(laddr + buf * 128 + c + q * tp));
+          for (int c = 0; c < 64; c += 16) {
+            if (c >= tp) continue;
+            // hi and lo of 16 rows; the last eight may be the next part's or none's, not used
+            uint32_t hi[16], lo[16];
+            sc_ld16(hi, laddr + slot * slot_cols + c);
+            sc_ld16(lo, laddr + slot * slot_cols + c + tp);
+            sc_ld_wait(hi);
+            sc_pin16(lo);
+#pragma unroll
+            for (int q = 0; q < 16; ++q) {
+              const float x = __uint_as_float(hi[q]) + __uint_as_float(lo[q]);
+              z[c + q] = c0 == 0 ? x : z[c + q] + x;
             }
-            sc_ld_wait(hl);
-#pragma unroll
-            for (int q = 0; q < 8; ++q)
-              zb[(c + q) * ZLD + warp * 32 + lane] = __uint_as_float(hl[q]) + __uint_as_float(hl[8 + q]);
           }
           asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
           __syncwarp();
-          if (lane == 0) mbar_arrive(&bars.acc_empty[buf]);
+          if (lane == 0) mbar_arrive(&bars.acc_empty[slot]);
+          if (++slot == a.slots) {
+            slot = 0;
+            slot_ph ^= 1;
+          }
+        }
+        if (ok) {
+#pragma unroll
+          for (int c = 0; c < SV_MAX_ROWS; ++c)
+            if (c < tp) zb[c * ZLD + warp * 32 + lane] = z[c];
         } else if (lane == 0) {
           atomicExch(&bars.abort, 1);
         }
@@ -619,7 +709,7 @@ __global__ void __launch_bounds__(SV_THREADS, 1)
       if (sc_barrier_or(!ok)) break;
       const int v0 = t * a.bn, valid = min(a.bn, a.V - v0);
       for (int row = warp; row < a.n; row += 8) {
-        const float rs = a.scale[row], rs2 = rs * a.log2e;
+        const float rs = a.scale[row], rs2 = rs * kLog2e;
         float x[4], top = -INFINITY;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -734,7 +824,7 @@ __global__ void __launch_bounds__(SV_THREADS, 1)
   __syncthreads();
   if (warp == 9) {
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 256;" ::"r"(tmem));
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
   }
   if (threadIdx.x == 0 && bars.abort) atomicExch(a.flag, 1);
 }
@@ -761,21 +851,17 @@ __device__ __forceinline__ void score_not_finite(const ScoreArgs& a, int row, in
 }
 
 // One warp: a row's outputs from its statistics, its chosen tokens (ids, logits by pass 1
-// in `fast`, by fp64 in zs) and the given token's logit zs[n_pick].
-//
-// The tensor cores add towards zero.  For the many small logits log2e makes up for that
-// on average; where one token has most of the probability, the sum of its products does
-// not wander but grows, and loses up to d 2^-28 of itself and more.  The chosen tokens'
-// terms of the sums are replaced by those of their fp64 logits.
+// in `fast`, by fp64 in zs) and the given token's logit zs[n_pick].  Where a few tokens
+// have most of the probability, the errors of their pass 1 logits are what the sums are
+// off by: the chosen tokens' terms are replaced by those of their fp64 logits.
 __device__ __forceinline__ void score_finish(const ScoreArgs& a, int row, float M, float L, float S, int n_pick,
-                                             int target, const double* zs, const int* ids, const float* fast,
-                                             float log2e) {
+                                             int target, const double* zs, const int* ids, const float* fast) {
   constexpr double kLn2 = 0.693147180559945309;
   const int lane = threadIdx.x & 31;
   double dl = 0.0, ds = 0.0;
   if (lane < n_pick) {
     // t0 as pass 1 had it.  e^t1 - e^t0 from the difference: both corrections need few bits
-    const double t1 = zs[lane] / kLn2 - (double)M, t0 = (double)fast[lane] * (double)log2e - (double)M;
+    const double t1 = zs[lane] / kLn2 - (double)M, t0 = (double)fast[lane] * (double)kLog2e - (double)M;
     const float e0 = exp2f((float)t0), step = (float)((t1 - t0) * kLn2);
     dl = (double)e0 * (double)expm1f(step);
     ds = dl * t1 + (double)e0 * (t1 - t0);
@@ -989,7 +1075,7 @@ __global__ void __launch_bounds__(SM_THREADS, 3) score_merge_kernel(ScoreArgs a,
     }
   }
   __syncthreads();
-  if (warp == 0) score_finish(a, row, M, L, S, n_pick, target, zs, ids, fast, tc.log2e);
+  if (warp == 0) score_finish(a, row, M, L, S, n_pick, target, zs, ids, fast);
 }
 
 // The same with a warp per row, for more rows than the CTA form has places for at once
@@ -1163,7 +1249,7 @@ __global__ void __launch_bounds__(32 * SW_WARPS) score_merge_rows_kernel(ScoreAr
     }
   }
   __syncwarp();
-  score_finish(a, row, M, L, S, n_pick, target, zs, ids, fast, tc.log2e);
+  score_finish(a, row, M, L, S, n_pick, target, zs, ids, fast);
 }
 
 size_t score_merge_smem(int slices, int kc, int d) { return (size_t)d * 8 + (size_t)slices * kc * sizeof(ScoreCand); }
@@ -1184,10 +1270,10 @@ struct ScorePlan {
   size_t smem, parts_off, scale_off, flag_off, stat_off, top_x_off, top_v_off, bytes;
 };
 
-// Up to 64 rows the embedding streams as the M side (its bytes are the bound); above,
+// Up to 56 rows the embedding streams as the M side (its bytes are the bound); above,
 // the rows are (the matrix work is).  Vocabulary 50257, d 2048, k 5, vocabulary-major
-// and row-major:  8 rows 52 and 69 us, 32 rows 56 and 71, 64 rows 69 and 73 (128
-// columns, the accumulator's size; 128 rows row-major 76).
+// and row-major:  8 rows 51 and 66 us, 32 rows 55 and 68, 48 rows 63 and 69, 56 rows 68
+// and 70, 64 rows 73 and 71 (128 rows row-major 74).
 ScorePlan score_plan(int n, int V, int d, int k) {
   ScorePlan p;
   memset(&p, 0, sizeof(p));
@@ -1204,15 +1290,13 @@ ScorePlan score_plan(int n, int V, int d, int k) {
     t.vt = (V + t.bn - 1) / t.bn;
     p.grid = std::min(kScoreSms, t.vt);
     t.slices = p.grid;
-    // Two k blocks per stage while three such stages fit: a stage costs its copying
-    // thread about 0.25 us however small, as long as a k block's rows take from HBM.
-    // One and two blocks: 1 row 49 and 47 us, 32 rows 60 and 56, 56 rows 66 and 65; at 64
-    // rows two stages of two lose, 69 and 71.
+    // Two k blocks per stage: a stage costs its copying thread about 0.25 us however
+    // small, as long as a k block's rows take from HBM.  One and two blocks: 1 row 49 and
+    // 47 us, 32 rows 60 and 56.  At least three stages fit.
     const size_t zb = (size_t)t.pad * 132 * 4;
-    const uint32_t block = 16384 + (uint32_t)(2 * t.pad * 128 + 1023) / 1024 * 1024;
-    t.kbs = 3 * 2 * (size_t)block + zb + 1024 <= kVocabSmem ? 2 : 1;
-    t.stage_bytes = (uint32_t)t.kbs * block;
+    t.stage_bytes = SV_KBS * (16384 + (uint32_t)(2 * t.pad * 128 + 1023) / 1024 * 1024);
     t.stages = (int)std::min<size_t>(12, (kVocabSmem - zb - 1024) / t.stage_bytes);
+    t.slots = std::min(SC_SLOTS, 512 / ((2 * t.pad + 31) / 32 * 32));
     p.smem = 1024 + (size_t)t.stages * t.stage_bytes + zb;
   } else {
     t.pad = (n + 127) / 128 * 128;
@@ -1220,10 +1304,10 @@ ScorePlan score_plan(int n, int V, int d, int k) {
     t.groups = kScoreSms / t.mt;
     // The tile width (a multiple of 32) with the least work on the busiest CTA, counting
     // a tile's fixed cost (its activations' copies, the first k blocks' latency) as 48
-    // columns.  Measured at every width: 50257 entries take 128 rows 93 us by 96, 76 by
-    // 192, 83 by 256, and 512 rows 212 by 160 and 189 by 256; 2000 entries take 128 rows
-    // 38 by 32 and 52 by 256.  The rule is within 5 % of the best width in all of 40
-    // combinations of 5 vocabularies and 8 batches, 0.2 % on average.
+    // columns.  Measured at every width: 50257 entries take 128 rows 96 us by 96, 74 by
+    // 192, 82 by 256, and 512 rows 207 by 160 and 180 by 256; 2000 entries take 128 rows
+    // 36 by 32 and 45 by 256.  The rule is within 7 % of the best width in all of 40
+    // combinations of 4 vocabularies, 5 batches and d 512 and 2048, 0.7 % on average.
     long best = -1;
     for (int bn = 256; bn >= 32; bn -= 32) {
       const int vt = (V + bn - 1) / bn;
@@ -1242,14 +1326,6 @@ ScorePlan score_plan(int n, int V, int d, int k) {
     t.stages = (int)std::min<size_t>(12, (kRowsSmem - queue - 1024) / t.stage_bytes);
     p.smem = 1024 + (size_t)t.stages * t.stage_bytes + queue;
   }
-  // The tensor cores add towards zero, so a logit of N additions whose partial sums
-  // wander at random loses z sum_i (i / N) 0.72 2^-24 = 0.36 N 2^-24 z on average (half a
-  // unit of a partial sum whose mantissa is spread by Benford's law, of expected size z i
-  // / N); N = d / 16, row-major twice that.  Measured: 0.29 d 2^-28 and 0.57 d 2^-28, within
-  // 0.02 d 2^-28 for d from 256 to 8192, 8 to 256 rows and 60 to 20000 entries.  The factor on
-  // the way to the exponentials takes that back (1021 rows of d 2048: the mean error of
-  // logp was 3.0e-6).
-  t.log2e = (float)(1.4426950408889634 * (1.0 + (p.by_rows ? 0.57 : 0.29) * d / 268435456.0));
   auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
   p.parts_off = 0;
   p.scale_off = up((size_t)2 * t.pad * d * 2);
@@ -1268,6 +1344,11 @@ tl_status launch_score_pass1(const ScorePlan& p, const CUtensorMap& my, const CU
   TL_TRY(once_per_device(attr_done, []() -> tl_status {
     TL_CUDA(cudaFuncSetAttribute(score_rows_kernel<KC>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRowsSmem));
     TL_CUDA(cudaFuncSetAttribute(score_vocab_kernel<KC>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kVocabSmem));
+    // with fewer registers at launch the statistics warpgroups would wait for the rest for good
+    cudaFuncAttributes fa;
+    TL_CUDA(cudaFuncGetAttributes(&fa, score_rows_kernel<KC>));
+    if (fa.numRegs < SR_REGS)
+      return set_error(TL_ERR_CUDA, "score_rows_kernel was built with %d registers, not %d", fa.numRegs, SR_REGS);
     return ok();
   }));
   if (p.by_rows) TL_LAUNCH_PDL(score_rows_kernel<KC>, p.grid, SR_THREADS, p.smem, s, my, me, p.t);
