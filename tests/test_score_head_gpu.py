@@ -393,3 +393,35 @@ def test_chunks_of_the_sums(n, V, d, k):
     if k:
         assert np.array_equal(ids, rids)
         assert (np.abs(top - rtop) <= eps[:, None] + 2.0 ** -24 * np.abs(rtop)).all()
+
+
+@pytest.mark.parametrize("n,V,d", [(1, 900, 2048), (40, 900, 512), (56, 700, 4096), (57, 900, 512), (200, 900, 2048), (70, 700, 8192)])
+def test_the_low_part_of_the_activations_counts(n, V, d):
+    """Activations just above an fp16 value, all on the side of the embedding's common
+    direction: an fp16 part alone would move every logit by 2^-12 of itself and more, the
+    same way, forty times the bound of the sums.  The low parts decide the result."""
+    mu = np.where(syn.normal((d,), 1.0, 120, "score.mu") > 0, 0.02, -0.02)
+    E = (mu + syn.normal((V, d), 0.002, 120, "score.E")).astype(np.float16)
+    h = ((0.3 + np.abs(syn.normal((n, d), 0.5, 120, "score.h"))) * np.sign(mu)).astype(np.float16).astype(np.float64)
+    y = (h * (1 + 0.9 * 2.0 ** -12)).astype(np.float32)
+    assert np.array_equal(y.astype(np.float16), h)          # what an fp16 part alone would hold
+    t = syn.token_ids(n, 120, "score.t", V)
+    err, z = _errors(E, y, t)
+    A = (np.abs(y).astype(np.float64) @ np.abs(E).astype(np.float64).T).max(1)
+    tol = _chunk_eps(A, d) + 2.0 ** -20 + 2.0 ** -24 * np.log(V)
+    assert (np.abs(err) <= tol).all(), (np.abs(err) / tol).max()
+    e64 = E.astype(np.float64).T
+    lse = [np.log(np.exp(x @ e64).sum(1)) for x in (y.astype(np.float64), h)]
+    assert (np.abs(lse[0] - lse[1]) > 10 * tol).all()
+
+
+@pytest.mark.parametrize("n", [56, 600])
+def test_rms_over_many_rows(n):
+    """Over rows that wander at random the errors stay together: each of an accumulator's 64
+    additions loses half of 2^-23 of a sum that is half the logit on average (2^-19 of the
+    probable logits), the result rounds by 2^-21 at most (logp is below 16), and the
+    exponentials and their sum by 2^-22 or so."""
+    V, d = 3000, 2048
+    E, y, t = _inputs(n, V, d, 121, lean=0.0)
+    err, z = _errors(E, y, t)
+    assert np.sqrt((err ** 2).mean()) <= 2.0 ** -19 * z.mean() + 2.0 ** -21 + 2.0 ** -22
