@@ -208,7 +208,8 @@ tl_status tl_kv_read_int4(const tl_kv_int4* cache, uint16_t* k, uint16_t* v, lon
  * Query head h reads cache head h / (q_heads / n_heads).  A query with P < 0
  * sees nothing and gets zeros.  What a query does not see has no effect on it,
  * NaN included.  Scores, maxima, exponentials and sums in fp32; softmax weights
- * and values enter the products as fp16; out is rounded to fp16.  A query's
+ * and values enter the products as fp16 (weights to 2^-11 of themselves, or to 2^-32
+ * of the largest where that is more); out is rounded to fp16.  A query's
  * result does not depend on the contents of other lanes.
  *   q      device fp16 [n_lanes * n_q][q_stride], row b * n_q + i, head h at
  *          column h * head_dim

@@ -346,3 +346,28 @@ def test_far_offsets():
     q = _q(3, 1, hd, 22)
     lens = [48, 47, 33]
     _check(_run(q, cache, lens, 1, 0), q, cache, lens, 1, 0)
+
+
+@pytest.mark.parametrize("lanes,H,ctx,hd,gap", [
+    (1, 1, 2112, 64, 26.0), (80, 1, 4096, 64, 26.0), (80, 1, 4096, 64, 30.0), (1, 2, 9000, 128, 28.0), (160, 4, 1024, 128, 24.5),
+])
+def test_many_keys_of_small_weight(lanes, H, ctx, hd, gap):
+    """Keys of a weight 2^-gap each below some heavy ones whose values are zero: the light
+    ones, of equal weight and value, are all of the output.  Every part of the split meets a
+    heavy key first.  A weight is off by half of fp16's least step at most, 2^-32 of the
+    heavy ones' (which weigh 2^7 or more), and by 2^-10 for the exponential of scores whose
+    terms are exact; the result rounds by 2^-11, or by half of fp16's least step, 2^-25,
+    where it is subnormal (1920 * 7 * 2^-30 = 1.25e-5 is)."""
+    heavy = np.arange(ctx) < ctx // 8
+    k = np.zeros((1, H, ctx, hd), np.float16)
+    k[:, :, heavy, 0] = 15                                  # held exactly: scale 1, zero point 0
+    v = np.where(heavy[None, None, :, None], 0.0, 1920.0) * np.ones((1, H, 1, hd))
+    cache = Cache(np.repeat(k, lanes, 0), np.repeat(v.astype(np.float16), lanes, 0))
+    q = np.zeros((lanes, H, hd), np.float16)
+    q[:, :, 0] = gap / np.log2(np.e) * np.sqrt(hd) / 15
+    got = _run(q, cache, [ctx] * lanes, 1, 0).astype(np.float64)
+    w = np.exp(-float(q[0, 0, 0]) * 15 / np.sqrt(hd))       # of a light key
+    light = ctx - heavy.sum()
+    want = 1920.0 * light * w / (heavy.sum() + light * w)
+    assert w * 2.0 ** 24 < 1
+    assert (np.abs(got - want) <= want * (2.0 ** -32 / w + 2.0 ** -10 + 2.0 ** -11) + 2.0 ** -25).all(), (got.min(), got.max(), want)

@@ -29,9 +29,9 @@
 // Work split: the context is cut into tiles of 32 keys; tile i belongs to slot i mod
 // slots, whatever the lane's length, so the work is even for every length and the
 // other queries of a launch do not change a query's arithmetic.  A warp takes a slot,
-// or some in turn, and keeps a running maximum and sum per query (base 2); the maximum
-// is raised only when a score exceeds it by more than 2^8, which spares the cross-lane
-// maximum on most tiles (weights stay at or below 2^8, well inside fp16).  The slots'
+// or some in turn, and keeps a running reference and sum per query (base 2); the reference
+// is raised only when a weight would pass 2^15 (A4_SLACK), which spares the cross-lane
+// maximum on most tiles.  The slots'
 // records are joined in a fixed order through shared memory, the CTAs of a cluster
 // through distributed shared memory, every CTA finishing its share of the outputs: one
 // launch, no workspace.  The longest contexts are split over more CTAs, whose records
@@ -61,7 +61,12 @@ constexpr int A4_MAX_CLUSTER = 8;
 constexpr int A4_MAX_SPLIT = 64;
 constexpr int A4_MAX_SMEM = 226 * 1024;   // beside the static array
 constexpr int A4_STAGES = 2;         // tiles of a warp's ring
-constexpr float A4_SLACK = 8.f;     // the running maximum may lag by 2^8
+// A softmax weight is 2^(score - m) with m 7 below a score that was the largest when it was
+// set, and m is raised when a score exceeds it by more than 15: the largest weight lies
+// between 2^7 and 2^15, so that in fp16 weights down to 2^-21 of it keep all their bits and
+// those down to 2^-32 of it count (with m at the largest score, keys below 2^-25 of it
+// vanished from the products while the sum had them).
+constexpr float A4_LIFT = 7.f, A4_SLACK = 15.f;
 constexpr float A4_NONE = -1e30f;   // below every score: no key yet
 
 __device__ __forceinline__ void a4_mma(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
@@ -446,8 +451,8 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == A4_WIDE ? 1 : 4) attn_int
           for (int w = 4; w < 32; w <<= 1) mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], w));
           mx[e] *= csc;
           const bool up = mx[e] > m[e] + A4_SLACK;
-          al[e] = up ? a4_ex2(m[e] - mx[e]) : 1.f;
-          if (up) m[e] = mx[e];
+          al[e] = up ? a4_ex2(m[e] - (mx[e] - A4_LIFT)) : 1.f;
+          if (up) m[e] = mx[e] - A4_LIFT;
           l[e] *= al[e];
         }
 #pragma unroll
@@ -458,8 +463,8 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == A4_WIDE ? 1 : 4) attn_int
           o[i][3] *= al[1];
         }
       }
-      // weights as fp16 (a rounding of 2^-11 each, of values the sum has in fp32),
-      // key pairs of column g
+      // weights as fp16 (a rounding of 2^-11 each, 2^-32 of the largest where they are
+      // subnormal, of values the sum has in fp32), key pairs of column g
       uint32_t pb[2][2];
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
