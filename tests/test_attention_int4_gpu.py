@@ -371,3 +371,22 @@ def test_many_keys_of_small_weight(lanes, H, ctx, hd, gap):
     want = 1920.0 * light * w / (heavy.sum() + light * w)
     assert w * 2.0 ** 24 < 1
     assert (np.abs(got - want) <= want * (2.0 ** -32 / w + 2.0 ** -10 + 2.0 ** -11) + 2.0 ** -25).all(), (got.min(), got.max(), want)
+
+
+@pytest.mark.parametrize("ctx,n_q,lens", [(90, 3, [90, 2, 0]), (2112, 1, [2112, 1, 0]), (9000, 2, [9000, 1, 0])])
+def test_an_infinite_query(ctx, n_q, lens):
+    """Scores that are all -inf have no distribution: NaN, not the zeros of a query that sees
+    nothing.  The other head's outputs are its own."""
+    H, hd = 2, 64
+    k, v = _kv(3, H, ctx, hd, 50)
+    k[..., 0] = -3 - np.abs(k[..., 0])                      # below zero as held, too
+    cache = Cache(k, v)
+    q = _q(3 * n_q, H, hd, 51)
+    want = _run(q, cache, lens, n_q, 0)
+    q[:, 0, 0] = np.inf
+    got = _run(q, cache, lens, n_q, 0)
+    assert np.array_equal(got[:, 1], want[:, 1])
+    for b, length in enumerate(lens):
+        for i in range(n_q):
+            sees = length - n_q + i >= 0
+            assert (np.isnan(got[b * n_q + i, 0]) if sees else got[b * n_q + i, 0] == 0).all(), (b, i)
