@@ -390,3 +390,17 @@ def test_an_infinite_query(ctx, n_q, lens):
         for i in range(n_q):
             sees = length - n_q + i >= 0
             assert (np.isnan(got[b * n_q + i, 0]) if sees else got[b * n_q + i, 0] == 0).all(), (b, i)
+
+
+def test_refusals_on_the_device():
+    """What is refused before any launch, with tensors where they belong."""
+    H, hd = 2, 64
+    cache = Cache(*_kv(1, H, 8, hd, 52))
+    q = torch.zeros(1, H * hd, dtype=torch.float16, device="cuda")
+    lens, out = torch.ones(1, dtype=torch.int32, device="cuda"), torch.full_like(q, 5.0)
+    none = [t[..., :0].contiguous() if i % 2 == 0 else t[..., :0, :].contiguous() for i, t in enumerate(cache.t)]
+    with pytest.raises(tl.TLError, match="no values"):
+        tl.tl_attention_int4(q, *none, lens, out)
+    with pytest.raises(tl.TLError, match="no values"):
+        tl.tl_kv_write_int4(q, q, *none, lens)
+    assert (out == 5).all()

@@ -166,6 +166,15 @@ def test_the_binding_refuses_what_the_library_cannot_see():
     assert (d.code_stride, d.param_stride) == (H * ctx * hd // 8, H * ctx * hd // 32)
 
 
+def test_rows_of_no_values_are_refused():
+    """A last dimension of 0 is refused like any other bad shape, before head sizes are divided by."""
+    c, p = torch.zeros(2, 2, 8, 0, dtype=torch.int32), torch.zeros(2, 2, 8, 0, 2, dtype=torch.float16)
+    with pytest.raises(tl.TLError, match="no values"):
+        tl._kv_int4("x", c, p, c, p)
+    with pytest.raises(tl.TLError):
+        tl.tl_attention_int4_workspace_bytes(c, p, c, p, 1, 2)
+
+
 # ---------------------------------------------------------------- the oracle's quantiser
 
 def test_oracle_int4_group_by_hand():

@@ -272,6 +272,8 @@ def _kv_int4(what: str, k_codes, k_params, v_codes, v_params) -> KvInt4Desc:
     not have four dimensions."""
     shape = k_codes.shape
     lanes, heads, ctx, words = shape
+    if not words:
+        _fail(f"{what}: codes {tuple(shape)} hold rows of no values")
     pshape = (lanes, heads, ctx, words // 4, 2)
     if v_codes.shape != shape or k_params.shape != pshape or v_params.shape != pshape:
         _fail(f"{what}: codes {tuple(shape)} and {tuple(v_codes.shape)}, parameters {tuple(k_params.shape)} and "
