@@ -404,3 +404,15 @@ def test_refusals_on_the_device():
     with pytest.raises(tl.TLError, match="no values"):
         tl.tl_kv_write_int4(q, q, *none, lens)
     assert (out == 5).all()
+
+
+@pytest.mark.parametrize("window", [1 << 31, (1 << 32) + 3, -(1 << 32), -(1 << 32) + 3, -1])
+def test_windows_out_of_range_are_refused(window):
+    """They are not cut to a window of another size."""
+    cache = Cache(*_kv(1, 1, 8, 64, 53))
+    q = torch.zeros(1, 64, dtype=torch.float16, device="cuda")
+    lens, out = torch.full((1,), 8, dtype=torch.int32, device="cuda"), torch.full_like(q, 5.0)
+    with pytest.raises(tl.TLError, match="window"):
+        tl.tl_attention_int4(q, *cache.t, lens, out, window=window)
+    torch.cuda.synchronize()
+    assert (out == 5).all()

@@ -175,6 +175,17 @@ def test_rows_of_no_values_are_refused():
         tl.tl_attention_int4_workspace_bytes(c, p, c, p, 1, 2)
 
 
+@pytest.mark.parametrize("bad", [dict(n=(1 << 32) + 1), dict(vocab=(1 << 32) + 100), dict(d=64 - (1 << 32)), dict(k=1 << 32)])
+def test_integers_beyond_32_bits_are_refused(bad):
+    """They are not cut to the size of another call."""
+    with pytest.raises(tl.TLError, match="out of range"):
+        tl.tl_score_head_workspace_bytes(**{**dict(n=1, vocab=100, d=64, k=0), **bad})
+    c, p = torch.zeros(1, 1, 9000, 8, dtype=torch.int32), torch.zeros(1, 1, 9000, 2, 2, dtype=torch.float16)
+    for n_q, heads in ((1 << 32 | 1, 1), (1, 1 << 32 | 1), (-(1 << 32) + 1, 1)):
+        with pytest.raises(tl.TLError, match="out of range"):
+            tl.tl_attention_int4_workspace_bytes(c, p, c, p, n_q, heads)
+
+
 # ---------------------------------------------------------------- the oracle's quantiser
 
 def test_oracle_int4_group_by_hand():

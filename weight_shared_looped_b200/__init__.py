@@ -217,6 +217,13 @@ def _fail(message: str) -> None:
     raise TLError(TL_ERR_INVALID_ARG, message)
 
 
+def _ints(what: str, **named) -> None:
+    """Refuses integers that ctypes would cut to 32 bits without a word."""
+    for name, v in named.items():
+        if not -(1 << 31) <= v < 1 << 31:
+            _fail(f"{what}: {name} = {v} is out of range")
+
+
 _TORCH: dict = {}
 
 
@@ -348,6 +355,7 @@ _INT4_SPLIT_CTX = 8192   # caches below this many positions need no workspace
 
 def tl_attention_int4_workspace_bytes(k_codes, k_params, v_codes, v_params, n_q: int,
                                       q_heads: int) -> int:
+    _ints("tl_attention_int4_workspace_bytes", n_q=n_q, q_heads=q_heads)
     b = SZ()
     _check(lib.tl_attention_int4_workspace_bytes(
         _kv_int4("tl_attention_int4", k_codes, k_params, v_codes, v_params), n_q, q_heads, b))
@@ -390,6 +398,7 @@ def tl_attention_int4(q, k_codes, k_params, v_codes, v_params, lens, out, n_q: i
         _fail(f"{what}: lens is not a contiguous [{lanes}]")
     if rows <= 1:
         qs = os_ = width
+    _ints(what, window=window)
     ws, ws_bytes = None, 0
     if d.max_ctx >= _INT4_SPLIT_CTX and rows:
         if workspace is None:
@@ -409,6 +418,7 @@ def tl_attention_int4(q, k_codes, k_params, v_codes, v_params, lens, out, n_q: i
 # --------------------------------------------------------------------- scoring head
 
 def tl_score_head_workspace_bytes(n: int, vocab: int, d: int, k: int) -> int:
+    _ints("tl_score_head_workspace_bytes", n=n, vocab=vocab, d=d, k=k)
     b = SZ()
     _check(lib.tl_score_head_workspace_bytes(n, vocab, d, k, b))
     return b.value
