@@ -186,6 +186,16 @@ def test_integers_beyond_32_bits_are_refused(bad):
             tl.tl_attention_int4_workspace_bytes(c, p, c, p, n_q, heads)
 
 
+@pytest.mark.parametrize("k", [-1, 17, 101])
+def test_a_models_scores_refuse_k(k):
+    """By the library's error, before any output is made."""
+    from types import SimpleNamespace
+    from weight_shared_looped_b200.model import DeviceModel
+    model = SimpleNamespace(embed=torch.zeros(100, 64, dtype=torch.float16), d=64)
+    with pytest.raises(tl.TLError, match="k = "):
+        DeviceModel.score(model, torch.zeros(2, 64), k=k)
+
+
 # ---------------------------------------------------------------- the oracle's quantiser
 
 def test_oracle_int4_group_by_hand():

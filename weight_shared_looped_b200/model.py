@@ -157,6 +157,7 @@ class DeviceModel:
         if self.embed is None:
             raise ValueError("the model has no embedding to use as its head")
         n, dev = y.shape[0], y.device
+        ws_bytes = tl_score_head_workspace_bytes(n, self.embed.shape[0], self.d, k)   # refuses a k out of range
         with _allocating_on(stream, dev):
             out = {"entropy": torch.empty(n, dtype=torch.float32, device=dev)}
             if targets is not None:
@@ -164,8 +165,7 @@ class DeviceModel:
             if k:
                 out["ids"] = torch.empty(n, k, dtype=torch.int32, device=dev)
                 out["top"] = torch.empty(n, k, dtype=torch.float32, device=dev)
-            ws = torch.empty(tl_score_head_workspace_bytes(n, self.embed.shape[0], self.d, k),
-                             dtype=torch.uint8, device=dev)
+            ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
         tl_score_head(self.embed, y, targets, out.get("logp"), out["entropy"], out.get("ids"),
                       out.get("top"), ws, stream=stream)
         return out
