@@ -540,7 +540,9 @@ tl_status tl_greedy_head(tl_model* model, const float* y, int n, int32_t* ids,
  * of the 2^-17 where it comes from few early elements, by less elsewhere.  The
  * given token's logit, the order of the best and the largest terms of the sum are
  * decided by fp64 dot products of the inputs.  A row with a logit that is not
- * finite gets NaN and ids of -1.
+ * finite gets NaN and ids of -1.  So does every row of a call one of whose device
+ * waits ran out (2 s; it does not happen to a GPU that works): tl_score_head_status
+ * tells the two apart.
  *   embed      device fp16 [vocab, d]
  *   y          device fp32 [n][y_stride]
  *   targets    device int32 [n], with logp; or both NULL
@@ -556,6 +558,20 @@ tl_status tl_score_head(const uint16_t* embed, int vocab, int d, const float* y,
                         int n, const int32_t* targets, float* logp, float* entropy, int k,
                         int32_t* top_ids, float* top_logp, void* workspace,
                         size_t workspace_bytes, tl_stream stream);
+
+/* Synchronise `stream`, then return the status of the last tl_score_head call (n > 0)
+ * that had this workspace, whose memory must not have been used otherwise since: TL_OK
+ * or TL_ERR_TIMEOUT. */
+tl_status tl_score_head_status(const void* workspace, tl_stream stream);
+
+/* Test hook for the scoring head's bounded waits: tl_score_head with rows y [n][d] and
+ * waits of limit_us microseconds (1 .. 2e6), whose copying threads stop after `copies`
+ * pieces each.  With fewer than the work needs, waits run out; the kernels return
+ * normally. */
+tl_status tl_check_score_wait(const uint16_t* embed, int vocab, int d, const float* y, int n,
+                              int copies, unsigned limit_us, float* entropy, int k,
+                              int32_t* top_ids, float* top_logp, void* workspace,
+                              size_t workspace_bytes, tl_stream stream);
 
 /* One greedy self-speculative step of one lane with one weight set and one
  * cache ("Current Status", self-speculative row; "TinyLoop Framework", "What

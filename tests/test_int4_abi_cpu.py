@@ -196,6 +196,17 @@ def test_a_models_scores_refuse_k(k):
         DeviceModel.score(model, torch.zeros(2, 64), k=k)
 
 
+def test_score_status_and_the_wait_hook_refuse():
+    def hook(copies=1, limit=1000, n=3, ws=256):
+        return tl.lib.tl_check_score_wait(_p(P16), 100, 64, _p(P16), n, copies, limit, None, 0, None, None, _p(ws), 1 << 30,
+                                          None)
+    assert hook(limit=0) == hook(limit=2000001) == hook(copies=-1) == hook(n=-1) == hook(ws=128) == BAD
+    assert hook(n=0) == tl.TL_OK
+    assert tl.lib.tl_score_head_status(None, None) == tl.lib.tl_score_head_status(_p(128), None) == BAD
+    with pytest.raises(tl.TLError, match="workspace"):
+        tl.tl_score_head_status(torch.zeros(512, dtype=torch.uint8))
+
+
 # ---------------------------------------------------------------- the oracle's quantiser
 
 def test_oracle_int4_group_by_hand():

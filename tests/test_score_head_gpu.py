@@ -425,3 +425,45 @@ def test_rms_over_many_rows(n):
     E, y, t = _inputs(n, V, d, 121, lean=0.0)
     err, z = _errors(E, y, t)
     assert np.sqrt((err ** 2).mean()) <= 2.0 ** -19 * z.mean() + 2.0 ** -21 + 2.0 ** -22
+
+
+@pytest.mark.parametrize("n,V,d", [(5, 600, 1024), (40, 9000, 1024), (130, 600, 1024), (600, 3001, 1088), (4800, 300, 1024)])
+@pytest.mark.parametrize("copies", [0, 1, 5])
+def test_a_wait_that_runs_out(n, V, d, copies):
+    """Copies that stop early: the waits for the rest give up after 2 ms, every row is NaN and
+    the status says why; the next call with the workspace is as if nothing had been."""
+    k = 3
+    E, y, t = _inputs(n, V, d, 130)
+    want = _run(E, y, t, k)
+    tE, ty = torch.from_numpy(E).cuda(), torch.from_numpy(y).cuda()
+    ws = torch.empty(tl.tl_score_head_workspace_bytes(n, V, d, k), dtype=torch.uint8, device="cuda")
+    h, ids = torch.zeros(n, device="cuda"), torch.zeros(n, k, dtype=torch.int32, device="cuda")
+    top = torch.zeros(n, k, device="cuda")
+
+    def hook(copies):
+        rc = tl.lib.tl_check_score_wait(tE.data_ptr(), V, d, ty.data_ptr(), n, copies, 2000, h.data_ptr(), k, ids.data_ptr(),
+                                        top.data_ptr(), ws.data_ptr(), ws.numel(), None)
+        assert rc == tl.TL_OK
+    hook(copies)
+    assert tl.tl_score_head_status(ws) == tl.TL_ERR_TIMEOUT
+    assert h.isnan().all() and top.isnan().all() and (ids == -1).all()
+    tl.tl_score_head(tE, ty, torch.from_numpy(t).cuda(), top[:, 0].contiguous(), h, ids, top, ws)
+    assert tl.tl_score_head_status(ws) == tl.TL_OK
+    for got, w in zip((h, ids, top), want[1:]):
+        assert np.array_equal(got.cpu().numpy(), w)
+    hook(2 ** 31 - 1)
+    assert tl.tl_score_head_status(ws) == tl.TL_OK and np.array_equal(h.cpu().numpy(), want[1])
+
+
+def test_a_models_scores_with_a_workspace():
+    """A non-finite row leaves the status as it is."""
+    E, y, t = _inputs(6, 600, 256, 131)
+    y[2, 3] = np.inf
+    model = SimpleNamespace(embed=torch.from_numpy(E).cuda(), d=256)
+    ws = torch.full((tl.tl_score_head_workspace_bytes(6, 600, 256, 2),), 0xAB, dtype=torch.uint8, device="cuda")
+    got = DeviceModel.score(model, torch.from_numpy(y).cuda(), torch.from_numpy(t.astype(np.int32)).cuda(), k=2, workspace=ws)
+    assert tl.tl_score_head_status(ws) == tl.TL_OK
+    want = _run(E, y, t, 2)
+    for key, w in zip(("logp", "entropy", "ids", "top"), want):
+        assert np.array_equal(got[key].cpu().numpy(), w, equal_nan=True)
+    assert np.isnan(want[0][2])

@@ -78,6 +78,8 @@ _SIGS = {
     "tl_attention_int4": ([ctypes.POINTER(KvInt4Desc), P, LG, I, I, P, I, P, LG, P, SZ, P], I),
     "tl_score_head_workspace_bytes": ([I, I, I, I, ctypes.POINTER(SZ)], I),
     "tl_score_head": ([P, I, I, P, LG, I, P, P, P, I, P, P, P, SZ, P], I),
+    "tl_score_head_status": ([P, P], I),
+    "tl_check_score_wait": ([P, I, I, P, I, I, ctypes.c_uint, P, I, P, P, P, SZ, P], I),
     "tl_attention_prefill": ([P, P, P, I, I, I, P, P], I),
     "tl_block_create": ([ctypes.POINTER(BlockDesc), ctypes.POINTER(P)], I),
     "tl_block_destroy": ([P], I),
@@ -466,6 +468,17 @@ def tl_score_head(embed, y, targets, logp, entropy, top_ids, top_logp, workspace
             ys if n > 1 else d, n, _ptr(targets), _ptr(logp), _ptr(entropy), k,
             _ptr(top_ids) if k else None, _ptr(top_logp) if k else None, workspace.data_ptr(),
             workspace.numel())
+
+
+def tl_score_head_status(workspace, stream=None) -> int:
+    """TL_OK or TL_ERR_TIMEOUT of the last tl_score_head call with this workspace, after the
+    stream's work (default: the current stream of the workspace's device)."""
+    n = _TORCH or _torch_names()
+    if workspace.dtype is not n["u8"] or not workspace.is_cuda or workspace.numel() < 256:
+        _fail("tl_score_head_status: workspace is not a uint8 tensor of a scoring call on a CUDA device")
+    with n["torch"].cuda.device(workspace.device):
+        s = n["torch"].cuda.current_stream().cuda_stream if stream is None else _stream(stream)
+        return lib.tl_score_head_status(workspace.data_ptr(), s)
 
 
 # --------------------------------------------------------------------- blocks / model

@@ -7,6 +7,7 @@
 // Memory", "KV cache INT8": 10 layers = 2 pre-blocks + L=8), final RMSNorm and
 // no output head.  L is an argument of every call ("Loop count is a runtime
 // knob"); the weights a model references do not depend on it.
+#include <climits>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -364,9 +365,11 @@ TL_API tl_status tl_score_head_workspace_bytes(int n, int vocab, int d, int k, s
   return ok();
 }
 
-TL_API tl_status tl_score_head(const uint16_t* embed, int vocab, int d, const float* y, long y_stride, int n,
-                               const int32_t* targets, float* logp, float* entropy, int k, int32_t* top_ids,
-                               float* top_logp, void* workspace, size_t workspace_bytes, tl_stream stream) {
+namespace {
+
+tl_status score_head(const uint16_t* embed, int vocab, int d, const float* y, long y_stride, int n,
+                     const int32_t* targets, float* logp, float* entropy, int k, int32_t* top_ids, float* top_logp,
+                     void* workspace, size_t workspace_bytes, uint64_t wait_ns, int copies, cudaStream_t s) {
   TL_TRY(check_score(n, vocab, d, k));
   TL_CHECK_ARG(y_stride >= d && y_stride % 4 == 0, "y_stride = %ld must be a multiple of 4, at least d = %d", y_stride,
                d);
@@ -393,8 +396,39 @@ TL_API tl_status tl_score_head(const uint16_t* embed, int vocab, int d, const fl
   a.top_ids = top_ids;
   a.top_logp = top_logp;
   a.ws = (char*)workspace;
-  return launch_score_head(a, (cudaStream_t)stream);
+  a.wait_ns = wait_ns;
+  a.copies = copies;
+  return launch_score_head(a, s);
 }
+
+}  // namespace
+
+TL_API tl_status tl_score_head(const uint16_t* embed, int vocab, int d, const float* y, long y_stride, int n,
+                               const int32_t* targets, float* logp, float* entropy, int k, int32_t* top_ids,
+                               float* top_logp, void* workspace, size_t workspace_bytes, tl_stream stream) {
+  return score_head(embed, vocab, d, y, y_stride, n, targets, logp, entropy, k, top_ids, top_logp, workspace,
+                    workspace_bytes, kScoreWaitNs, INT_MAX, (cudaStream_t)stream);
+}
+
+TL_API tl_status tl_score_head_status(const void* workspace, tl_stream stream) {
+  TL_CHECK_ARG(workspace && ((uintptr_t)workspace & 255) == 0, "workspace is NULL or not 256-byte aligned");
+  int code = 0;
+  TL_CUDA(cudaMemcpyAsync(&code, workspace, 4, cudaMemcpyDeviceToHost, (cudaStream_t)stream));
+  TL_CUDA(cudaStreamSynchronize((cudaStream_t)stream));
+  if (code == 0) return ok();
+  if (code == TL_ERR_TIMEOUT) return set_error(TL_ERR_TIMEOUT, "a bounded device wait of the scoring head ran out");
+  return set_error(TL_ERR_INVALID_ARG, "workspace holds no call's status (%d)", code);
+}
+
+TL_API tl_status tl_check_score_wait(const uint16_t* embed, int vocab, int d, const float* y, int n, int copies,
+                                     unsigned limit_us, float* entropy, int k, int32_t* top_ids, float* top_logp,
+                                     void* workspace, size_t workspace_bytes, tl_stream stream) {
+  TL_CHECK_ARG(limit_us >= 1 && limit_us <= 2000000, "limit_us = %u out of [1, 2000000]", limit_us);
+  TL_CHECK_ARG(copies >= 0, "copies = %d must be >= 0", copies);
+  return score_head(embed, vocab, d, y, d, n, nullptr, nullptr, entropy, k, top_ids, top_logp, workspace,
+                    workspace_bytes, (uint64_t)limit_us * 1000ull, copies, (cudaStream_t)stream);
+}
+
 
 TL_API tl_status tl_attention_prefill(const uint16_t* q, const uint16_t* k, const uint16_t* v,
                                       int T, int H, int hd, uint16_t* out, tl_stream stream) {

@@ -82,11 +82,11 @@ __device__ __forceinline__ float sc_ex2(float x) {
 // One CTA per row of the padded batch: parts[row] = hi, parts[pad + row] = lo
 // (zeros behind the batch), scale[row] = the power of two taken out.
 __global__ void __launch_bounds__(256) score_split_kernel(const float* __restrict__ y, long y_stride, int n, int d,
-                                                          int pad, __half* parts, float* scale, int* flag) {
+                                                          int pad, __half* parts, float* scale, int* clear) {
   pdl_enter();
   __shared__ float wmax[8];
   const int row = blockIdx.x, tid = threadIdx.x;
-  if (row == 0 && tid == 0) *flag = 0;
+  if (row == 0 && tid == 0 && clear) *clear = 0;
   __half* hi = parts + (size_t)row * d;
   __half* lo = parts + (size_t)(pad + row) * d;
   if (row >= n) {
@@ -162,9 +162,9 @@ __device__ __forceinline__ void sc_copy(uint64_t* bar, void* dst, const CUtensor
       : "memory");
 }
 // a bounded wait by one thread; false once it ran out or another role gave up
-__device__ __forceinline__ bool sc_wait(uint64_t* bar, uint32_t parity, const int* abort_flag) {
+__device__ __forceinline__ bool sc_wait(uint64_t* bar, uint32_t parity, const int* abort_flag, uint64_t limit_ns) {
   if (mbar_try(smem_u32(bar), parity)) return true;
-  return mbar_wait(bar, parity) && !*(volatile const int*)abort_flag;
+  return mbar_wait(bar, parity, limit_ns) && !*(volatile const int*)abort_flag;
 }
 
 __device__ __forceinline__ void sc_ld16(uint32_t* u, uint32_t addr) {
@@ -213,7 +213,9 @@ struct ScoreTc {
   int slots;              // vocabulary-major: accumulators in TMEM
   const float* scale;
   ScoreRec rec;
-  int* flag;              // set when a bounded wait ran out
+  int* flag;              // takes kDevTimeout when a bounded wait ran out
+  uint64_t wait_ns;       // limit of a wait
+  int copies;             // stages that the copying thread fills at most (a test of the waits fills too few)
 };
 
 constexpr int SC_SLOTS = 8;        // accumulators of a CTA, at most
@@ -221,9 +223,25 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 struct ScoreBars {
   uint64_t full[12], empty[12], acc_full[SC_SLOTS], acc_empty[SC_SLOTS];
+  uint64_t drained;
   uint32_t tmem;
-  int abort;
+  int abort, issued;      // a role gave up; stages requested
 };
+
+// After the roles have met: where one gave up, the copies and MMAs still in flight end
+// before the CTA leaves and gives back its TMEM (threads 256 and 288 issued them).
+__device__ __forceinline__ void sc_settle(ScoreBars& bars, int stages, int* flag) {
+  if (!bars.abort) return;
+  if (threadIdx.x == 256)
+    for (int i = max(0, bars.issued - stages); i < bars.issued; ++i) mbar_wait(&bars.full[i % stages], (i / stages) & 1);
+  if (threadIdx.x == 288) {
+    sc_commit(&bars.drained);
+    mbar_wait(&bars.drained, 0);
+  }
+  if (threadIdx.x == 0) atomicExch(flag, kDevTimeout);
+  __syncwarp();
+  __syncthreads();
+}
 
 // Row-major variant: 128 rows of activations (hi and lo) are the MMA's M side,
 // bn vocabulary entries its N side, so an epilogue thread owns one row and walks
@@ -270,7 +288,8 @@ __global__ void __launch_bounds__(SR_THREADS, 1)
       mbar_init(&bars.acc_full[s], 1);
       mbar_init(&bars.acc_empty[s], 8);
     }
-    bars.abort = 0;
+    mbar_init(&bars.drained, 1);
+    bars.abort = bars.issued = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   __syncwarp();
@@ -294,8 +313,8 @@ __global__ void __launch_bounds__(SR_THREADS, 1)
         const int r0 = mt * 128;
         for (int vt = group; vt < a.vt && ok; vt += a.groups) {
           const int v0 = vt * a.bn;
-          for (int kb = 0; kb < a.nkb; ++kb) {
-            if (issued >= a.stages && !sc_wait(&bars.empty[s], ph, &bars.abort)) {
+          for (int kb = 0; kb < a.nkb && issued < a.copies; ++kb) {
+            if (issued >= a.stages && !sc_wait(&bars.empty[s], ph, &bars.abort, a.wait_ns)) {
               ok = false;
               break;
             }
@@ -312,8 +331,7 @@ __global__ void __launch_bounds__(SR_THREADS, 1)
           }
         }
         if (!ok) atomicExch(&bars.abort, 1);
-        if (*(volatile int*)&bars.abort)               // the copies still in flight land before the CTA leaves
-          for (int i = max(0, issued - a.stages); i < issued; ++i) mbar_wait(&bars.full[i % a.stages], (i / a.stages) & 1);
+        bars.issued = issued;
       }
       __syncwarp();
     } else if (warp == 9) {
@@ -326,11 +344,11 @@ __global__ void __launch_bounds__(SR_THREADS, 1)
         for (int vt = group; vt < a.vt && ok; vt += a.groups) {
           for (int k0 = 0; k0 < a.nkb && ok; k0 += SC_CHUNK, ++i) {
             const int buf = i & 1, use = i >> 1;
-            if (use > 0) ok = sc_wait(&bars.acc_empty[buf], (use & 1) ^ 1, &bars.abort);
+            if (use > 0) ok = sc_wait(&bars.acc_empty[buf], (use & 1) ^ 1, &bars.abort, a.wait_ns);
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             const uint32_t acc = tmem + buf * 256;
             for (int kb = k0; kb < min(k0 + SC_CHUNK, a.nkb) && ok; ++kb) {
-              ok = sc_wait(&bars.full[s], ph, &bars.abort);
+              ok = sc_wait(&bars.full[s], ph, &bars.abort, a.wait_ns);
               if (!ok) break;
               asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
               const uint64_t hi = desc0 + (uint64_t)(s * (a.stage_bytes >> 4)), lo = hi + (16384 >> 4), e = hi + (32768 >> 4);
@@ -401,7 +419,7 @@ __global__ void __launch_bounds__(SR_THREADS, 1)
     for (int vt = group; vt < a.vt && ok; vt += a.groups) {
       for (int k0 = 0; k0 < a.nkb; k0 += SC_CHUNK, ++i) {
         const int buf = i & 1, use = i >> 1;
-        if (!warp_wait(&bars.acc_full[buf], use & 1, &bars.abort, true)) {
+        if (!warp_wait(&bars.acc_full[buf], use & 1, &bars.abort, true, a.wait_ns)) {
           if (lane == 0) atomicExch(&bars.abort, 1);
           ok = false;
           break;
@@ -502,15 +520,14 @@ __global__ void __launch_bounds__(SR_THREADS, 1)
         a.rec.top_v[((size_t)row * KC + p) * a.slices + 2 * group + half] = cv[p];
       }
     }
-    if (!ok && lane == 0) atomicExch(a.flag, 1);
     __syncwarp();
   }
   __syncthreads();
+  sc_settle(bars, a.stages, a.flag);
   if (warp == 9) {
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
   }
-  if (threadIdx.x == 0 && bars.abort) atomicExch(a.flag, 1);
 }
 
 // Vocabulary-major variant for few rows: bn <= 128 vocabulary entries are the
@@ -546,7 +563,8 @@ __global__ void __launch_bounds__(SV_THREADS, 1)
       mbar_init(&bars.acc_full[s], 1);
       mbar_init(&bars.acc_empty[s], 4);
     }
-    bars.abort = 0;
+    mbar_init(&bars.drained, 1);
+    bars.abort = bars.issued = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   __syncwarp();
@@ -575,7 +593,7 @@ __global__ void __launch_bounds__(SV_THREADS, 1)
   const int spt = (a.nkb + SV_KBS - 1) / SV_KBS;       // stages per tile
   if (warp == 8) {
     if (lane == 0) {
-      const int total = (a.vt - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x * spt;
+      const int total = min(a.copies, (a.vt - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x * spt);
       const int v_step = (int)gridDim.x * a.bn;
       auto copy_e = [&](int s, int k0, int v0) {     // expect the stage, request its embedding rows
         uint8_t* sp = smem + (size_t)s * a.stage_bytes;
@@ -599,7 +617,7 @@ __global__ void __launch_bounds__(SV_THREADS, 1)
       int s = 0, ph = 1, issued = 0, ky = 0;
       for (; issued < total; ++issued) {
         if (issued >= a.stages) {
-          if (!sc_wait(&bars.empty[s], ph, &bars.abort)) {
+          if (!sc_wait(&bars.empty[s], ph, &bars.abort, a.wait_ns)) {
             atomicExch(&bars.abort, 1);
             break;
           }
@@ -618,8 +636,7 @@ __global__ void __launch_bounds__(SV_THREADS, 1)
           ph ^= 1;
         }
       }
-      if (*(volatile int*)&bars.abort)
-        for (int i = max(0, issued - a.stages); i < issued; ++i) mbar_wait(&bars.full[i % a.stages], (i / a.stages) & 1);
+      bars.issued = issued;
     }
     __syncwarp();
   } else if (warp == 9) {
@@ -631,11 +648,11 @@ __global__ void __launch_bounds__(SV_THREADS, 1)
       bool ok = true;
       for (int t = blockIdx.x; t < a.vt && ok; t += gridDim.x) {
         for (int c0 = 0; c0 < a.nkb && ok; c0 += SC_CHUNK) {
-          if (used >= a.slots) ok = sc_wait(&bars.acc_empty[slot], slot_ph, &bars.abort);
+          if (used >= a.slots) ok = sc_wait(&bars.acc_empty[slot], slot_ph, &bars.abort, a.wait_ns);
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
           const uint32_t acc = tmem + slot * slot_cols;
           for (int k0 = c0; k0 < min(c0 + SC_CHUNK, a.nkb) && ok; k0 += SV_KBS) {
-            ok = sc_wait(&bars.full[s], ph, &bars.abort);
+            ok = sc_wait(&bars.full[s], ph, &bars.abort, a.wait_ns);
             if (!ok) break;
             asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
             const uint64_t e0 = desc0 + (uint64_t)(s * (a.stage_bytes >> 4)), y0 = e0 + (ybase >> 4);
@@ -672,7 +689,7 @@ __global__ void __launch_bounds__(SV_THREADS, 1)
       if (warp < 4) {
         float z[64];                                     // an entry's logits
         for (int c0 = 0; c0 < a.nkb; c0 += SC_CHUNK) {
-          ok = warp_wait(&bars.acc_full[slot], slot_ph, &bars.abort, true);
+          ok = warp_wait(&bars.acc_full[slot], slot_ph, &bars.abort, true, a.wait_ns);
           if (!ok) break;
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 #pragma unroll
@@ -822,11 +839,11 @@ __global__ void __launch_bounds__(SV_THREADS, 1)
     }
   }
   __syncthreads();
+  sc_settle(bars, a.stages, a.flag);
   if (warp == 9) {
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
   }
-  if (threadIdx.x == 0 && bars.abort) atomicExch(a.flag, 1);
 }
 
 // ------------------------------------------------------------------ pass 2
@@ -1267,7 +1284,7 @@ struct ScorePlan {
   ScoreTc t;
   bool by_rows;
   int grid;
-  size_t smem, parts_off, scale_off, flag_off, stat_off, top_x_off, top_v_off, bytes;
+  size_t smem, parts_off, scale_off, stat_off, top_x_off, top_v_off, bytes;
 };
 
 // Up to 56 rows the embedding streams as the M side (its bytes are the bound); above,
@@ -1327,10 +1344,9 @@ ScorePlan score_plan(int n, int V, int d, int k) {
     p.smem = 1024 + (size_t)t.stages * t.stage_bytes + queue;
   }
   auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
-  p.parts_off = 0;
-  p.scale_off = up((size_t)2 * t.pad * d * 2);
-  p.flag_off = p.scale_off + up((size_t)t.pad * 4);
-  p.stat_off = p.flag_off + 256;
+  p.parts_off = 256;               // behind the flag, which has its place whatever the sizes are
+  p.scale_off = p.parts_off + up((size_t)2 * t.pad * d * 2);
+  p.stat_off = p.scale_off + up((size_t)t.pad * 4);
   p.top_x_off = p.stat_off + up((size_t)n * t.slices * 16);
   const size_t top = up((size_t)n * t.slices * score_cand(k) * 4);
   p.top_v_off = p.top_x_off + top;
@@ -1390,7 +1406,9 @@ tl_status launch_score_head(const ScoreArgs& a0, cudaStream_t s) {
     __half* parts = (__half*)(a.ws + p.parts_off);
     float* scale = (float*)(a.ws + p.scale_off);
     t.scale = scale;
-    t.flag = (int*)(a.ws + p.flag_off);
+    t.flag = (int*)a.ws;
+    t.wait_ns = a.wait_ns;
+    t.copies = a.copies;
     t.rec.stat = (float4*)(a.ws + p.stat_off);
     t.rec.top_x = (float*)(a.ws + p.top_x_off);
     t.rec.top_v = (int*)(a.ws + p.top_v_off);
@@ -1399,7 +1417,8 @@ tl_status launch_score_head(const ScoreArgs& a0, cudaStream_t s) {
                      p.by_rows ? 128 : 2 * t.pad, CU_TENSOR_MAP_SWIZZLE_128B));
     TL_TRY(encode_2d(&me, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, a.E, a.d, a.V, (uint64_t)a.d * 2, SC_BK, t.bn,
                      CU_TENSOR_MAP_SWIZZLE_128B));
-    TL_LAUNCH_PDL(score_split_kernel, t.pad, 256, 0, s, a.y, a.y_stride, a.n, a.d, t.pad, parts, scale, t.flag);
+    TL_LAUNCH_PDL(score_split_kernel, t.pad, 256, 0, s, a.y, a.y_stride, a.n, a.d, t.pad, parts, scale,
+                  r0 == 0 ? t.flag : nullptr);
     const int kc = score_cand(a.k);
     TL_TRY(kc == 4   ? launch_score_pass1<4>(p, my, me, s)
                    : kc == 8 ? launch_score_pass1<8>(p, my, me, s)

@@ -92,10 +92,10 @@ __device__ __forceinline__ void mma_commit_elect(uint64_t* bar) {
 // Bounded wait (when needed) by lane 0 with the outcome (and the CTA's abort flag) broadcast
 // to the warp, so the warp stays converged.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const int* abort_flag,
-                                          bool needed) {
+                                          bool needed, uint64_t limit_ns = kWaitLimitNs) {
   bool ok = true;
   if ((threadIdx.x & 31) == 0)
-    ok = (!needed || mbar_wait(bar, parity)) && !*(volatile const int*)abort_flag;
+    ok = (!needed || mbar_wait(bar, parity, limit_ns)) && !*(volatile const int*)abort_flag;
   return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
 }
 

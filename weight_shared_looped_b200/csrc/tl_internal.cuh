@@ -322,8 +322,11 @@ struct ScoreArgs {
   int k;
   int32_t* top_ids;                // [n][k]
   float* top_logp;
-  char* ws;
+  char* ws;                        // its first word: a status, kDevTimeout when a wait ran out
+  uint64_t wait_ns;                // limit of a device wait
+  int copies;                      // INT_MAX, or too few for a test of the waits
 };
+constexpr uint64_t kScoreWaitNs = 2000000000ull;
 size_t score_workspace(int n, int V, int d, int k);
 tl_status launch_score_head(const ScoreArgs& a, cudaStream_t s);
 

@@ -150,10 +150,12 @@ class DeviceModel:
         tl_greedy_head(self.handle, y, ids, stream=stream)
         return ids
 
-    def score(self, y, targets=None, k: int = 0, stream=None) -> Dict[str, torch.Tensor]:
+    def score(self, y, targets=None, k: int = 0, stream=None, workspace=None) -> Dict[str, torch.Tensor]:
         """Log probabilities under the tied embedding of final-norm outputs y fp32 [n, d]:
         "logp" of the given tokens (targets int32 [n], -1: none), the distributions' "entropy",
-        and the k most probable tokens, "ids" and "top" (allocated for use on `stream`)."""
+        and the k most probable tokens, "ids" and "top" (allocated for use on `stream`).  With a
+        workspace (uint8, tl_score_head_workspace_bytes) of the caller's own, tl_score_head_status
+        tells afterwards whether a device wait ran out."""
         if self.embed is None:
             raise ValueError("the model has no embedding to use as its head")
         n, dev = y.shape[0], y.device
@@ -165,7 +167,7 @@ class DeviceModel:
             if k:
                 out["ids"] = torch.empty(n, k, dtype=torch.int32, device=dev)
                 out["top"] = torch.empty(n, k, dtype=torch.float32, device=dev)
-            ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+            ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev) if workspace is None else workspace
         tl_score_head(self.embed, y, targets, out.get("logp"), out["entropy"], out.get("ids"),
                       out.get("top"), ws, stream=stream)
         return out
