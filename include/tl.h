@@ -153,7 +153,9 @@ tl_status tl_kv_quant_int8(const uint16_t* x, int rows, int hd, int8_t* codes,
  *   scale = fp16, rounded towards zero, of (hi - lo) / 15;   zero = lo
  *   code  = clamp(rint((x - lo) * (1 / scale)), 0, 15), scale == 0 gives 0
  * (difference, reciprocal and product each rounded; rint ties to even).  The
- * value held is zero + code * scale, within [lo, hi].  A group with a NaN or an
+ * value held is zero + code * scale, within [lo, hi], and off by half a scale or, at
+ * the group's upper end, by 2^-10 (hi - lo) or 15 * 2^-24, whichever is most (the last
+ * counts for ranges below 15 * 2^-14; one below 15 * 2^-24 is held as lo).  A group with a NaN or an
  * infinity gets NaN scale and zero and codes 0.
  * Layout of one lane: codes uint32 [n_heads][max_ctx][head_dim / 8] (word j of a
  * row holds elements 8j .. 8j + 7, element 8j + i in bits 4i .. 4i + 3) and

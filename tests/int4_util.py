@@ -91,3 +91,23 @@ def attend(q, K, V, length, n_q, window):
             tol[i, h] = (w @ np.abs(v)) * rel + 2.0 ** -25 * np.abs(v).sum(0)
             tol[i, h] += np.abs(out[i, h]) * u + 2.0 ** -25
     return out, tol
+
+
+def narrow_groups():
+    """Groups whose ranges pass through the subnormal scales, from 2^-24 to 2^-9, at zero points
+    of several sizes; fp16 [n, 64]."""
+    rng = np.random.default_rng(9)
+    span = np.exp2(np.linspace(-24, -9, 240))[:, None] * rng.random((240, 64))
+    span[:, ::32], span[:, 1::32] = 0, np.exp2(np.linspace(-24, -9, 240))[:, None]
+    span[0, 1::32] = 28.5 * 2.0 ** -24                      # scale 2^-24, nearly two steps a unit
+    lo = np.array([0.0, -2.0 ** -14, 2.0 ** -12, -1.0])[np.arange(240) % 4, None]
+    return (lo + span).astype(np.float16)
+
+
+def held_bound(x):
+    """How far a value may be from the one held, element by element: half a scale, or at the
+    upper end what rounding the scale towards zero takes (kv_int4.cuh); fp32 steps 2^-22."""
+    g = x.reshape(x.shape[:-1] + (x.shape[-1] // 32, 32)).astype(np.float64)
+    width = g.max(-1, keepdims=True) - g.min(-1, keepdims=True)
+    most = np.maximum(np.maximum(width / 30, width * 2.0 ** -10), np.minimum(width, 15 * 2.0 ** -24))
+    return np.broadcast_to(most * (1 + 2.0 ** -22) + width * 2.0 ** -22, g.shape).reshape(x.shape)

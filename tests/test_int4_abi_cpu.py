@@ -230,6 +230,19 @@ def test_oracle_int4_scale_rounds_towards_zero():
     assert (v >= g.min(-1, keepdims=True)).all() and (v <= g.max(-1, keepdims=True)).all()
 
 
+def test_oracle_int4_narrow_groups():
+    """Subnormal scales: the absolute bound holds, one relative to the step does not."""
+    from int4_util import held_bound, narrow_groups
+    x = narrow_groups()
+    c, s, z = o.kv_quant_int4(x)
+    err = np.abs(o.kv_dequant_int4(c, s, z) - x.astype(np.float64))
+    assert (err <= held_bound(x)).all()
+    g = x.reshape(-1, 32).astype(np.float64)
+    step = (g.max(-1) - g.min(-1)) / 15
+    worst = err.reshape(-1, 32).max(-1)
+    assert (worst > 5 * step).any() and (s == 0).any()       # the case of range 28.5 * 2^-24, and collapsed groups
+
+
 def test_a_planted_mistake_is_seen():
     """The bit-exact comparison tells rounding to nearest from towards zero, a
     missing + 8 of the signed codes, and a swapped nibble order."""

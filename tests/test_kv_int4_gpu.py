@@ -10,7 +10,7 @@ import synthetic as syn
 import weight_shared_looped_b200 as tl
 from oracle import tinyloop_oracle as o
 
-from int4_util import pack, quantise, values
+from int4_util import held_bound, narrow_groups, pack, quantise, values
 
 pytestmark = pytest.mark.gpu
 
@@ -227,3 +227,21 @@ def test_oracle_pack_matches_canonical_words():
     c = np.arange(64, dtype=np.uint8).reshape(2, 32) % 16
     w = pack(c).view(np.uint32)
     assert w[0, 0] == 0x76543210 and w[1, 1] == 0xFEDCBA98 and w.shape == (2, 4)
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+def test_narrow_groups(hd):
+    """Groups whose scale is subnormal or zero: read back within the absolute bound of the
+    rows that were written (and the read-back's own rounding)."""
+    x = narrow_groups().reshape(-1, hd)
+    n = len(x)
+    t = torch.from_numpy(x).cuda()
+    cache = _empty(1, 1, n, hd)
+    tl.tl_kv_write_int4(t, t, *cache, _dev([0]))
+    k, v = torch.zeros_like(t), torch.zeros_like(t)
+    tl.tl_kv_read_int4(*cache, _dev([0]), k, v)
+    torch.cuda.synchronize()
+    _same(cache, _expect(cache, x[:, None], x[:, None], [(0, p) for p in range(n)]))
+    got, rows = k.cpu().numpy().astype(np.float64), x.astype(np.float64)
+    assert (np.abs(got - rows) <= held_bound(x) + np.abs(got) * 2.0 ** -11 + 2.0 ** -25).all()
+    assert torch.equal(k, v)

@@ -10,8 +10,10 @@
 // function of the row: the standalone writer, the prefill append and the
 // decode append give the same bits.  The scale is rounded towards zero so that
 // no value leaves [lo, hi] (with a scale rounded up, a group that spans the
-// fp16 range would read back as infinity); that costs at most 15 * 2^-10 of a
-// step at the group's upper end.  A zero point of -0 is stored as +0, which
+// fp16 range would read back as infinity).  What that costs at the group's upper
+// end, beyond half a step: at most 15 * 2^-10 of a step; for ranges below 15 * 2^-14,
+// whose scale is subnormal in fp16, less than 15 * 2^-24 in all (many steps of such a
+// group: a range below 15 * 2^-24 has scale 0 and reads back as lo).  A zero point of -0 is stored as +0, which
 // keeps the bits independent of the order of the minimum.  A group holding a
 // NaN or an infinity gets NaN parameters and codes 0: whoever attends it sees
 // NaN, nobody a plausible number.
