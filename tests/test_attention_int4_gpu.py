@@ -416,3 +416,13 @@ def test_windows_out_of_range_are_refused(window):
         tl.tl_attention_int4(q, *cache.t, lens, out, window=window)
     torch.cuda.synchronize()
     assert (out == 5).all()
+
+
+@pytest.mark.parametrize("ctx,lanes,H,group,hd,n_q", [
+    (129, 38, 1, 1, 64, 1), (520, 40, 1, 1, 128, 1), (1024, 74, 1, 1, 64, 1), (1025, 48, 1, 1, 64, 1), (4064, 40, 1, 1, 64, 1),
+    (4095, 75, 1, 1, 64, 1), (4096, 65, 1, 1, 64, 1), (4097, 40, 1, 2, 128, 1), (4100, 75, 1, 1, 64, 1), (8192, 38, 1, 1, 64, 1),
+    (8193, 65, 1, 1, 64, 1), (8300, 22, 4, 1, 64, 2), (8200, 130, 1, 1, 64, 1),
+])
+def test_both_sides_of_the_split(ctx, lanes, H, group, hd, n_q):
+    """Contexts and unit counts around those where the split changes."""
+    test_any_number_of_lanes(ctx, lanes, H, group, hd, n_q)

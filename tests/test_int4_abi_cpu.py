@@ -88,6 +88,18 @@ def test_attention_workspace():
     assert tl.lib.tl_attention_int4_workspace_bytes(ctypes.byref(_cache()), 9, 4, ctypes.byref(ctypes.c_size_t())) == BAD
 
 
+@pytest.mark.parametrize("units,split", [(37, True), (38, True), (64, True), (65, False), (74, False), (75, True),
+                                         (80, True), (128, True), (130, False), (148, False), (149, False)])
+def test_long_contexts_use_every_sm(units, split):
+    """From 38 to 148 lanes and heads one or two CTAs each only where they fill the GPU; else
+    long contexts are split further, through the workspace (up to where four CTAs per SM
+    leave a cluster's worth a unit or less)."""
+    b = ctypes.c_size_t(7)
+    c = _cache(code_stride=1 << 40, param_stride=1 << 40, n_lanes=units, n_heads=1, max_ctx=16384)
+    assert tl.lib.tl_attention_int4_workspace_bytes(ctypes.byref(c), 1, 1, ctypes.byref(b)) == tl.TL_OK
+    assert (b.value > 0) == (split and 592 // units > 8)
+
+
 def test_empty_calls_do_nothing():
     none = _cache(n_lanes=0, k_codes=None, v_codes=None, k_params=None, v_params=None)
     for fn in (tl.lib.tl_kv_write_int4, tl.lib.tl_kv_read_int4):

@@ -728,26 +728,37 @@ size_t a4_smem_bytes(const A4Split& p, int cols) {
 
 // The split of a caller's attention, for n (row, cache head, column tile) units.
 //
-// One CTA of 12 warps per SM leaves a cluster's join out, or needs one of two CTAs only.
-// 16 heads of 128, us with four warps (as many CTAs as are resident) and with 12:  4
-// lanes of 2112 positions 11.5 and 10.2; 8 lanes of 512 positions 7.7 and 6.5, of 2112
-// 16.0 and 13.7, of 4200 26.8 and 23.2; two lanes 8.6 and (three CTAs) 8.3, 16 lanes 25.5
-// and (two rounds of CTAs) 26.2.
+// One CTA of 12 warps per SM leaves a cluster's join out, or needs one of two CTAs only;
+// it takes whole SMs, of which 38 to 60 and 75 to 125 units leave many idle.  Four warps:
+// four CTAs per SM; a cluster of eight for each of 74 units finds no place at once.  Heads of
+// 128, us with 12 warps and with four:
+//   positions  38 units      64         74         75         88         128        148
+//        512   6.5   5.3   6.5  5.6   6.6  6.7   6.2  6.7   6.5  7.0   7.3  8.0   7.5  11.5
+//       1024   7.8   7.0   8.7  8.2   9.0  12.2  8.9  10.1  9.2  10.5  9.5  10.7  9.7  14.3
+//       2112  10.7  10.9  11.2 11.7  11.4  16.2 14.1  12.5 14.4  12.9 15.2  16.7 15.6  22.3
+//       4096  15.3  14.2  16.3 15.5  16.7  20.8 23.4  17.8 23.7  20.5 25.2  25.9 25.8  32.2
+//       8192  25.0  19.3  27.2 26.6  27.2  32.9 42.9  29.9 44.0  33.0 44.9  45.1 46.0  57.4
+//      16384  44.2  29.9  46.1 43.3  46.8  56.4 79.8  51.8 79.8  58.6 82.1  81.4 82.8 103.5
+// (heads of 64 alike).  So 12 warps where seven eighths of the SMs get a CTA; else up to 1024
+// positions where a unit has one CTA, and between 1024 and 4096.
 //
-// Four warps: four CTAs per SM.  More than a cluster's eight cost a second launch and a
-// workspace: one lane of 16 heads takes 12.3 us in a cluster and 10.3 through the
-// workspace at 4096 positions (12.3 and 13.3 with two lanes), 16.4 and 13.2 at 8192.
+// More than a cluster's eight cost a second launch and a workspace: one lane of 16 heads
+// takes 12.3 us in a cluster and 10.3 through the workspace at 4096 positions (12.3 and 13.3
+// with two lanes), 16.4 and 13.2 at 8192.
 A4Split a4_split(int max_ctx, long n) {
   const int tiles = (max_ctx + A4_TILE - 1) / A4_TILE;
-  if (n > 37 && n <= 148 && tiles > A4_GROUP)
-    return {std::min((tiles + A4_WIDE - 1) / A4_WIDE, n <= 74 ? 2 : 1), A4_WIDE, 1, 0};
+  const int wide = std::min((tiles + A4_WIDE - 1) / A4_WIDE, n <= 74 ? 2 : 1);
+  if (n > 37 && n <= 148 && tiles > A4_GROUP &&
+      (8 * n * wide >= 7 * 148 || (tiles <= 32 ? wide == 1 : tiles < 128)))
+    return {wide, A4_WIDE, 1, 0};
   const int c = (int)std::min<long>((tiles + A4_GROUP - 1) / A4_GROUP, std::max(1L, 148 * 4 / n));
   if (max_ctx < kInt4SplitCtx || c <= A4_MAX_CLUSTER) return {std::min(c, A4_MAX_CLUSTER), A4_GROUP, 1, 0};
   return {std::min(c, A4_MAX_SPLIT), A4_GROUP, 1, std::min(c, A4_MAX_SPLIT)};
 }
 
 // The split of a model's attention, whose results must not depend on how many lanes
-// run: the groups of four slots, and the way they are joined, follow from max_ctx.
+// run: the groups of four slots, and the way they are joined, follow from max_ctx.  Where
+// one CTA of 12 warps takes a unit, 75 to 125 units leave SMs idle, as above.
 // Below kInt4SplitCtx six groups, in a CTA each or all in one; from there on 24,
 // through the workspace.
 template <int HD>
