@@ -212,7 +212,9 @@ tl_status tl_kv_read_int4(const tl_kv_int4* cache, uint16_t* k, uint16_t* v, lon
  * NaN included.  Scores, maxima, exponentials and sums in fp32; softmax weights
  * and values enter the products as fp16 (weights to 2^-11 of themselves, or to 2^-32
  * of the largest where that is more); out is rounded to fp16.  A query's
- * result does not depend on the contents of other lanes.
+ * result does not depend on the contents of other lanes, nor on the run; how the
+ * work is split, and with it the last bits, follows from max_ctx, n_lanes, n_heads
+ * and n_q * q_heads / n_heads.
  *   q      device fp16 [n_lanes * n_q][q_stride], row b * n_q + i, head h at
  *          column h * head_dim
  *   lens   device int32 [n_lanes]: positions that hold entries, the queries' own

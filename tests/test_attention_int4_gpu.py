@@ -426,3 +426,21 @@ def test_windows_out_of_range_are_refused(window):
 def test_both_sides_of_the_split(ctx, lanes, H, group, hd, n_q):
     """Contexts and unit counts around those where the split changes."""
     test_any_number_of_lanes(ctx, lanes, H, group, hd, n_q)
+
+
+@pytest.mark.parametrize("lanes,H,group,ctx,same", [
+    (1, 2, 1, 400, True), (2, 2, 2, 2112, True), (20, 2, 4, 2112, False), (6, 8, 2, 9000, False), (2, 1, 4, 9000, False),
+])
+def test_a_query_alone_and_with_others_of_its_lane(lanes, H, group, ctx, same):
+    """The last of eight queries as a call of its own: right in both; the same bits where the
+    number of column tiles leaves the split as it is, else the split may differ."""
+    hd, n_q = 64, 8
+    cache = Cache(*_kv(lanes, H, ctx, hd, 54))
+    q = _q(lanes * n_q, H * group, hd, 55, 2.0)
+    lens = [ctx - 5 * b for b in range(lanes)]
+    many = _run(q, cache, lens, n_q, 0)
+    _check(many, q, cache, lens, n_q, 0)
+    alone = _run(q[n_q - 1::n_q], cache, lens, 1, 0)
+    _check(alone, q[n_q - 1::n_q], cache, lens, 1, 0)
+    if same:
+        assert np.array_equal(alone, many[n_q - 1::n_q])

@@ -27,12 +27,13 @@
 // 41 us, 3.6 TB/s.  Many short lanes are bound by their launch, the merge and the tail.
 //
 // Work split: the context is cut into tiles of 32 keys; tile i belongs to slot i mod
-// slots, whatever the lane's length, so the work is even for every length and the
-// other queries of a launch do not change a query's arithmetic.  A warp takes a slot,
+// slots, whatever the lane's length, so the work is even for every length.  For a
+// given split the other queries of a launch do not change a query's arithmetic; a
+// caller's split follows from max_ctx and the number of lanes, heads and column tiles
+// (eight queries x query heads each), a model's from max_ctx alone.  A warp takes a slot,
 // or some in turn, and keeps a running reference and sum per query (base 2); the reference
 // is raised only when a weight would pass 2^15 (A4_SLACK), which spares the cross-lane
-// maximum on most tiles.  The slots'
-// records are joined in a fixed order through shared memory, the CTAs of a cluster
+// maximum on most tiles.  The slots' records are joined in a fixed order through shared memory, the CTAs of a cluster
 // through distributed shared memory, every CTA finishing its share of the outputs: one
 // launch, no workspace.  The longest contexts are split over more CTAs, whose records
 // a second launch joins.  The bits are the same at every run.
