@@ -339,7 +339,10 @@ tl_status tl_model_set_graphs(tl_model* model, int enable);
  * CTA streams `chunks_per_cta` consecutive chunks.  0 (the default) picks, per
  * call, the fewest chunks per CTA that run all (row, head) pairs in the fewest
  * waves on this GPU.  The result is bit-identical for every value: this is a
- * tuning and testing knob.  Frees the model's captured graphs.
+ * tuning and testing knob.  A TL_KV_INT4 cache has no such chunks and takes no
+ * notice of the value: its attention splits the context into six parts (24 from
+ * 8192 positions on), equally independent of the lanes that run.  Frees the
+ * model's captured graphs.
  * Errors: TL_ERR_INVALID_ARG for a NULL model or a value outside [0, 8]. */
 tl_status tl_model_set_decode_chunks(tl_model* model, int chunks_per_cta);
 

@@ -282,3 +282,21 @@ def test_a_run_of_them_together():
     assert torch.equal(a["ids"][:, 0], m.greedy_head(ys["fp16"]))
     kv.close()
     m.close()
+
+
+def test_the_chunk_knob_leaves_a_4bit_cache_alone():
+    """tl_model_set_decode_chunks sets how other caches are streamed; no value of it changes a
+    4-bit cache's results."""
+    m = device_model("tiny", max_tokens=64, max_lanes=1, max_ctx=128)
+    x = to_dev(syn.hidden_input(syn.WORKLOADS["tiny"], 41, name="int4.knob"), torch.float16)
+    outs = []
+    for chunks in (0, 1, 3, 8):
+        m.set_decode_chunks(chunks)
+        kv = m.new_kv([2], max_ctx=100, dtype="int4")
+        m.prefill(h_in=x[:40], L=2, kv=kv, lane=0)
+        outs.append(m.decode(kv, h_in=x[40:], L_per_lane=[2]).cpu())
+        assert m.sync_status() == tl.TL_OK
+        kv.close()
+    for y in outs[1:]:
+        assert torch.equal(y, outs[0])
+    m.close()

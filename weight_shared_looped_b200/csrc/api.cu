@@ -791,8 +791,8 @@ size_t h_workspace_bytes(const tl_model* m, int n_lanes, int max_ctx, size_t* la
   return *part_off + align256(part * 2 * m->d * sizeof(float));
 }
 
-// 4-bit caches: the attention's workspace for up to 8 rows (decode) or 8 queries of a
-// row (extend).
+// 4-bit caches: the attention's workspace for up to 8 rows of one query (decode), which
+// covers a row of up to 8 queries (extend): they fill the one column tile of each head.
 size_t int4_workspace_bytes(const tl_model* m, int max_ctx) {
   AttnInt4Args a;
   memset(&a, 0, sizeof(a));

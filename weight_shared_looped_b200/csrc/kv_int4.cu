@@ -14,7 +14,8 @@
 // token; read back, the reverse.  16384 tokens of 16 heads of 128 (176 MB each way)
 // are written in 42 us, 4.2 TB/s (bound by issue slots: about 140 instructions per
 // eight values, for the group's extremes and parameters and the rounding of each
-// code), and read back in 31 us, 5.7 TB/s.  One token per lane takes 2 us, a launch.
+// code), and read back in 31 us, 5.7 TB/s.  One token per lane is a launch: 2 us
+// in a row of them, 6.4 us for a write and a read-back of buffers that left the caches.
 #include "kv_int4.cuh"
 #include "tl_launch.cuh"
 
