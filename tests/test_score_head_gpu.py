@@ -467,3 +467,55 @@ def test_a_models_scores_with_a_workspace():
     for key, w in zip(("logp", "entropy", "ids", "top"), want):
         assert np.array_equal(got[key].cpu().numpy(), w, equal_nan=True)
     assert np.isnan(want[0][2])
+
+
+@pytest.mark.parametrize("n,k", [(5, 1), (56, 16), (57, 1), (130, 6), (200, 16)])
+@pytest.mark.parametrize("order", ["rising", "falling", "equal"])
+def test_every_logit_a_new_best(n, k, order):
+    """Logits in the order of the ids, one by one better than all before, worse, or equal:
+    candidates at every place, and at none but the first."""
+    V, d = 20000, 64
+    E = np.zeros((V, d), np.float16)
+    E[:, 5] = (np.arange(V, dtype=np.uint16) + 0x0400).view(np.float16)     # neighbours, up to 30
+    if order == "falling":
+        E[:, 5] = E[::-1, 5].copy()
+    elif order == "equal":
+        E[:, 5] = 1.5
+    y = np.zeros((n, d), np.float32)
+    y[:, 5] = np.linspace(0.5, 1.0, n)
+    lp, h, ids, top = _run(E, y, np.arange(n) * 7, k)
+    want = np.arange(V)[::-1][:k] if order == "rising" else np.arange(k)
+    assert (ids == want).all()
+    z = np.float64(y[:, 5:6]) * E[:, 5].astype(np.float64)
+    lse = np.log(np.exp(z - z.max(1, keepdims=True)).sum(1)) + z.max(1)
+    tol = z.max() * 2.0 ** -21 + 2.0 ** -20
+    assert np.abs(top - (z[:, want] - lse[:, None])).max() <= tol + 2.0 ** -24 * 40
+    assert np.abs(lp - (z[np.arange(n), np.arange(n) * 7] - lse)).max() <= tol + 2.0 ** -24 * 40
+
+
+@pytest.mark.parametrize("n,V,d,k", [(56, 333, 64, 3), (57, 333, 64, 3), (130, 2100, 64, 0), (260, 90, 128, 10), (64, 16, 64, 16),
+                                     (500, 33, 192, 1), (4737, 65, 64, 2)])
+def test_short_rows_and_small_vocabularies(n, V, d, k):
+    test_matches_fp64(n, V, d, k)
+
+
+def test_the_first_call_of_a_process_in_a_capture():
+    """Kernel attributes are set, and the kernels loaded, within a capture too."""
+    import subprocess
+    import sys
+    code = """
+import torch, weight_shared_looped_b200 as tl
+for n in (3, 200):
+    E, y = torch.ones(500, 64, dtype=torch.float16, device="cuda"), torch.ones(n, 64, device="cuda")
+    h = torch.zeros(n, device="cuda")
+    ws = torch.empty(tl.tl_score_head_workspace_bytes(n, 500, 64, 0), dtype=torch.uint8, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        tl.tl_score_head(E, y, None, None, h, None, None, ws)
+    g.replay()
+    assert tl.tl_score_head_status(ws) == tl.TL_OK
+    assert (h - torch.log(torch.tensor(500.0))).abs().max() < 1e-5
+print("fine")
+"""
+    out = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=120)
+    assert out.returncode == 0 and "fine" in out.stdout, out.stderr[-2000:]

@@ -400,7 +400,8 @@ def tl_attention_int4(q, k_codes, k_params, v_codes, v_params, lens, out, n_q: i
         _fail(f"{what}: lens is not a contiguous [{lanes}]")
     if rows <= 1:
         qs = os_ = width
-    _ints(what, window=window)
+    if not -(1 << 31) <= window < 1 << 31:
+        _ints(what, window=window)
     ws, ws_bytes = None, 0
     if d.max_ctx >= _INT4_SPLIT_CTX and rows:
         if workspace is None:
