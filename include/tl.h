@@ -546,7 +546,10 @@ tl_status tl_greedy_head(tl_model* model, const float* y, int n, int32_t* ids,
  * off by at most (2^-22 + 2^-17 + d 2^-33) sum_i |y_i E_i[v]|; towards zero by half
  * of the 2^-17 where it comes from few early elements, by less elsewhere.  The
  * given token's logit, the order of the best and the largest terms of the sum are
- * decided by fp64 dot products of the inputs.  A row with a logit that is not
+ * decided by fp64 dot products of the inputs: of the k + 2 largest by those sums, so
+ * where three tokens or more lie within that error of the k-th, another of them may
+ * stand in its place (with its own log probability).  Tokens of equal embedding rows
+ * have equal sums and keep their order.  A row with a logit that is not
  * finite gets NaN and ids of -1.  So does every row of a call one of whose device
  * waits ran out (2 s; it does not happen to a GPU that works): tl_score_head_status
  * tells the two apart.

@@ -519,3 +519,24 @@ print("fine")
 """
     out = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=120)
     assert out.returncode == 0 and "fine" in out.stdout, out.stderr[-2000:]
+
+
+@pytest.mark.parametrize("n,k", [(9, 5), (130, 5), (500, 12)])
+def test_nearly_equal_best_tokens(n, k):
+    """Two hundred tokens a rounding of pass 1 apart: whichever are returned, each has its own
+    log probability, in order, and none is further below the true one than the sums' error."""
+    V, d = 3000, 512
+    E, y, t = _inputs(n, V, d, 140)
+    base = E[7].astype(np.float32)
+    E[1000:1200] = base.astype(np.float16)
+    E[np.arange(1000, 1200), np.arange(200)] = np.nextafter(E[7, :200], np.float16(np.inf))
+    y = (y * 0.01 + 40 * base / np.linalg.norm(base)).astype(np.float32)
+    _, _, ids, top = _run(E, y, t, k)
+    z = y.astype(np.float64) @ E.astype(np.float64).T
+    want = -np.sort(-z, 1)[:, :k]
+    A = (np.abs(y).astype(np.float64) @ np.abs(E).astype(np.float64).T).max(1)[:, None]
+    got = np.take_along_axis(z, ids, 1)
+    assert (np.diff(got, axis=1) <= 0).all() and all(len(set(r)) == k for r in ids.tolist())
+    assert (got >= want - 2 * _chunk_eps(A, d)).all()
+    lse = np.log(np.exp(z - z.max(1, keepdims=True)).sum(1, keepdims=True)) + z.max(1, keepdims=True)
+    assert (np.abs(top - (got - lse)) <= _chunk_eps(A, d) + 2.0 ** -20 + 2.0 ** -24 * np.abs(top)).all()

@@ -24,12 +24,11 @@
 // Pass 1 streams the embedding through tcgen05 and keeps, per row and slice of
 // the vocabulary, the running maximum m, l = sum e^(z - m), s = sum e^(z - m) (z - m)
 // and the best candidates.
-// Pass 2, a CTA per row (a warp per row where there are many), merges the slices and decides the order of the best
-// k + kSpare candidates, and the given token's logit, by fp64 dot products of the
-// inputs, so the ranking does not depend on pass 1's rounding (ties go to the
-// lowest token id; equal embedding rows tie in pass 1 already, and for another
-// token to be missed, three logits would have to lie within pass 1's error of the
-// k-th).
+// Pass 2, a CTA per row (a warp per row where there are many), merges the slices and
+// decides the order of the best k + kSpare candidates, and the given token's logit, by
+// fp64 dot products of the inputs (ties go to the lowest token id; equal embedding rows
+// tie in pass 1 already, and for another token to be missed, three logits have to lie
+// within pass 1's error of the k-th: it is then as good to that error).
 //
 // Bounds (vocabulary 50257, d 2048): few rows by the embedding's 206 MB, 31 us; one row
 // with k 5 takes 46 us (passes 0 and 2 and the fill and tail of pass 1 are 12 of
