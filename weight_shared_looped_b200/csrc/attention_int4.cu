@@ -154,17 +154,11 @@ __device__ __forceinline__ void a4_copy4(uint32_t* dst, const uint32_t* src) {
                : "memory");
 }
 
-// Positions of the row's lane that hold entries, its queries' own included.
-__device__ __forceinline__ int a4_len(const AttnInt4Args& a, int row) {
-  const int len = a.hdr != nullptr ? a.hdr->pos[a.row_lane[row]] + a.n_q : a.lens[row];
-  return max(0, min(len, a.max_ctx));
-}
-
 // A query's output from its weighted sum and the sum of its weights.  One that sees no key
 // gets zeros; where all of its scores are -inf (an infinite query) there is no distribution:
-// 0 / 0, NaN.
+// NaN.
 __device__ __forceinline__ __half a4_output(float acc, float L, bool sees) {
-  return __float2half_rn(sees ? acc / L : 0.f);
+  return __float2half_rn(L == 0.f ? (sees ? CUDART_NAN_F : 0.f) : acc / L);
 }
 
 template <int HD, int WARPS, bool FUSED>
@@ -184,19 +178,23 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == A4_WIDE ? 1 : 4) attn_int
 
   // the lane's cache and length
   const uint32_t *kc, *vc, *kp, *vp;
+  int len;
   if (a.hdr != nullptr) {
+    const int ln = a.row_lane[row];
     const char* base = a.kv_base + (size_t)(a.row_cum[row] + a.layer) * a.layer_bytes;
     kc = reinterpret_cast<const uint32_t*>(base);
     vc = reinterpret_cast<const uint32_t*>(base + a.region_bytes);
     kp = reinterpret_cast<const uint32_t*>(base + 2 * a.region_bytes);
     vp = reinterpret_cast<const uint32_t*>(base + a.region_bytes + a.layer_bytes / 2);
+    len = a.hdr->pos[ln] + a.n_q;
   } else {
     kc = a.k_codes + (size_t)row * a.code_stride;
     vc = a.v_codes + (size_t)row * a.code_stride;
     kp = a.k_params + (size_t)row * a.param_stride;
     vp = a.v_params + (size_t)row * a.param_stride;
+    len = a.lens[row];
   }
-  const int len = a4_len(a, row);
+  len = max(0, min(len, a.max_ctx));
   kc += (size_t)head * a.max_ctx * C::RW;
   vc += (size_t)head * a.max_ctx * C::RW;
   kp += (size_t)head * a.max_ctx * C::RP;
@@ -563,7 +561,7 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS == A4_WIDE ? 1 : 4) attn_int
   };
   auto to_output = [&](int i, float acc, float L) {
     const int cc = c0 + i / HD, qi = cc / a.group, hq = head * a.group + cc % a.group;
-    a.out[(size_t)(row * a.n_q + qi) * a.out_stride + (size_t)hq * HD + i % HD] = a4_output(acc, L, last_of(cc) >= 0);
+    a.out[(size_t)(row * a.n_q + qi) * a.out_stride + (size_t)hq * HD + i % HD] = a4_output(acc, L, FUSED || last_of(cc) >= 0);
   };
   // a split beyond a cluster: record `all` of `of` goes to the merge kernel
   auto to_workspace = [&](int all, int of, int i, float M, float acc, float L) {
@@ -678,6 +676,12 @@ __global__ void __launch_bounds__(2 * HD) attn_int4_merge_kernel(AttnInt4Args a,
 #pragma unroll
   for (int s = 0; s < HALF; ++s)
     v[s] = 2 * s + h < splits ? rec[(size_t)(2 * s + h) * REC + c * HD + d] : 0.f;
+  // a model's decode step sees its own entry at least
+  bool sees = true;
+  if (a.qkv == nullptr) {
+    const int len = a.hdr != nullptr ? a.hdr->pos[a.row_lane[row]] + a.n_q : a.lens[row];
+    sees = max(0, min(len, a.max_ctx)) - a.n_q + cc / a.group >= 0;
+  }
   if (threadIdx.x < 32) {
     float m[2], l[2], M = A4_NONE, L = 0.f;
 #pragma unroll
@@ -709,7 +713,7 @@ __global__ void __launch_bounds__(2 * HD) attn_int4_merge_kernel(AttnInt4Args a,
   if (h == 0) {
     const float L = sum;
     a.out[(size_t)(row * a.n_q + cc / a.group) * a.out_stride + (size_t)(head * a.group + cc % a.group) * HD + d] =
-        a4_output(acc + part[d], L, a4_len(a, row) - a.n_q + cc / a.group >= 0);
+        a4_output(acc + part[d], L, sees);
   }
 }
 
