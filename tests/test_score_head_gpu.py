@@ -440,18 +440,18 @@ def test_a_wait_that_runs_out(n, V, d, copies):
     h, ids = torch.zeros(n, device="cuda"), torch.zeros(n, k, dtype=torch.int32, device="cuda")
     top = torch.zeros(n, k, device="cuda")
 
-    def hook(copies):
-        rc = tl.lib.tl_check_score_wait(tE.data_ptr(), V, d, ty.data_ptr(), n, copies, 2000, h.data_ptr(), k, ids.data_ptr(),
+    def hook(copies, limit_us):
+        rc = tl.lib.tl_check_score_wait(tE.data_ptr(), V, d, ty.data_ptr(), n, copies, limit_us, h.data_ptr(), k, ids.data_ptr(),
                                         top.data_ptr(), ws.data_ptr(), ws.numel(), None)
         assert rc == tl.TL_OK
-    hook(copies)
+    hook(copies, 2000)
     assert tl.tl_score_head_status(ws) == tl.TL_ERR_TIMEOUT
     assert h.isnan().all() and top.isnan().all() and (ids == -1).all()
     tl.tl_score_head(tE, ty, torch.from_numpy(t).cuda(), top[:, 0].contiguous(), h, ids, top, ws)
     assert tl.tl_score_head_status(ws) == tl.TL_OK
     for got, w in zip((h, ids, top), want[1:]):
         assert np.array_equal(got.cpu().numpy(), w)
-    hook(2 ** 31 - 1)
+    hook(2 ** 31 - 1, 2000000)
     assert tl.tl_score_head_status(ws) == tl.TL_OK and np.array_equal(h.cpu().numpy(), want[1])
 
 
